@@ -17,7 +17,8 @@
  *    block) and of 32 for the quantizer (one pad40 chunk).
  *  - Return value: QIG_OK, or a negative QIG_E* code; nothing is enqueued
  *    when an argument check fails.  qig_strerror() names a code.
- *  - Outputs never alias inputs.  NaN/Inf inputs give unspecified output.
+ *  - Outputs never alias inputs.  NaN/Inf inputs give unspecified output
+ *    (the int8 and experts' calls state what they give).
  *  - Calls on one stream run in order; calls on different streams that write
  *    the same buffer race.
  */
@@ -359,6 +360,153 @@ int mmq_q4k_xf32(const void *W, int64_t od, int64_t id, const float *x,
 int mmq_q4k_q8t_noalloc(const void *W, int64_t od, int64_t id,
                         const void *q8t, int64_t nt, float *y, int64_t ldy,
                         hipStream_t stream);
+
+/*
+ * The int8 linear layer and the experts' layer: weights in 8-bit integers
+ * with one scale per output channel, activations in 8-bit integers with one
+ * scale per row, next to the k-quant products above.
+ *
+ * Element types of the fp32 or 16-bit operands:
+ */
+#define QIG_F32 0
+#define QIG_BF16 1
+#define QIG_F16 2
+
+/*
+ * quantize_i8 -- rows to int8 with one fp32 scale a row: activations per
+ * token before a product, or weight rows once per matrix.
+ *   s = max|x| / 127 over the row, rounded to fp32;
+ *   q = the integer nearest x / s (of the stored s), ties away from zero,
+ *       clamped to [-127, 127]; all 0 where s = 0.
+ * Which integer is nearest is decided exactly.  A row that holds a NaN or an
+ * infinity gets s = NaN and q = 0, so that products with it are NaN.
+ *
+ *   x      [nt][ldx] elements of xtype, ldx >= id, aligned to an element
+ *   q      [nt][ldq] int8, ldq >= id; only the id bytes of each row are
+ *          written.  (The products below need ldq % 16 == 0 and q 16-byte
+ *          aligned.)
+ *   s      [nt] fp32
+ * Errors: QIG_EINVAL (unknown type, nt < 0 or >= 2^31, id <= 0 or >= 2^31,
+ *         ldx < id, ldq < id), QIG_EALIGN, QIG_ELAUNCH.
+ */
+int quantize_i8(const void *x, int xtype, int64_t nt, int64_t id, int64_t ldx,
+                int8_t *q, int64_t ldq, float *s, hipStream_t stream);
+
+/*
+ * mm_i8 -- the product of int8 rows and int8 weights:
+ *   P[t][j] = sum over k < id of q[t][k] * W[j][k]   (int32, exact),
+ *   v[t][j] = P * sq[t] * sw[j] + bias[j]            (fp32),
+ *   y[t][j] = v[t][j], or with glu = 1, where W, sw and bias have 2 * od rows
+ *             (first the gate rows, then the up rows),
+ *             a * sigmoid(a) * b, a = v[t][j], b = v[t][od + j],
+ * rounded once to ytype.  id need not be a multiple of anything; bytes of a
+ * row past id are read up to the next multiple of 16 and have no effect.
+ *
+ *   W      [od or 2 od][ldw] int8, ldw >= id, ldw % 16 == 0, 16-byte aligned;
+ *          any byte values, -128 included
+ *   sw     [od or 2 od] fp32;  bias the same, or NULL
+ *   q, sq  as written by quantize_i8, ldq % 16 == 0, q 16-byte aligned
+ *   y      [nt][ldy] elements of ytype, ldy >= od, aligned to an element;
+ *          overwritten
+ *   ws     NULL, or a workspace as for the stream-K calls (the same rules:
+ *          zero-filled once, not shared by calls that may run at the same
+ *          time, two replayed graphs among them): lets a product with few
+ *          output tiles split the sums over id.  The sums are integers, so y
+ *          is bit-identical with and without ws.
+ * Errors: QIG_EINVAL (nt or od < 0 or >= 2^31 (od: 2^30), id <= 0 or > 131071
+ *         (beyond which an int32 sum could overflow), ldw or ldq < id or >
+ *         8388352, ldy < od, unknown ytype, glu not 0 or 1), QIG_EALIGN,
+ *         QIG_ELAUNCH.
+ */
+int mm_i8(const int8_t *W, int64_t ldw, const float *sw, int64_t od,
+          int64_t id, const int8_t *q, int64_t ldq, const float *sq,
+          int64_t nt, const float *bias, int glu, void *y, int ytype,
+          int64_t ldy, void *ws, hipStream_t stream);
+
+/*
+ * route_experts -- for each token the k experts it goes to, and their
+ * weights, from the router's logits.
+ *   p = softmax(l) over the row (QIG_SOFTMAX) or sigmoid(l) (QIG_SIGMOID);
+ *   c = p + bias                 (bias: a balance term, used for the choice
+ *                                 alone; NULL: 0)
+ *   groups > 1: the experts form `groups` runs of ne / groups; a run's score
+ *   is the sum of its group_top (1 or 2) largest c, and only the topk_groups
+ *   best runs stay;
+ *   ids = the k experts with the largest c, largest first;
+ *   w = p of those experts, divided by their sum if renorm, times scale.
+ * Equal values go to the lower index.  p and c are formed and compared in 64
+ * bits (softmax without a bias: the logits themselves are compared), w is
+ * rounded once.  A logit of -infinity or NaN is an expert that may not be
+ * chosen (+infinity counts as the largest fp32 number): where fewer than k
+ * can be chosen the remaining ids are -1 with weight 0.  renorm over a sum of
+ * 0 gives weights 0.
+ *
+ *   logits [nt][ldl] elements of ltype, ldl >= ne
+ *   bias   [ne] fp32 or NULL; an expert whose c is NaN is not chosen
+ *   ids    [nt][k] int32;  w [nt][k] fp32; both contiguous
+ * Errors: QIG_EINVAL (unknown type or score, nt < 0 or >= 2^31, ne < 1 or >
+ *         512, ldl < ne, groups < 1 or > 64 or not a divisor of ne,
+ *         topk_groups < 1 or > groups, group_top not 1 or 2, k < 1 or > 32 or
+ *         more than the experts of topk_groups groups), QIG_EALIGN,
+ *         QIG_ELAUNCH.
+ */
+#define QIG_SOFTMAX 0
+#define QIG_SIGMOID 1
+int route_experts(const void *logits, int ltype, int64_t nt, int64_t ne,
+                  int64_t ldl, const float *bias, int score, int64_t groups,
+                  int64_t topk_groups, int64_t group_top, int64_t k,
+                  int renorm, float scale, int32_t *ids, float *w,
+                  hipStream_t stream);
+
+/*
+ * plan_experts -- the order of rows by expert that mm_i8_experts works in,
+ * built on the GPU from the routing's ids (no host round trip).  A row is one
+ * (token, slot) pair, row = token * k + slot.  The plan is int32 words:
+ *   [0 .. ne]    first position of each expert's rows in the order; [ne] is
+ *                the number of rows with an expert
+ *   [ne + 1]     nrows
+ *   [ne + 2 ..]  the order: rows sorted by expert, by row within an expert
+ *                (the same on every call); rows whose id lies outside
+ *                [0, ne), such as the -1 of an unfilled slot, last
+ * expert_plan_bytes returns 0 for invalid arguments (nrows < 0 or >= 2^29,
+ * ne < 1 or > 512).
+ *   ids    [nrows] int32;  plan expert_plan_bytes(nrows, ne) bytes, 4-byte
+ *          aligned, every byte written
+ * Errors: QIG_EINVAL, QIG_EALIGN, QIG_ELAUNCH.
+ */
+size_t expert_plan_bytes(int64_t nrows, int64_t ne);
+int plan_experts(const int32_t *ids, int64_t nrows, int64_t ne, void *plan,
+                 hipStream_t stream);
+
+/*
+ * mm_i8_experts -- every row's product with its expert's weights: y[r] is
+ * mm_i8's y for row r / slots of q and the weights of row r's expert.  Rows
+ * without an expert get zeros.
+ *   W      [ne][od or 2 od][ldw] int8; sw and bias [ne][od or 2 od]
+ *   q, sq  nrows / slots rows: slots = k where the k rows of a token share
+ *          its activations (gate and up), 1 where each row has its own (down)
+ *   plan   made by plan_experts for the same nrows and ne
+ *   y      [nrows][ldy], in the order of the rows, not of the plan
+ * Other arguments and errors as mm_i8; also QIG_EINVAL for nrows >= 2^29, ne
+ * < 1 or > 512, slots < 1 or not a divisor of nrows.
+ */
+int mm_i8_experts(const int8_t *W, int64_t ldw, const float *sw, int64_t ne,
+                  int64_t od, int64_t id, const int8_t *q, int64_t ldq,
+                  const float *sq, int64_t nrows, int64_t slots,
+                  const void *plan, const float *bias, int glu, void *y,
+                  int ytype, int64_t ldy, hipStream_t stream);
+
+/*
+ * combine_experts -- y[t] = sum over s < k of w[t][s] * h[t * k + s], in fp32
+ * in the order of s, rounded once to ytype.
+ *   h      [nt * k][ldh] elements of htype, ldh >= od;  w [nt][k] fp32
+ *   y      [nt][ldy] elements of ytype, ldy >= od
+ * Errors: QIG_EINVAL (unknown type, nt or od < 0, k < 1, nt * k >= 2^31, ldh
+ *         or ldy < od), QIG_EALIGN, QIG_ELAUNCH.
+ */
+int combine_experts(const void *h, int htype, int64_t ldh, const float *w,
+                    int64_t nt, int64_t k, int64_t od, void *y, int ytype,
+                    int64_t ldy, hipStream_t stream);
 
 /*
  * Test exports: the int32 sub-block partials of the same kernels, for the

@@ -17,6 +17,7 @@ _lib = None
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
+_int = ctypes.c_int
 
 # name -> (restype, argtypes), mirroring include/qig.h
 SIGNATURES = {
@@ -54,6 +55,15 @@ SIGNATURES = {
     "q6k_limbs_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "prepare_q6k_limbs": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp]),
     "mmq_q6k_limbs_q8t": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "quantize_i8": (ctypes.c_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mm_i8": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _int, _vp, _int, _i64, _vp, _vp]),
+    "route_experts": (ctypes.c_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _i64, _i64, _i64, _int,
+                                     ctypes.c_float, _vp, _vp, _vp]),
+    "expert_plan_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "plan_experts": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp]),
+    "mm_i8_experts": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _int,
+                                     _vp, _int, _i64, _vp]),
+    "combine_experts": (ctypes.c_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _vp, _int, _i64, _vp]),
 }
 
 

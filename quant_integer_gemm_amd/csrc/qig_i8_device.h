@@ -1,0 +1,68 @@
+// qig_i8_device.h -- element types of the int8 linear layer's inputs and
+// outputs on the device.
+#pragma once
+#include "qig_device.h"
+#include "qig_i8.h"
+
+namespace qig {
+
+template <int T> struct Elem;
+template <> struct Elem<T_F32> { typedef float type; };
+template <> struct Elem<T_BF16> { typedef __bf16 type; };
+template <> struct Elem<T_F16> { typedef _Float16 type; };
+template <int T> using elem_t = typename Elem<T>::type;
+
+// 16 bytes of elements as fp32 (4 of fp32, 8 of the 16-bit types).
+template <int T> constexpr int VEC = T == T_F32 ? 4 : 8;
+
+template <int T>
+__device__ __forceinline__ void unpack16(u32x4 v, float (&o)[VEC<T>])
+{
+    if constexpr (T == T_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_bit_cast(float, (uint32_t)v[i]);
+    } else if constexpr (T == T_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = v[i];
+            o[2 * i] = __builtin_bit_cast(float, w << 16);
+            o[2 * i + 1] = __builtin_bit_cast(float, w & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = v[i];
+            o[2 * i] = h2f(w);
+            o[2 * i + 1] = h2f(w >> 16);
+        }
+    }
+}
+
+// fp32 to 16 bytes of elements, each rounded once (to nearest even).
+template <int T>
+__device__ __forceinline__ u32x4 pack16(const float (&f)[VEC<T>])
+{
+    u32x4 v;
+    if constexpr (T == T_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(uint32_t, f[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const elem_t<T> a = (elem_t<T>)f[2 * i], b = (elem_t<T>)f[2 * i + 1];
+            v[i] = (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
+        }
+    }
+    return v;
+}
+
+// a * sigmoid(a) * b in fp32 from the hardware's exp2 and reciprocal (each
+// within about an ulp): for a far below zero exp2 overflows and the
+// reciprocal of infinity gives the limit 0.
+__device__ __forceinline__ float silu_mul(float a, float b)
+{
+    const float e = __builtin_amdgcn_exp2f(a * -1.4426950408889634f);
+    return a * __builtin_amdgcn_rcpf(1.0f + e) * b;
+}
+
+}  // namespace qig
