@@ -21,6 +21,9 @@
 #include "qig_i8_device.h"
 #include "qig_launch.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace qig {
 
 constexpr int BK = 128;
@@ -30,8 +33,10 @@ struct I8Args {
     const float *sw, *sq, *bias;
     void *y;
     const int32_t *plan;
+    int32_t *part;    // split sums: one BM x BN slot of int32 a workgroup
+    uint32_t *cnt;    // and one arrival counter a tile
     int64_t ldw, ldq, ldy, od, nt;
-    int id, nbt, nbj, ne, slots;
+    int id, nbt, nbj, ne, slots, splits;
 };
 
 __device__ __forceinline__ uint64_t uniform64(const void *p)
@@ -65,6 +70,22 @@ __device__ __forceinline__ void copy16_at(uint64_t addr, uint32_t lds)
                  :
                  : "v"(addr), "{m0}"(m0v)
                  : "memory");
+}
+
+// Workgroup -> tile.  Workgroups go round-robin over the eight XCDs, each with
+// its own L2: XCD x takes a contiguous run of the tile order, and the order
+// walks bands of BAND token tiles, band rows fastest, so that the tiles an XCD
+// works on at one time share both weight rows and tokens.
+constexpr unsigned BAND = 8;
+__device__ __forceinline__ void tile_of(unsigned b, int nbt, int nbj, int &mt, int &jt)
+{
+    const unsigned total = (unsigned)nbt * (unsigned)nbj, per = total / 8, rem = total % 8, x = b % 8;
+    const unsigned i = x * per + (x < rem ? x : rem) + b / 8;
+    const unsigned band = BAND * (unsigned)nbj;
+    const unsigned bi = i / band, in = i - bi * band;
+    const unsigned left = (unsigned)nbt - bi * BAND, h = left < BAND ? left : BAND;
+    jt = (int)(in / h);
+    mt = (int)(bi * BAND + in % h);
 }
 
 // Which expert and rows a workgroup's token tile covers: tile number mt
@@ -113,7 +134,7 @@ __device__ __forceinline__ Rows find_rows(const int32_t *plan, int ne, int mt)
 // GLU: of every 64 of the tile's weight rows the first 32 are gate rows and
 // the last 32 the up rows of the same outputs, so a wave holds both halves of
 // an output in the same lane and register.
-template <int BM, int BN, int WM, int WN, bool GLU, bool EXPERTS, int YT>
+template <int BM, int BN, int WM, int WN, int S, bool SPLIT, bool GLU, bool EXPERTS, int YT>
 __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 {
     constexpr int NW = WM * WN;
@@ -122,14 +143,21 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     constexpr int STAGE = (BM + BN) * BK;
     constexpr int BJ = GLU ? BN / 2 : BN;               // outputs of a tile
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TM >= 1 && TN >= 1, "tile");
+    static_assert(S == 2 || S >= 4, "stages");
     static_assert(!GLU || TN % 2 == 0, "gate and up rows of an output in one wave");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S * STAGE];
     __shared__ float s_sq[BM];
     __shared__ int32_t s_row[EXPERTS ? BM : 1];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int jt = (int)(blockIdx.x % (unsigned)g.nbj), mt = (int)(blockIdx.x / (unsigned)g.nbj);
+    int jt, mt, split = 0;
+    unsigned block = blockIdx.x;
+    if constexpr (SPLIT) {
+        split = (int)(block % (unsigned)g.splits);
+        block /= (unsigned)g.splits;
+    }
+    tile_of(block, g.nbt, g.nbj, mt, jt);
     const int64_t j0 = (int64_t)jt * BJ;
     const uint8_t *W = g.W;
     const float *sw = g.sw, *bias = g.bias;
@@ -196,25 +224,58 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     const uint64_t abase0 = EXPERTS ? 0 : uniform64(g.q + t0 * g.ldq);
     const uint32_t l0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
 
-    const int nk = (g.id + BK - 1) / BK;
-    const int tail = g.id - (nk - 1) * BK;   // bytes of the last step, 1 .. 128
+    int nk = (g.id + BK - 1) / BK;
+    int tail = g.id - (nk - 1) * BK;   // bytes of the last step, 1 .. 128
+    int kfirst = 0;
+    if constexpr (SPLIT) {
+        // this workgroup's share of the steps (at least one)
+        const int all = nk;
+        kfirst = (int)((int64_t)all * split / g.splits);
+        nk = (int)((int64_t)all * (split + 1) / g.splits) - kfirst;
+        if (kfirst + nk < all) tail = BK;
+    }
 
-    auto issue = [&](int kt) {
-        const uint32_t dst = l0 + (kt & 1) * STAGE;
-        const uint64_t k0 = (uint64_t)kt * BK;
+    // The stage that holds step kt.
+    auto buffer = [&](int kt) -> uint32_t {
+        if constexpr ((S & (S - 1)) == 0)
+            return (uint32_t)kt & (S - 1);
+        else
+            return (uint32_t)kt % S;
+    };
+    // Copy piece p of step kt: first the wave's PA pieces of the activations,
+    // then its PB pieces of the weights.
+    auto copy = [&](int kt, int p) {
+        const uint32_t dst = l0 + buffer(kt) * STAGE;
+        const uint64_t k0 = (uint64_t)(kfirst + kt) * BK;
         uint32_t go = 16 * gran;
         if (kt == nk - 1 && (int)go >= tail) go = 0;
-#pragma unroll
-        for (int p = 0; p < PA; ++p) {
+        if (p < PA) {
             const uint32_t d = dst + 1024 * (PA * wave + p);
             if constexpr (EXPERTS)
                 copy16_at(aptr[p] + k0 + go, d);
             else
                 copy16(abase0 + k0, aoff[p] + go, d);
-        }
-#pragma unroll
-        for (int p = 0; p < PB; ++p)
+        } else {
+            p -= PA;
             copy16(bbase + k0 + (bup[p] ? uphalf : 0), boff[p] + go, dst + BM * BK + 1024 * (PB * wave + p));
+        }
+    };
+    // Step kt's bytes past id become zero in the activations' rows.
+    auto clear_tail = [&](uint8_t *st) {
+        for (int i = tid; i < BM * 8; i += NW * 64) {
+            const int r = i >> 3, slot = i & 7;
+            const int left = tail - 16 * (slot ^ (r & 7));   // valid bytes of the granule
+            if (left >= 16) continue;
+            u32x4 *p = reinterpret_cast<u32x4 *>(st + 16 * i);
+            u32x4 v = *p;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int b = left - 4 * w;
+                v[w] = b >= 4 ? v[w] : (b <= 0 ? 0u : v[w] & ((1u << (8 * b)) - 1u));
+            }
+            *p = v;
+        }
+        __syncthreads();
     };
 
     const int wm = wave / WN, wn = wave % WN;
@@ -227,48 +288,199 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[m][n][i] = 0;
 
-    issue(0);
-    for (int kt = 0; kt < nk; ++kt) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        uint8_t *st = lds + (kt & 1) * STAGE;
-        if (kt + 1 < nk) {
-            issue(kt + 1);
-        } else if (tail < BK) {
-            // zero the activations' bytes past id
-            for (int i = tid; i < BM * 8; i += NW * 64) {
-                const int r = i >> 3, slot = i & 7;
-                const int left = tail - 16 * (slot ^ (r & 7));   // valid bytes of the granule
-                if (left >= 16) continue;
-                u32x4 *p = reinterpret_cast<u32x4 *>(st + 16 * i);
-                u32x4 v = *p;
+    // Chunk c of a step is 32 bytes of every row: granules 2 c and 2 c + 1.
+    // Rows of one lane differ by multiples of 32, so its slot is the same in
+    // all of them.
+    constexpr int NC = BK / 32;
+    uint32_t aat[NC], bat[NC];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int b = left - 4 * w;
-                    v[w] = b >= 4 ? v[w] : (b <= 0 ? 0u : v[w] & ((1u << (8 * b)) - 1u));
-                }
-                *p = v;
+    for (int c = 0; c < NC; ++c) {
+        const uint32_t slot = 16 * ((2 * c + lhalf) ^ (lrow & 7));
+        aat[c] = (wm * TM * 32 + lrow) * BK + slot;
+        bat[c] = (BM + wn * TN * 32 + lrow) * BK + slot;
+    }
+    struct Frag {
+        i32x4 a[TM], b[TN];
+    } f[S == 2 ? 2 : NC];
+    auto read = [&](Frag &o, int kt, int c, int i) {
+        const uint8_t *st = lds + buffer(kt) * STAGE;
+        if (i < TN)
+            o.b[i] = *reinterpret_cast<const i32x4 *>(st + bat[c] + i * 32 * BK);
+        else
+            o.a[i - TN] = *reinterpret_cast<const i32x4 *>(st + aat[c] + (i - TN) * 32 * BK);
+    };
+    constexpr int NM = TM * TN, NR = TM + TN, NP = PA + PB, P3 = NP / 2;
+    // One chunk's MFMAs, in issue order, behind them the reads of the next
+    // chunk (chunk rc of step rk) one by one, and the copies [P0, P1) of step
+    // ck, evenly spread.
+    auto chunk = [&](auto reads, auto p0, auto p1, const Frag &o, Frag &nx, int rk, int rc, int ck) {
+        constexpr int P0 = p0, N = p1 - p0;
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            acc[i / TN][i % TN] = mfma_i8(o.a[i / TN], o.b[i % TN], acc[i / TN][i % TN]);
+            if constexpr (reads) {
+                if (i < NR) read(nx, rk, rc, i);
+                if (i == NM - 1)
+#pragma unroll
+                    for (int r = NM; r < NR; ++r) read(nx, rk, rc, r);
             }
-            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j * NM / (N > 0 ? N : 1) == i) copy(ck, P0 + j);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    constexpr std::integral_constant<int, 0> c0;
+    constexpr std::integral_constant<int, P3> cm;
+    constexpr std::integral_constant<int, NP> cn;
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    // All but the copies of the last S - 2 steps issued have landed, and
+    // everybody's reads before this point are done.
+    auto landed = [&](auto all) {
+        if constexpr (all)
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * NP) : "memory");
+        __syncthreads();
+    };
+    // Step kt, its first chunk in f[0]: with it go the copies of step
+    // kt + S - 1 from piece P3 on (`late`), and, once step kt + 1 has landed
+    // and the stage of step kt - 1 + S is free of readers, those of step
+    // kt + S up to P3 (`early`).
+    auto step = [&](auto late, auto early, int kt) {
+        if constexpr (late)
+            chunk(yes, cm, cn, f[0], f[1], kt, 1, kt + S - 1);
+        else
+            chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
+#pragma unroll
+        for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
+        landed(std::bool_constant<!late>{});
+        if constexpr (early) {
+            chunk(yes, c0, cm, f[(NC - 1) & 1], f[0], kt + 1, 0, kt + S);
+        } else {
+            if (kt + 1 == nk - 1 && tail < BK) clear_tail(lds + buffer(kt + 1) * STAGE);
+            chunk(yes, c0, c0, f[(NC - 1) & 1], f[0], kt + 1, 0, 0);
+        }
+    };
+
+    if constexpr (S == 2) {
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k)
+            if (k < nk)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) copy(k, p);
+        if (nk >= S - 1)
+            landed(no);
+        else
+            landed(yes);
+        if (nk == 1 && tail < BK) clear_tail(lds);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) read(f[0], 0, 0, i);
+        int kt = 0;
+        if (nk >= S) {
+#pragma unroll
+            for (int p = 0; p < P3; ++p) copy(S - 1, p);
+            for (; kt < nk - S; ++kt) step(yes, yes, kt);
+            step(yes, no, kt++);
+        }
+        for (; kt < nk - 1; ++kt) step(no, no, kt);
+        chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
+#pragma unroll
+        for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
+        chunk(no, c0, c0, f[(NC - 1) & 1], f[0], 0, 0, 0);
+    } else {
+        // Body kt multiplies step kt, held in registers, and reads step
+        // kt + 1 chunk by chunk into the registers as they come free, so
+        // nearly a whole step lies between a read and its use; it copies step
+        // kt + S - 1 into the stage of step kt - 1, whose reads every wave
+        // has used by then.
+        auto body = [&](auto copies, int kt) {
+            constexpr int N = copies ? NP : 0;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < NM; ++i) {
+                    acc[i / TN][i % TN] = mfma_i8(f[c].a[i / TN], f[c].b[i % TN], acc[i / TN][i % TN]);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (i == NM - 1) read(f[c], kt + 1, c, r);
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j * NM * NC / N == c * NM + i) copy(kt + S - 1, j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            if constexpr (copies)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k)
+            if (k < nk)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) copy(k, p);
+        if (nk >= S - 1)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (nk <= 2 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) read(f[c], 0, c, r);
+        int kt = 0;
+        for (; kt <= nk - S; ++kt) body(yes, kt);
+        for (; kt < nk - 1; ++kt) {
+            body(no, kt);
+            if (kt + 2 == nk - 1 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
         }
 #pragma unroll
-        for (int c = 0; c < BK / 32; ++c) {
-            i32x4 a[TM], b[TN];
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int m = 0; m < TM; ++m) {
-                const int r = (wm * TM + m) * 32 + lrow;
-                a[m] = *reinterpret_cast<const i32x4 *>(st + r * BK + 16 * ((2 * c + lhalf) ^ (r & 7)));
-            }
+            for (int i = 0; i < NM; ++i)
+                acc[i / TN][i % TN] = mfma_i8(f[c].a[i / TN], f[c].b[i % TN], acc[i / TN][i % TN]);
+    }
+
+    if constexpr (SPLIT) {
+        // Every share leaves its sums in its slot; the last to arrive at the
+        // tile adds the others' to its own (integers: in any order the same)
+        // and finishes.  Slots and counter go through agent-scope accesses:
+        // the shares run on XCDs whose L2s are not coherent.
+        constexpr int LANES = NW * 64;
+        const int tile = (int)(blockIdx.x / (unsigned)g.splits);
+        int32_t *slot = g.part + (int64_t)tile * g.splits * (BM * BN);
+        int32_t *mine = slot + (int64_t)split * (BM * BN) + tid;
 #pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                const int r = (wn * TN + n) * 32 + lrow;
-                b[n] = *reinterpret_cast<const i32x4 *>(st + BM * BK + r * BK + 16 * ((2 * c + lhalf) ^ (r & 7)));
-            }
+        for (int m = 0; m < TM; ++m)
+#pragma unroll
+            for (int n = 0; n < TN; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    __hip_atomic_store(mine + ((m * TN + n) * 16 + i) * LANES, acc[m][n][i], __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the sums are at the coherence point
+        __syncthreads();
+        __shared__ uint32_t s_before;
+        if (tid == 0) s_before = __hip_atomic_fetch_add(g.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (s_before != (uint32_t)g.splits - 1) return;
+        for (int o = 0; o < g.splits; ++o) {
+            if (o == split) continue;
+            int32_t *other = slot + (int64_t)o * (BM * BN) + tid;
 #pragma unroll
             for (int m = 0; m < TM; ++m)
 #pragma unroll
-                for (int n = 0; n < TN; ++n) acc[m][n] = mfma_i8(a[m], b[n], acc[m][n]);
+                for (int n = 0; n < TN; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[m][n][i] += __hip_atomic_load(other + ((m * TN + n) * 16 + i) * LANES, __ATOMIC_RELAXED,
+                                                          __HIP_MEMORY_SCOPE_AGENT);
         }
+        if (tid == 0) __hip_atomic_store(g.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 
     // Lane l, register i: token 8 (i / 4) + 4 (l / 32) + i % 4, weight row l % 32.
@@ -306,24 +518,243 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     }
 }
 
-template <int BM, int BN, int WM, int WN, bool GLU, bool EXPERTS, int YT>
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+// The weights' bytes are what counts here: each is used for a few products, and
+// a tile in LDS would only delay it.  A workgroup owns 16 weight rows (gated:
+// 16 gate and 16 up rows) and 16 tokens; its waves take the 128-byte pieces of
+// id in turn, load both operands straight into the registers of the
+// 16 x 16 x 64 MFMA (lane l: row l % 16, 16 bytes l / 16 of each 64), DEPTH
+// pieces before the first product, and their sums meet in LDS at the end.  The
+// weights are the rows of the result, so a lane holds four neighbouring
+// outputs of one token.
+constexpr int GEMV_WAVES = 8, GEMV_ROWS = 16;
+
+template <bool GLU, bool EXPERTS, int YT>
+__global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
+{
+    constexpr int NW = GEMV_WAVES, BM = 16;
+    constexpr int NB = GLU ? 2 : 1;   // blocks of 16 weight rows
+    constexpr int DEPTH = 4;          // pieces in flight a wave
+    __shared__ i32x4 s_sum[NW][NB][64];
+    __shared__ float s_sq[BM];
+    __shared__ int32_t s_row[EXPERTS ? BM : 1];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int jt = (int)(blockIdx.x % (unsigned)g.nbj), mt = (int)(blockIdx.x / (unsigned)g.nbj);
+    const int64_t j0 = (int64_t)jt * GEMV_ROWS;
+    const uint8_t *W = g.W;
+    const float *sw = g.sw, *bias = g.bias;
+    const int64_t t0 = (int64_t)mt * BM;
+    int count;
+    elem_t<YT> *y = static_cast<elem_t<YT> *>(g.y);
+    if constexpr (EXPERTS) {
+        const Rows r = find_rows<BM>(g.plan, g.ne, mt);
+        if (r.count == 0) return;
+        count = r.count;
+        const int32_t *order = g.plan + g.ne + 2 + r.first;
+        if (r.e == g.ne) {
+            // dropped rows: zeros
+            for (int i = tid; i < count * GEMV_ROWS; i += NW * 64)
+                if (j0 + i % GEMV_ROWS < g.od)
+                    y[(int64_t)order[i / GEMV_ROWS] * g.ldy + j0 + i % GEMV_ROWS] = (elem_t<YT>)0.0f;
+            return;
+        }
+        const int64_t rows = GLU ? 2 * g.od : g.od;
+        W += (int64_t)r.e * rows * g.ldw;
+        sw += (int64_t)r.e * rows;
+        if (bias) bias += (int64_t)r.e * rows;
+        if (tid < BM) {
+            const int32_t row = order[tid < count ? tid : count - 1];
+            s_row[tid] = row;
+            s_sq[tid] = g.sq[row / g.slots];
+        }
+        __syncthreads();
+    } else {
+        count = (int)(g.nt - t0 < BM ? g.nt - t0 : BM);
+        if (tid < BM) s_sq[tid] = g.sq[t0 + (tid < count ? tid : count - 1)];
+    }
+    const int l16 = lane & 15, quad = lane >> 4;
+    const int64_t j = j0 + l16 < g.od ? j0 + l16 : g.od - 1;
+    const uint8_t *wp[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wp[b] = W + (j + b * g.od) * g.ldw + 16 * quad;
+    const int64_t xrow = EXPERTS ? (int64_t)(s_row[l16] / g.slots) : t0 + (l16 < count ? l16 : count - 1);
+    const uint8_t *xp = g.q + xrow * g.ldq + 16 * quad;
+    i32x4 acc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = i32x4{0, 0, 0, 0};
+
+    struct Piece {
+        i32x4 w[NB][2], x[2];
+    };
+    auto load = [&](Piece &p, int64_t k) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) p.w[b][h] = *reinterpret_cast<const i32x4 *>(wp[b] + k + 64 * h);
+            p.x[h] = *reinterpret_cast<const i32x4 *>(xp + k + 64 * h);
+        }
+    };
+    auto multiply = [&](const Piece &p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(p.w[b][h], p.x[h], acc[b], 0, 0, 0);
+    };
+    const int full = g.id / BK;
+    Piece p[DEPTH];
+    int c = wave;
+    for (; c + (DEPTH - 1) * NW < full; c += DEPTH * NW) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(p[d], (int64_t)(c + d * NW) * BK);
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) multiply(p[d]);
+    }
+    // fewer than DEPTH pieces left: still all loads before the products (a
+    // piece that is not there is read as the first, and zeroed in x)
+    if (c < full) {
+#pragma unroll
+        for (int d = 0; d < DEPTH - 1; ++d) {
+            const bool there = c + d * NW < full;
+            load(p[d], there ? (int64_t)(c + d * NW) * BK : 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) p[d].x[h] = there ? p[d].x[h] : i32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH - 1; ++d) multiply(p[d]);
+    }
+    if (full % NW == wave && g.id % BK != 0) {
+        // the last, partial piece: granules past id are not read, and the
+        // tokens' bytes past id are zeros
+        const int64_t k = (int64_t)full * BK;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int left = g.id - (int)k - 64 * h - 16 * quad;   // valid bytes of this lane's granule
+            const int64_t at = left > 0 ? k + 64 * h : -16 * quad;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) p[0].w[b][h] = *reinterpret_cast<const i32x4 *>(wp[b] + at);
+            i32x4 v = *reinterpret_cast<const i32x4 *>(xp + at);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int b = left - 4 * w;
+                v[w] = b >= 4 ? v[w] : (b <= 0 ? 0 : (int)((uint32_t)v[w] & ((1u << (8 * b)) - 1u)));
+            }
+            p[0].x[h] = v;
+        }
+        multiply(p[0]);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s_sum[wave][b][lane] = acc[b];
+    __syncthreads();
+    // waves 0 .. 3 finish one of a lane's four outputs each
+    if (wave >= 4) return;
+    int v[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        v[b] = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v[b] += reinterpret_cast<const int32_t *>(&s_sum[w][b][lane])[wave];
+    }
+    const int64_t o = j0 + 4 * quad + wave;
+    if (l16 >= count || o >= g.od) return;
+    const float s = s_sq[l16];
+    float r = (float)v[0] * s * sw[o] + (bias ? bias[o] : 0.0f);
+    if constexpr (GLU) r = silu_mul(r, (float)v[NB - 1] * s * sw[g.od + o] + (bias ? bias[g.od + o] : 0.0f));
+    const int64_t row = EXPERTS ? (int64_t)s_row[l16] : t0 + l16;
+    y[row * g.ldy + o] = (elem_t<YT>)r;
+}
+
+template <bool GLU, bool EXPERTS, int YT>
+static int launch_gemv(I8Args a, hipStream_t stream)
+{
+    const int64_t nbj = (a.od + GEMV_ROWS - 1) / GEMV_ROWS;
+    const int64_t nbt = EXPERTS ? a.nt / 16 + (a.nt < a.ne + 1 ? a.nt : a.ne + 1) : (a.nt + 15) / 16;
+    if (nbt * nbj > 0x7fffffff) return -1;
+    a.nbt = (int)nbt;
+    a.nbj = (int)nbj;
+    return launch_kernel(gemv_i8_kernel<GLU, EXPERTS, YT>, dim3((unsigned)(nbt * nbj)), dim3(GEMV_WAVES * 64), stream,
+                         a);
+}
+
+template <int BM, int BN, int WM, int WN, int S, bool SPLIT, bool GLU, bool EXPERTS, int YT>
 static int launch_tile(I8Args a, int64_t od, int64_t nt, hipStream_t stream)
 {
     constexpr int BJ = GLU ? BN / 2 : BN;
     const int64_t nbj = (od + BJ - 1) / BJ;
     // experts: every expert, and the dropped rows, may end in a partial tile
     const int64_t nbt = EXPERTS ? nt / BM + (nt < a.ne + 1 ? nt : a.ne + 1) : (nt + BM - 1) / BM;
-    if (nbt * nbj > 0x7fffffff) return -1;
+    const int64_t n = nbt * nbj * (SPLIT ? a.splits : 1);
+    if (n > 0x7fffffff) return -1;
     a.nbt = (int)nbt;
     a.nbj = (int)nbj;
-    return launch_kernel(gemm_i8_kernel<BM, BN, WM, WN, GLU, EXPERTS, YT>, dim3((unsigned)(nbt * nbj)),
+    return launch_kernel(gemm_i8_kernel<BM, BN, WM, WN, S, SPLIT, GLU, EXPERTS, YT>, dim3((unsigned)n),
                          dim3(WM * WN * 64), stream, a);
 }
 
-template <bool GLU, bool EXPERTS, int YT>
-static int pick(const I8Args &a, hipStream_t stream)
+// What a tile shape costs, in us per 128-byte step of one tile.  `alone`: a
+// round of tiles (one a CU; two for 128 x 128) whose CUs are not all busy;
+// `full`: a CU's share when all are, where the card's power holds the clock
+// down (1.75 GHz measured under the 256 x 256 tiles against 2.4).  Measured at
+// 8192^3 (full) and at 3584 x 18944 with 2630 tokens (alone).
+struct TileCost {
+    int bm, bn, per_cu;
+    double alone, full, ends;   // ends: first loads and epilogue of a round, us
+};
+constexpr TileCost COST_256 = {256, 256, 1, 1.25, 1.9, 8.0};
+constexpr TileCost COST_192 = {192, 256, 1, 0.95, 1.48, 7.0};
+constexpr TileCost COST_64 = {64, 128, 1, 0.30, 0.36, 6.0};
+
+template <bool GLU, bool EXPERTS>
+static double cost(const TileCost &c, const I8Args &a)
 {
-    return launch_tile<128, 128, 2, 2, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
+    const double nbj = (double)((a.od + (GLU ? c.bn / 2 : c.bn) - 1) / (GLU ? c.bn / 2 : c.bn));
+    // experts: half a tile lost in each that has rows
+    const double nbt = EXPERTS ? (double)a.nt / c.bm + 0.5 * (double)(a.nt < a.ne ? a.nt : a.ne)
+                               : (double)((a.nt + c.bm - 1) / c.bm);
+    const double tiles = nbt * nbj, rounds = __builtin_ceil(tiles / (256.0 * c.per_cu));
+    const double nk = (double)((a.id + BK - 1) / BK);
+    const double busy = tiles / 256.0 * c.full, alone = rounds * c.alone;
+    return nk * (busy > alone ? busy : alone) + rounds * c.ends;
+}
+
+// Bytes of weights (times passes over them) up to which the few-token kernel
+// is taken whatever the number of tokens: at 12.8 MB (3584 x 3584) it measured
+// 7.7 us against the tiles' 13 us at 16 tokens and level with them at 64; at
+// 68 MB and 32 tokens 37 us against 24 us.
+constexpr int64_t GEMV_BYTES = int64_t(40) << 20;
+// Split sums: shares of at least SPLIT_STEPS steps, a workgroup a CU, and at
+// most SPLIT_MOST shares: the last share to arrive reads the others' sums one
+// after the other (18944 -> 3584, 32 tokens: 48 us whole, 24 us in four, 28 us
+// in nine).  SPLIT_SLOTS and SPLIT_TILES are what the workspace holds.
+constexpr int SPLIT_STEPS = 16, SPLIT_MOST = 4, SPLIT_SLOTS = 1024, SPLIT_TILES = 4096, SPLIT_CUS = 256;
+
+template <bool GLU, bool EXPERTS, int YT>
+static int pick(I8Args a, hipStream_t stream)
+{
+    const int64_t wbytes = (GLU ? 2 : 1) * a.od * (int64_t)a.id;
+    if (EXPERTS ? a.nt <= 10 * (int64_t)a.ne
+                : a.nt <= 16 || (a.nt <= 64 && (a.nt + 15) / 16 * wbytes <= GEMV_BYTES))
+        return launch_gemv<GLU, EXPERTS, YT>(a, stream);
+    const double c256 = cost<GLU, EXPERTS>(COST_256, a), c192 = cost<GLU, EXPERTS>(COST_192, a);
+    const double c64 = cost<GLU, EXPERTS>(COST_64, a);
+    if (c64 < c256 && c64 < c192) {
+        if constexpr (!EXPERTS) {
+            const int64_t tiles = (a.nt + 63) / 64 * ((a.od + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
+            const int64_t nk = (a.id + BK - 1) / BK;
+            const int64_t splits = std::min<int64_t>(std::min<int64_t>(nk / SPLIT_STEPS, SPLIT_MOST), SPLIT_CUS / tiles);
+            if (a.part && splits >= 2 && tiles * splits <= SPLIT_SLOTS && tiles <= SPLIT_TILES) {
+                a.splits = (int)splits;
+                return launch_tile<64, 128, 2, 2, 4, true, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
+            }
+        }
+        return launch_tile<64, 128, 2, 2, 4, false, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
+    }
+    if (c192 < c256) return launch_tile<192, 256, 2, 4, 2, false, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
+    return launch_tile<256, 256, 2, 4, 2, false, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
 }
 
 template <int YT>
@@ -343,6 +774,10 @@ int launch_i8_gemm(const I8Gemm &g, hipStream_t stream)
     a.bias = g.bias;
     a.y = g.y;
     a.plan = g.plan;
+    a.part = static_cast<int32_t *>(g.ws);
+    a.cnt = g.ws ? reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(g.ws) + mmq_ws_partial_bytes(MMQ_MAX_WORKERS))
+                 : nullptr;
+    a.splits = 1;
     a.ldw = g.ldw;
     a.ldq = g.ldq;
     a.ldy = g.ldy;
