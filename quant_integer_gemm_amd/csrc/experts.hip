@@ -12,69 +12,142 @@ namespace qig {
 // ---------------------------------------------------------------------------
 // Scores: p = softmax(l) or sigmoid(l); the choice is by c = p + bias, the k
 // largest among the experts of the topk_groups best groups (a group's score:
-// the sum of its group_top largest c), equal values to the lower index.  The
-// scores are formed and compared in 64 bits: which expert wins is a
-// comparison of near values, and in 32 bits the rounding of exp would decide
-// about one row in ten thousand.  Softmax without a bias keeps the order of
-// the logits, so there the choice compares the logits themselves (also where
-// the scores underflow).  A logit of -infinity or NaN is an expert that may
-// not be chosen; +infinity counts as the largest finite number.
+// the sum of its group_top largest c), equal values to the lower index.  Which
+// expert wins is a comparison of near values: it is decided in 64 bits, since
+// in 32 the rounding of exp would decide about one row in ten thousand.
+// Softmax without a bias keeps the order of the logits, so there the choice
+// compares the logits themselves (also where the scores underflow).  A logit of
+// -infinity or NaN is an expert that may not be chosen; +infinity counts as the
+// largest finite number.
+//
+// Only rows that need 64 bits pay for them: route_kernel first chooses by c in
+// 32 bits with a bound on its error.  Where neighbours among the first k + 1 are
+// nearer than that bound, those are put in order by their c in 64 bits; where
+// that cannot settle it (three values at the border of the chosen, two groups at
+// theirs), the whole row is chosen again by route_exact.  The weights of the k
+// chosen are formed in 64 bits either way (one expert a lane).
 
-// One wave a token, lane l holding experts l, l + 64, ...
-template <int NS, int T>
-__global__ __launch_bounds__(64) void route_kernel(RouteArgs a)
+constexpr float LARGEST = 3.402823466e38f;
+
+// Order-preserving integer of a finite or infinite fp32 (never 0).
+__device__ __forceinline__ uint32_t order_key(float x)
 {
-    __shared__ double s_c[NS * 64];
-    __shared__ double s_g[64];
-    __shared__ uint8_t s_keep[64];
-    const int lane = threadIdx.x;
-    const int64_t t = blockIdx.x;
-    const elem_t<T> *l = static_cast<const elem_t<T> *>(a.logits) + t * a.ldl;
-    double v[NS], p[NS], c[NS];
-    bool ok[NS];
-    double top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int e = lane + 64 * i;
-        float x = e < a.ne ? (float)l[e] : -INFINITY;
-        ok[i] = x > -INFINITY;   // false for NaN
-        x = ok[i] ? __builtin_fminf(x, 3.402823466e38f) : 0.0f;
-        v[i] = (double)x;
-        if (ok[i]) top = fmax(top, v[i]);
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);   // -0 to +0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// Largest of the wave's values, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+#define QIG_STEP(ctrl, rows)                                                                                   \
+    {                                                                                                          \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false);           \
+        v = o > v ? o : v;                                                                                     \
     }
-    if (a.score == 0) {
+    QIG_STEP(0x111, 0xf)   // from the lane 1 before, in rows of 16
+    QIG_STEP(0x112, 0xf)
+    QIG_STEP(0x114, 0xf)
+    QIG_STEP(0x118, 0xf)
+    QIG_STEP(0x142, 0xa)   // last lane of row 0 to row 1, of 2 to 3
+    QIG_STEP(0x143, 0xc)   // last lane of row 1 to rows 2 and 3
+#undef QIG_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+__device__ __forceinline__ void lds_order()
+{
+    // one wave's LDS accesses are executed in order: only the compiler must
+    // keep theirs
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A logit as the routing takes it: whether the expert may be chosen.
+__device__ __forceinline__ bool take_logit(bool there, float v, float &x)
+{
+    x = there ? v : -INFINITY;
+    const bool ok = x > -INFINITY;   // false for NaN
+    x = ok ? __builtin_fminf(x, LARGEST) : 0.0f;
+    return ok;
+}
+
+// A lane's NS neighbouring values, n of them there (0 for the others).
+template <int NS, typename E>
+__device__ __forceinline__ void load_run(const E *p, int n, float (&o)[NS])
+{
+    if (n >= NS) {
+        struct __attribute__((packed, aligned(2))) Run {
+            E v[NS];
+        };
+        const Run r = *reinterpret_cast<const Run *>(p);
 #pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            p[i] = ok[i] ? exp(v[i] - top) : 0.0;
-            sum += p[i];
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-        const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) p[i] *= inv;
+        for (int i = 0; i < NS; ++i) o[i] = (float)r.v[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) p[i] = ok[i] ? 1.0 / (1.0 + exp(-v[i])) : 0.0;
+        for (int i = 0; i < NS; ++i) o[i] = i < n ? (float)p[i] : 0.0f;
     }
-    const bool by_logit = a.score == 0 && !a.bias && (a.groups == 1 || a.group_top == 1);
+}
+
+// One wave chooses a token's experts in 64 bits: lane l holds experts l,
+// l + 64, ...  Returns the expert of slot `lane` (-1: none).
+template <int NS, int T>
+__device__ int route_exact(const RouteArgs &a, const elem_t<T> *l, double *s_c, double *s_g, uint8_t *s_keep)
+{
+    const int lane = threadIdx.x & 63;
+    double c[NS];
+    bool ok[NS];
+    double top = -INFINITY, sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
+        float x;
         const int e = lane + 64 * i;
-        c[i] = by_logit ? v[i] : p[i] + (a.bias && e < a.ne ? (double)a.bias[e] : 0.0);
+        ok[i] = take_logit(e < a.ne, e < a.ne ? (float)l[e] : 0.0f, x);
+        c[i] = (double)x;
+        if (ok[i]) top = fmax(top, c[i]);
+    }
+    const bool by_logit = a.score == 0 && !a.bias && (a.groups == 1 || a.group_top == 1);
+    if (!by_logit) {
+        if (a.score == 0) {
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                c[i] = ok[i] ? exp(c[i] - top) : 0.0;
+                sum += c[i];
+            }
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+            const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) c[i] *= inv;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) c[i] = ok[i] ? 1.0 / (1.0 + exp(-c[i])) : 0.0;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (a.bias && lane + 64 * i < a.ne) c[i] += (double)a.bias[lane + 64 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
         if (!ok[i] || !(c[i] > -INFINITY)) {
             ok[i] = false;
             c[i] = -INFINITY;
         }
-    }
     if (a.groups > 1) {
         const int size = a.ne / a.groups;
 #pragma unroll
         for (int i = 0; i < NS; ++i) s_c[lane + 64 * i] = c[i];
-        __syncthreads();
+        lds_order();
         if (lane < a.groups) {
             double b1 = -INFINITY, b2 = -INFINITY;
             for (int e = lane * size; e < (lane + 1) * size; ++e) {
@@ -85,64 +158,281 @@ __global__ __launch_bounds__(64) void route_kernel(RouteArgs a)
             // a group's missing second score adds nothing
             s_g[lane] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
         }
-        __syncthreads();
+        lds_order();
         if (lane < a.groups) {
             int better = 0;
-            for (int o = 0; o < a.groups; ++o)
-                better += s_g[o] > s_g[lane] || (s_g[o] == s_g[lane] && o < lane);
+            for (int o = 0; o < a.groups; ++o) better += s_g[o] > s_g[lane] || (s_g[o] == s_g[lane] && o < lane);
             s_keep[lane] = better < a.topk_groups;
         }
-        __syncthreads();
+        lds_order();
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int e = lane + 64 * i;
             if (e < a.ne && !s_keep[e / size]) ok[i] = false;
         }
     }
-    // k rounds of the largest remaining (value, then lowest index)
-    double wsum = 0.0, mine = 0.0;
     int my_id = -1;
     for (int r = 0; r < a.k; ++r) {
-        double best = -INFINITY, bp = 0.0;
+        double best = -INFINITY;
         int be = 0x7fffffff;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             if (ok[i] && c[i] > best) {
                 best = c[i];
                 be = lane + 64 * i;
-                bp = p[i];
             }
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) {
-            const double ob = __shfl_xor(best, d), op = __shfl_xor(bp, d);
+            const double ob = __shfl_xor(best, d);
             const int oe = __shfl_xor(be, d);
             if (ob > best || (ob == best && oe < be)) {
                 best = ob;
                 be = oe;
-                bp = op;
             }
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             if (lane + 64 * i == be) ok[i] = false;
-        const bool found = be != 0x7fffffff;
-        if (lane == r) {
-            my_id = found ? be : -1;
-            mine = found ? bp : 0.0;
+        if (lane == r && be != 0x7fffffff) my_id = be;
+    }
+    return my_id;
+}
+
+constexpr int ROUTE_WAVES = 4;
+
+// One wave a token, four a workgroup; lane l holds the NS experts from l NS on,
+// sorted by falling key, so that each of the k rounds compares one key a lane:
+// a DPP maximum over the wave, then the first lane that has it (the lowest
+// expert among equals, since a lane's equals stay in order).
+//
+// Error bounds of the 32-bit scores (u = 2^-24): sigmoid(x) is off by at most
+// p (1 - p) (|x| + 2) u + 3 p u < 4 u; softmax, its sum of up to 512 terms added
+// in a tree of 15 levels, by less than 20 u times the row's largest p; the sum
+// with the bias adds u |c|.  A comparison of two group scores takes four of
+// them.  So values further apart than 2^-20 (sigmoid) or 2^-17 p_max (softmax)
+// plus 2^-21 |c| (a group's score: the sum of its |c|) are in their exact order.
+//
+// Bound by its instructions and their latencies, not by the logits' bytes:
+// 16384 tokens, 256 experts in 8 groups, k = 8 (17 MB) 26 us, without groups 18,
+// and 14 for k = 1.  Eight waves a SIMD (64 registers) against six: 26 and 30.
+template <int NS, int T>
+__global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kernel(RouteArgs a)
+{
+    __shared__ double s_all[ROUTE_WAVES][NS * 64 + 64];
+    __shared__ uint8_t s_keeps[ROUTE_WAVES][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + wave;
+    if (t >= a.nt) return;
+    const elem_t<T> *l = static_cast<const elem_t<T> *>(a.logits) + t * a.ldl;
+    float x[NS], c[NS];
+    bool ok[NS];
+    float top = -INFINITY;
+    const int here = a.ne - lane * NS;   // experts of this lane (any number)
+    load_run<NS>(l + lane * NS, here, x);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        ok[i] = take_logit(i < here, x[i], x[i]);
+        if (ok[i]) top = __builtin_fmaxf(top, x[i]);
+    }
+    if (a.score == 0) top = key_value(wave_max(order_key(top)));
+    const bool by_logit = a.score == 0 && !a.bias && (a.groups == 1 || a.group_top == 1);
+    float tol = 0.0f;   // nearer values than tol + 2^-21 |c| are not told apart here
+    if (by_logit) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) c[i] = x[i];
+    } else {
+        if (a.score == 0) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                c[i] = ok[i] ? __builtin_amdgcn_exp2f((x[i] - top) * 1.4426950408889634f) : 0.0f;
+                sum += c[i];
+            }
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) c[i] *= inv;
+            tol = 0x1p-17f * inv;   // the largest p is inv
+        } else {
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                c[i] = ok[i] ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.4426950408889634f)) : 0.0f;
+            tol = 0x1p-20f;
         }
-        wsum += found ? bp : 0.0;
+        if (a.bias) {
+            float b[NS];
+            load_run<NS>(a.bias + lane * NS, here, b);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) c[i] += b[i];
+        }
+    }
+    // key 0: not to be chosen
+    uint32_t key[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) key[i] = ok[i] && c[i] > -INFINITY ? order_key(c[i]) : 0u;
+    bool near_groups = false;
+    if (a.groups > 1) {
+        const int size = a.ne / a.groups;
+        uint32_t *s_k = reinterpret_cast<uint32_t *>(s_all[wave]);
+        uint8_t *s_keep = s_keeps[wave];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) s_k[lane * NS + i] = key[i];
+        lds_order();
+        // `lanes` lanes a group (a power of two), each over every lanes-th expert
+        int lanes = 1;
+        while (2 * lanes * a.groups <= 64) lanes *= 2;
+        const int g = lane / lanes;
+        uint32_t b1 = 0, b2 = 0;
+        if (g < a.groups)
+            for (int e = g * size + lane % lanes; e < (g + 1) * size; e += lanes) {
+                const uint32_t v = s_k[e];
+                const uint32_t low = b1 < v ? b1 : v;
+                b2 = low > b2 ? low : b2;
+                b1 = b1 > v ? b1 : v;
+            }
+        for (int d = 1; d < lanes; d *= 2) {
+            const uint32_t o1 = (uint32_t)__shfl_xor((int)b1, d), o2 = (uint32_t)__shfl_xor((int)b2, d);
+            const uint32_t low = b1 < o1 ? b1 : o1;
+            b2 = b2 > o2 ? b2 : o2;
+            b2 = low > b2 ? low : b2;
+            b1 = b1 > o1 ? b1 : o1;
+        }
+        // a group's missing second score adds nothing; -infinity: nothing to choose
+        float score = b1 ? key_value(b1) : -INFINITY;
+        float size12 = __builtin_fabsf(score);   // of the terms that the score is rounded from
+        if (a.group_top == 2 && b2) {
+            score += key_value(b2);
+            size12 += __builtin_fabsf(key_value(b2));
+        }
+        int rank = 64;   // of the group, in its first lane
+        if (lane % lanes == 0 && g < a.groups) rank = 0;
+        for (int o = 0; o < a.groups; ++o) {
+            const float other = lane_value(score, o * lanes);
+            rank += other > score || (other == score && o < g);
+        }
+        if (lane % lanes == 0 && g < a.groups) s_keep[g] = rank < a.topk_groups;
+        if (!by_logit && a.topk_groups < a.groups) {
+            // the last group that stays against the first that goes
+            const int w0 = __ffsll((unsigned long long)__ballot(rank == a.topk_groups - 1)) - 1;
+            const int w1 = __ffsll((unsigned long long)__ballot(rank == a.topk_groups)) - 1;
+            const float size12s = __builtin_fmaxf(lane_value(size12, w0), lane_value(size12, w1));
+            near_groups = lane_value(score, w0) - lane_value(score, w1) <= tol + 0x1p-21f * size12s;
+        }
+        lds_order();
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int e = lane * NS + i;
+            if (e < a.ne && !s_keep[e / size]) key[i] = 0;
+        }
+    }
+    // the lane's keys by falling value, equals in order
+    int slot[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) slot[i] = i;
+#pragma unroll
+    for (int i = 1; i < NS; ++i)
+#pragma unroll
+        for (int j = i; j > 0; --j) {
+            const bool swap = key[j] > key[j - 1];
+            const uint32_t k0 = swap ? key[j] : key[j - 1], k1 = swap ? key[j - 1] : key[j];
+            const int s0 = swap ? slot[j] : slot[j - 1], s1 = swap ? slot[j - 1] : slot[j];
+            key[j - 1] = k0;
+            key[j] = k1;
+            slot[j - 1] = s0;
+            slot[j] = s1;
+        }
+    // round r puts its key and expert into lane r; two rounds more than k show
+    // what the last ones won against
+    int my_id = -1;
+    uint32_t my_key = 0;
+    const int rounds = by_logit ? a.k : a.k + 2;
+    for (int r = 0; r < rounds; ++r) {
+        const uint32_t best = wave_max(key[0]);
+        const int w = __ffsll((unsigned long long)__ballot(key[0] == best)) - 1;
+        const int id = w * NS + __builtin_amdgcn_readlane(slot[0], w);
+        my_id = lane == r ? id : my_id;
+        my_key = lane == r ? best : my_key;
+        const bool mine = lane == w;
+#pragma unroll
+        for (int i = 0; i + 1 < NS; ++i) {
+            key[i] = mine ? key[i + 1] : key[i];
+            slot[i] = mine ? slot[i + 1] : slot[i];
+        }
+        key[NS - 1] = mine ? 0u : key[NS - 1];
+    }
+    if (!by_logit) {
+        // nearer to the next (or the one after it) than the bound?
+        const uint32_t k1 = (uint32_t)__shfl_down((int)my_key, 1), k2 = (uint32_t)__shfl_down((int)my_key, 2);
+        const float v = key_value(my_key), n1 = key_value(k1), n2 = key_value(k2);
+        const bool near1 = k1 != 0 && v - n1 <= tol + 0x1p-21f * __builtin_fabsf(n1);
+        const bool near2 = k2 != 0 && v - n2 <= tol + 0x1p-21f * __builtin_fabsf(n2);
+        if (near_groups || __any(lane == a.k - 1 && near2)) {
+            my_id = route_exact<NS, T>(a, l, s_all[wave], s_all[wave] + NS * 64, s_keeps[wave]);
+            my_key = my_id >= 0 ? 1u : 0u;
+        } else if (__any(lane < a.k && near1)) {
+            // the k + 1 first hold the k chosen: put them in order in 64 bits
+            double e = -INFINITY, sum = 1.0;
+            if (a.score == 0) {
+                sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) sum += ok[i] ? exp((double)x[i] - (double)top) : 0.0;
+#pragma unroll
+                for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+            }
+            if (lane <= a.k && my_key != 0) {
+                float xi;
+                take_logit(true, (float)l[my_id], xi);
+                e = a.score == 0 ? exp((double)xi - (double)top) * (1.0 / sum) : 1.0 / (1.0 + exp(-(double)xi));
+                if (a.bias) e += (double)a.bias[my_id];
+            }
+            int rank = 0;
+            for (int o = 0; o <= a.k; ++o) {
+                const double oe = __shfl(e, o);
+                const int oid = __shfl(my_id, o);
+                rank += oe > e || (oe == e && (e == -INFINITY ? o < lane : oid < my_id));
+            }
+            if (lane > a.k) rank = lane;
+            my_id = __builtin_amdgcn_ds_permute(4 * rank, my_id);
+            my_key = (uint32_t)__builtin_amdgcn_ds_permute(4 * rank, (int)my_key);
+        }
+    }
+    if (lane >= a.k || my_key == 0) my_id = -1;
+
+    // weights in 64 bits, lane r the r-th chosen
+    double p = 0.0;
+    float xi = 0.0f;
+    if (my_id >= 0) take_logit(true, (float)l[my_id], xi);
+    if (a.score == 0) {
+        p = my_id >= 0 ? exp((double)xi - (double)top) : 0.0;
+        if (!a.renorm) {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) sum += ok[i] ? exp((double)x[i] - (double)top) : 0.0;
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+            p = my_id >= 0 ? p / sum : 0.0;
+        }
+    } else if (my_id >= 0) {
+        p = 1.0 / (1.0 + exp(-(double)xi));
+    }
+    double scale = (double)a.scale;
+    if (a.renorm) {
+        double sum = p;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor(sum, d);   // k is at most 32
+        scale = sum > 0.0 ? scale / sum : 0.0;
     }
     if (lane < a.k) {
-        const double scale = a.renorm ? (wsum > 0.0 ? (double)a.scale / wsum : 0.0) : (double)a.scale;
         a.ids[t * a.k + lane] = my_id;
-        a.w[t * a.k + lane] = (float)(mine * scale);
+        a.w[t * a.k + lane] = (float)(p * scale);
     }
 }
 
 template <int T>
 static int route_typed(const RouteArgs &a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)a.nt), block(64);
+    const dim3 grid((unsigned)((a.nt + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(ROUTE_WAVES * 64);
     if (a.ne <= 64) return launch_kernel(route_kernel<1, T>, grid, block, stream, a);
     if (a.ne <= 128) return launch_kernel(route_kernel<2, T>, grid, block, stream, a);
     if (a.ne <= 256) return launch_kernel(route_kernel<4, T>, grid, block, stream, a);
@@ -162,34 +452,61 @@ int launch_route(const RouteArgs &a, hipStream_t stream)
 // ---------------------------------------------------------------------------
 // the order of rows by expert
 // ---------------------------------------------------------------------------
-// A stable counting sort by one workgroup: every wave counts a contiguous
-// share of the rows per expert, the counts become first positions (expert
-// major, wave minor), and every wave places its rows in order.  Ids outside
+// A stable counting sort in one launch.  Every workgroup counts all rows per
+// expert, those before its own share apart (LDS counters; the ids come from the
+// caches), which gives it the first position of its rows of each expert without
+// waiting for another workgroup; then each wave places its part of the share,
+// 64 rows at a time, a row's rank among the 64 being the number of lower lanes
+// with the same expert.  The placing is what costs (a ballot a bit of the
+// expert's number), and it is what the workgroups share out.  Ids outside
 // [0, ne) count as expert ne (dropped rows).
-constexpr int PLAN_WAVES = 16;
+constexpr int PLAN_WAVES = 16, PLAN_THREADS = PLAN_WAVES * 64, PLAN_BATCH = 16, PLAN_GROUPS = 64;
 
-__global__ __launch_bounds__(PLAN_WAVES * 64) void plan_kernel(const int32_t *__restrict__ ids, int nrows, int ne,
-                                                               int32_t *__restrict__ plan)
+__global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(const int32_t *__restrict__ ids, int nrows, int ne,
+                                                            int share, int32_t *__restrict__ plan)
 {
-    extern __shared__ int32_t hist[];   // [ne + 1][PLAN_WAVES]
+    __shared__ int32_t s_before[EXPERTS_MAX + 1], s_rest[EXPERTS_MAX + 1];
+    __shared__ int32_t s_at[EXPERTS_MAX + 1][PLAN_WAVES];   // next position of a wave's rows
     __shared__ int32_t part[PLAN_WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n = (ne + 1) * PLAN_WAVES;
-    for (int i = tid; i < n; i += PLAN_WAVES * 64) hist[i] = 0;
+    const int lo = (int)blockIdx.x * share;   // a multiple of PLAN_THREADS
+    const int per = share / PLAN_WAVES;       // a wave's rows, a multiple of 64
+    const int wlo = lo + wave * per;
+    const int whi = wlo + per < nrows ? wlo + per : nrows;
+    int e[PLAN_BATCH];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int b = 0; b < PLAN_BATCH; ++b) {
+            const int64_t i = (int64_t)i0 + PLAN_THREADS * b + tid;
+            e[b] = i < nrows ? ids[i] : -1;
+        }
+#pragma unroll
+        for (int b = 0; b < PLAN_BATCH; ++b) e[b] = (unsigned)e[b] < (unsigned)ne ? e[b] : ne;
+    };
+    load(0);
+    for (int i = tid; i <= ne; i += PLAN_THREADS) {
+        s_before[i] = 0;
+        s_rest[i] = 0;
+    }
+    for (int i = tid; i < (ne + 1) * PLAN_WAVES; i += PLAN_THREADS) s_at[i / PLAN_WAVES][i % PLAN_WAVES] = 0;
     __syncthreads();
-    const int per = (nrows + PLAN_WAVES * 64 - 1) / (PLAN_WAVES * 64) * 64;
-    const int lo = wave * per, hi = lo + per < nrows ? lo + per : nrows;
-    for (int i = lo + lane; i < hi; i += 64) {
-        const int e = ids[i];
-        atomicAdd(&hist[((unsigned)e < (unsigned)ne ? e : ne) * PLAN_WAVES + wave], 1);
+    for (int64_t i0 = 0; i0 < nrows; i0 += PLAN_THREADS * PLAN_BATCH) {
+        if (i0 > 0) load((int)i0);
+#pragma unroll
+        for (int b = 0; b < PLAN_BATCH; ++b) {
+            const int64_t i = i0 + PLAN_THREADS * b;
+            if (i + tid < nrows) atomicAdd(i < lo ? &s_before[e[b]] : &s_rest[e[b]], 1);
+        }
+    }
+    for (int i = wlo + lane; i < whi; i += 64) {
+        const int x = ids[i];
+        atomicAdd(&s_at[(unsigned)x < (unsigned)ne ? x : ne][wave], 1);
     }
     __syncthreads();
-    // exclusive scan of hist in its order
-    const int chunk = (n + PLAN_WAVES * 64 - 1) / (PLAN_WAVES * 64);
-    const int a = tid * chunk, b = a + chunk < n ? a + chunk : n;
-    int sum = 0;
-    for (int i = a; i < b; ++i) sum += hist[i];
-    int incl = sum;
+    // thread i: expert i (ne <= 512 < 1024)
+    const int before = tid <= ne ? s_before[tid] : 0;
+    const int all = tid <= ne ? before + s_rest[tid] : 0;
+    int incl = all;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int o = __shfl_up(incl, d);
@@ -197,60 +514,115 @@ __global__ __launch_bounds__(PLAN_WAVES * 64) void plan_kernel(const int32_t *__
     }
     if (lane == 63) part[wave] = incl;
     __syncthreads();
-    int at = incl - sum;
-    for (int w = 0; w < wave; ++w) at += part[w];
-    for (int i = a; i < b; ++i) {
-        const int c = hist[i];
-        hist[i] = at;
-        at += c;
+    int first = incl - all;
+    for (int w = 0; w < wave; ++w) first += part[w];
+    if (tid <= ne) {
+        int at = first + before;
+#pragma unroll
+        for (int w = 0; w < PLAN_WAVES; ++w) {
+            const int c = s_at[tid][w];
+            s_at[tid][w] = at;
+            at += c;
+        }
+        if (blockIdx.x == 0) plan[tid] = first;
     }
-    __syncthreads();
-    for (int e = tid; e <= ne; e += PLAN_WAVES * 64) plan[e] = hist[e * PLAN_WAVES];
-    if (tid == 0) plan[ne + 1] = nrows;
+    if (blockIdx.x == 0 && tid == 0) plan[ne + 1] = nrows;
     __syncthreads();
     int32_t *order = plan + ne + 2;
-    for (int i0 = lo; i0 < hi; i0 += 64) {
+    const int bits = 32 - __builtin_clz(ne);
+    for (int i0 = wlo; i0 < whi; i0 += 64) {
         const int i = i0 + lane;
-        const bool live = i < hi;
-        int e = live ? ids[i] : ne;
-        e = (unsigned)e < (unsigned)ne ? e : ne;
-        // lanes with the same expert, by its bits
-        uint64_t same = __ballot(live);
-        for (int bit = 0; (1 << bit) <= ne; ++bit) {
-            const uint64_t set = __ballot((e >> bit) & 1);
-            same &= ((e >> bit) & 1) ? set : ~set;
+        const bool live = i < whi;
+        int x = live ? ids[i] : ne;
+        x = (unsigned)x < (unsigned)ne ? x : ne;
+        uint64_t same = __ballot(live);   // lanes with the same expert, by its bits
+        for (int bit = 0; bit < bits; ++bit) {
+            const bool mine = (x >> bit) & 1;
+            const uint64_t set = __ballot(mine);
+            same &= mine ? set : ~set;
         }
         const int rank = __popcll(same & ((1ull << lane) - 1));
-        int base = 0;
-        if (live) base = hist[e * PLAN_WAVES + wave];
-        if (live) order[base + rank] = i;
-        if (live && rank == 0) hist[e * PLAN_WAVES + wave] = base + __popcll(same);
+        if (live) {
+            const int base = s_at[x][wave];
+            order[base + rank] = i;
+            if (rank == 0) s_at[x][wave] = base + __popcll(same);
+        }
     }
 }
 
 int launch_plan(const int32_t *ids, int64_t nrows, int64_t ne, int32_t *plan, hipStream_t stream)
 {
-    int n = (int)nrows, e = (int)ne;
-    void *args[] = {&ids, &n, &e, &plan};
-    const hipError_t r = hipLaunchKernel(reinterpret_cast<const void *>(plan_kernel), dim3(1), dim3(PLAN_WAVES * 64),
-                                         args, (size_t)(ne + 1) * PLAN_WAVES * 4, stream);
-    return r == hipSuccess ? 0 : -3;
+    // shares of a multiple of PLAN_THREADS rows, at most PLAN_GROUPS of them
+    int64_t share = (nrows + PLAN_GROUPS - 1) / PLAN_GROUPS;
+    share = (share + PLAN_THREADS - 1) / PLAN_THREADS * PLAN_THREADS;
+    if (share == 0) share = PLAN_THREADS;
+    const int64_t groups = nrows > 0 ? (nrows + share - 1) / share : 1;
+    return launch_kernel(plan_kernel, dim3((unsigned)groups), dim3(PLAN_THREADS), stream, ids, (int)nrows, (int)ne,
+                         (int)share, plan);
 }
 
 // ---------------------------------------------------------------------------
 // the weighted sum
 // ---------------------------------------------------------------------------
-// y[t] = sum over s of w[t][s] h[t k + s], in fp32 and in the order of s.
+// y[t] = sum over s of w[t][s] h[t k + s], in fp32 and in the order of s.  A
+// thread owns V neighbouring outputs of one token and reads BATCH slots' values
+// before it adds them.  Bound by memory: 2630 tokens, k = 6, od = 3584, bf16
+// (132 MB) MEASURED_COMBINE.
 template <int TH, int TY>
 __global__ __launch_bounds__(256) void combine_kernel(const elem_t<TH> *__restrict__ h, int64_t ldh,
-                                                      const float *__restrict__ w, int k, int64_t od,
-                                                      elem_t<TY> *__restrict__ y, int64_t ldy)
+                                                      const float *__restrict__ w, int k, int64_t od, int64_t per,
+                                                      int64_t total, elem_t<TY> *__restrict__ y, int64_t ldy)
 {
-    const int64_t t = blockIdx.x;
-    for (int64_t j = threadIdx.x; j < od; j += 256) {
-        float v = 0.0f;
-        for (int s = 0; s < k; ++s) v += w[t * k + s] * (float)h[(t * k + s) * ldh + j];
-        y[t * ldy + j] = (elem_t<TY>)v;
+    constexpr int V = VEC<TH>, BATCH = 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const int64_t t = i / per, j = (i - t * per) * V;
+    const elem_t<TH> *row = h + t * k * ldh + j;
+    const float *wt = w + t * k;
+    elem_t<TY> *out = y + t * ldy + j;
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = 0.0f;
+    if (j + V <= od) {
+        int s = 0;
+        for (; s + BATCH <= k; s += BATCH) {
+            u32x4 r[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) r[b] = load16<TH>(row + (s + b) * ldh);
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                float f[V];
+                unpack16<TH>(r[b], f);
+                const float g = wt[s + b];
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] += g * f[e];
+            }
+        }
+        for (; s < k; ++s) {
+            float f[V];
+            unpack16<TH>(load16<TH>(row + s * ldh), f);
+            const float g = wt[s];
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += g * f[e];
+        }
+        if constexpr (VEC<TY> <= V) {
+#pragma unroll
+            for (int p = 0; p < V / VEC<TY>; ++p) {
+                float o[VEC<TY>];
+#pragma unroll
+                for (int e = 0; e < VEC<TY>; ++e) o[e] = v[p * VEC<TY> + e];
+                store16<TY>(out + p * VEC<TY>, pack16<TY>(o));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) out[e] = (elem_t<TY>)v[e];
+        }
+    } else {
+        for (int e = 0; j + e < od; ++e) {
+            float a = 0.0f;
+            for (int s = 0; s < k; ++s) a += wt[s] * (float)row[s * ldh + e];
+            out[e] = (elem_t<TY>)a;
+        }
     }
 }
 
@@ -258,8 +630,11 @@ template <int TH, int TY>
 static int combine(const void *h, int64_t ldh, const float *w, int64_t nt, int64_t k, int64_t od, void *y,
                    int64_t ldy, hipStream_t stream)
 {
-    return launch_kernel(combine_kernel<TH, TY>, dim3((unsigned)nt), dim3(256), stream,
-                         static_cast<const elem_t<TH> *>(h), ldh, w, (int)k, od, static_cast<elem_t<TY> *>(y), ldy);
+    const int64_t per = (od + VEC<TH> - 1) / VEC<TH>, total = nt * per, grid = (total + 255) / 256;
+    if (grid > 0x7fffffff) return -1;
+    return launch_kernel(combine_kernel<TH, TY>, dim3((unsigned)grid), dim3(256), stream,
+                         static_cast<const elem_t<TH> *>(h), ldh, w, (int)k, od, per, total,
+                         static_cast<elem_t<TY> *>(y), ldy);
 }
 
 template <int TH>
@@ -276,7 +651,6 @@ static int combine_to(const void *h, int64_t ldh, const float *w, int64_t nt, in
 int launch_combine(const void *h, int htype, int64_t ldh, const float *w, int64_t nt, int64_t k, int64_t od,
                    void *y, int ytype, int64_t ldy, hipStream_t stream)
 {
-    if (nt > 0x7fffffff) return -1;
     switch (htype) {
     case T_F32: return combine_to<T_F32>(h, ldh, w, nt, k, od, y, ytype, ldy, stream);
     case T_BF16: return combine_to<T_BF16>(h, ldh, w, nt, k, od, y, ytype, ldy, stream);

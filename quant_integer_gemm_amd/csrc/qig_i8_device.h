@@ -56,6 +56,21 @@ __device__ __forceinline__ u32x4 pack16(const float (&f)[VEC<T>])
     return v;
 }
 
+// The 16 bytes at any element's address: the hardware takes unaligned vector
+// accesses, so rows may start and step anywhere.
+template <int T>
+__device__ __forceinline__ u32x4 load16(const elem_t<T> *p)
+{
+    typedef u32x4 u32x4u __attribute__((aligned(2)));
+    return *reinterpret_cast<const u32x4u *>(p);
+}
+template <int T>
+__device__ __forceinline__ void store16(elem_t<T> *p, u32x4 v)
+{
+    typedef u32x4 u32x4u __attribute__((aligned(2)));
+    *reinterpret_cast<u32x4u *>(p) = v;
+}
+
 // a * sigmoid(a) * b in fp32 from the hardware's exp2 and reciprocal (each
 // within about an ulp): for a far below zero exp2 overflows and the
 // reciprocal of infinity gives the limit 0.
