@@ -27,6 +27,8 @@
 namespace qig {
 
 constexpr int BK = 128;
+// Bands of the tile order (tile_of).
+constexpr unsigned BAND = 8, EXPERT_BAND = 1;
 
 struct I8Args {
     const uint8_t *W, *q;
@@ -72,40 +74,58 @@ __device__ __forceinline__ void copy16_at(uint64_t addr, uint32_t lds)
                  : "memory");
 }
 
-// Workgroup -> tile.  Workgroups go round-robin over the eight XCDs, each with
-// its own L2: XCD x takes a contiguous run of the tile order, and the order
-// walks bands of BAND token tiles, band rows fastest, so that the tiles an XCD
-// works on at one time share both weight rows and tokens.
-constexpr unsigned BAND = 8;
-__device__ __forceinline__ void tile_of(unsigned b, int nbt, int nbj, int &mt, int &jt)
+// Tile i of the tile order: bands of BAND token tiles, the tiles of a band
+// fastest, so that the tiles in work at one time share both weight rows and
+// tokens.
+template <unsigned BAND>
+__device__ __forceinline__ void tile_of(unsigned i, unsigned nbt, unsigned nbj, int &mt, int &jt)
 {
-    const unsigned total = (unsigned)nbt * (unsigned)nbj, per = total / 8, rem = total % 8, x = b % 8;
-    const unsigned i = x * per + (x < rem ? x : rem) + b / 8;
-    const unsigned band = BAND * (unsigned)nbj;
+    const unsigned band = BAND * nbj;
     const unsigned bi = i / band, in = i - bi * band;
-    const unsigned left = (unsigned)nbt - bi * BAND, h = left < BAND ? left : BAND;
+    const unsigned left = nbt - bi * BAND, h = left < BAND ? left : BAND;
     jt = (int)(in / h);
     mt = (int)(bi * BAND + in % h);
 }
 
-// Which expert and rows a workgroup's token tile covers: tile number mt
-// counts the experts' tiles in order, the dropped rows' tiles last (e == ne).
+// Workgroup b's place in the order of `total` tiles.  Workgroups go round-robin
+// over the eight XCDs, each with its own L2: XCD x takes a contiguous run.
+// False: more workgroups than tiles, and this one has none.
+__device__ __forceinline__ bool place_of(unsigned b, unsigned total, unsigned &i)
+{
+    const unsigned per = total / 8, rem = total % 8, x = b % 8;
+    i = x * per + (x < rem ? x : rem) + b / 8;
+    return b / 8 < per + (x < rem);
+}
+
+// The experts' token tiles, counted in order, the dropped rows' tiles last
+// (expert ne).  One wave's lanes hold 64 experts at a time.
 struct Rows {
-    int e, first, count;   // expert, first position in the order, rows of the tile (0: no such tile)
+    int e, first, count;   // expert, first position in the order, rows of the tile
 };
 
+// Token tiles of all experts.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const int32_t *plan, int ne)
+{
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int e = lane; e <= ne; e += 64) n += (plan[e + 1] - plan[e] + BM - 1) / BM;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Token tile mt, which exists.
 template <int BM>
 __device__ __forceinline__ Rows find_rows(const int32_t *plan, int ne, int mt)
 {
     const int lane = threadIdx.x & 63;
+    Rows r = {0, 0, 0};
     int before = 0;
     for (int e0 = 0; e0 <= ne; e0 += 64) {
         const int e = e0 + lane;
-        int lo = 0, n = 0;
-        if (e <= ne) {
-            lo = plan[e];
-            n = plan[e + 1] - lo;
-        }
+        const int lo = e <= ne ? plan[e] : 0;
+        const int n = e <= ne ? plan[e + 1] - lo : 0;
         const int tiles = (n + BM - 1) / BM;
         int incl = tiles;
 #pragma unroll
@@ -117,17 +137,16 @@ __device__ __forceinline__ Rows find_rows(const int32_t *plan, int ne, int mt)
         const uint64_t hit = __ballot(mt >= excl && mt < excl + tiles);
         if (hit) {
             const int src = __ffsll((unsigned long long)hit) - 1;
-            const int m = mt - __shfl(excl, src);
-            Rows r;
+            const int m = mt - __builtin_amdgcn_readlane(excl, src);
             r.e = e0 + src;
-            r.first = __shfl(lo, src) + m * BM;
-            const int left = __shfl(n, src) - m * BM;
+            r.first = __builtin_amdgcn_readlane(lo, src) + m * BM;
+            const int left = __builtin_amdgcn_readlane(n, src) - m * BM;
             r.count = left < BM ? left : BM;
-            return r;
+            break;
         }
-        before += __shfl(incl, 63);
+        before += __builtin_amdgcn_readlane(incl, 63);
     }
-    return Rows{0, 0, 0};
+    return r;
 }
 
 // BM x BN tile, WM x WN waves, each BM/WM x BN/WN in 32 x 32 MFMA tiles.
@@ -138,15 +157,16 @@ template <int BM, int BN, int WM, int WN, int S, bool SPLIT, bool GLU, bool EXPE
 __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 {
     constexpr int NW = WM * WN;
-    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-    constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;   // 1 KB pieces a wave copies each step
+    constexpr int TMAX = BM / WM / 32, TN = BN / WN / 32;
+    constexpr int PAMAX = BM / 8 / NW, PB = BN / 8 / NW;   // 1 KB pieces a wave copies each step
     constexpr int STAGE = (BM + BN) * BK;
     constexpr int BJ = GLU ? BN / 2 : BN;               // outputs of a tile
-    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TM >= 1 && TN >= 1, "tile");
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TMAX >= 1 && TMAX <= 4 && TN >= 1, "tile");
     static_assert(S == 2 || S >= 4, "stages");
     static_assert(!GLU || TN % 2 == 0, "gate and up rows of an output in one wave");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S * STAGE];
     __shared__ float s_sq[BM];
+    __shared__ __attribute__((aligned(16))) float s_sw[BN], s_bias[BN];
     __shared__ int32_t s_row[EXPERTS ? BM : 1];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -157,7 +177,16 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         split = (int)(block % (unsigned)g.splits);
         block /= (unsigned)g.splits;
     }
-    tile_of(block, g.nbt, g.nbj, mt, jt);
+    if constexpr (EXPERTS) {
+        unsigned i;
+        const unsigned nbt = (unsigned)count_tiles<BM>(g.plan, g.ne);
+        if (!place_of(block, nbt * (unsigned)g.nbj, i)) return;
+        tile_of<EXPERT_BAND>(i, nbt, (unsigned)g.nbj, mt, jt);
+    } else {
+        unsigned i;
+        place_of(block, (unsigned)g.nbt * (unsigned)g.nbj, i);
+        tile_of<BAND>(i, (unsigned)g.nbt, (unsigned)g.nbj, mt, jt);
+    }
     const int64_t j0 = (int64_t)jt * BJ;
     const uint8_t *W = g.W;
     const float *sw = g.sw, *bias = g.bias;
@@ -167,7 +196,6 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 
     if constexpr (EXPERTS) {
         const Rows r = find_rows<BM>(g.plan, g.ne, mt);
-        if (r.count == 0) return;
         count = r.count;
         const int32_t *order = g.plan + g.ne + 2 + r.first;
         if (r.e == g.ne) {
@@ -193,15 +221,24 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         for (int i = tid; i < BM; i += NW * 64) s_sq[i] = g.sq[t0 + (i < count ? i : count - 1)];
     }
 
+    // scales and biases of the tile's weight rows, in the order of its LDS rows
+    for (int i = tid; i < BN; i += NW * 64) {
+        int64_t j = j0 + (GLU ? (i >> 6) * 32 + (i & 31) : i);
+        j = j < g.od ? j : g.od - 1;
+        if (GLU && (i & 32)) j += g.od;
+        s_sw[i] = sw[j];
+        s_bias[i] = bias ? bias[j] : 0.0f;
+    }
+
     // The rows that this lane copies: piece p of the wave holds rows
-    // 8 (PA wave + p) .. + 7, lane l row l / 8 and slot l % 8.
+    // 8 (NW p + wave) .. + 7, lane l row l / 8 and slot l % 8.
     const int lr = lane >> 3;
     const uint32_t gran = (uint32_t)((lane & 7) ^ lr);   // the granule that belongs in this lane's slot
-    uint32_t aoff[EXPERTS ? 1 : PA], boff[PB];
-    uint64_t aptr[EXPERTS ? PA : 1];
+    uint32_t aoff[EXPERTS ? 1 : PAMAX], boff[PB];
+    uint64_t aptr[EXPERTS ? PAMAX : 1];
 #pragma unroll
-    for (int p = 0; p < PA; ++p) {
-        const int r = 8 * (PA * wave + p) + lr;
+    for (int p = 0; p < PAMAX; ++p) {
+        const int r = 8 * (NW * p + wave) + lr;
         if constexpr (EXPERTS)
             aptr[p] = reinterpret_cast<uintptr_t>(g.q + (int64_t)(s_row[r] / g.slots) * g.ldq);
         else
@@ -214,9 +251,9 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     for (int p = 0; p < PB; ++p) {
         // a piece's eight rows lie in one block of 32, so gate or up is the
         // same for the whole piece
-        const int r = 8 * (PB * wave + p) + lr;
+        const int r = 8 * (NW * p + wave) + lr;
         int j = GLU ? (r >> 6) * 32 + (r & 31) : r;
-        bup[p] = GLU && ((8 * (PB * wave + p)) & 32) != 0;
+        bup[p] = GLU && ((8 * (NW * p + wave)) & 32) != 0;
         const int64_t last = g.od - 1 - j0;
         if (j > last) j = (int)last;
         boff[p] = (uint32_t)j * (uint32_t)g.ldw;
@@ -235,287 +272,341 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         if (kfirst + nk < all) tail = BK;
     }
 
-    // The stage that holds step kt.
-    auto buffer = [&](int kt) -> uint32_t {
-        if constexpr ((S & (S - 1)) == 0)
-            return (uint32_t)kt & (S - 1);
-        else
-            return (uint32_t)kt % S;
-    };
-    // Copy piece p of step kt: first the wave's PA pieces of the activations,
-    // then its PB pieces of the weights.
-    auto copy = [&](int kt, int p) {
-        const uint32_t dst = l0 + buffer(kt) * STAGE;
-        const uint64_t k0 = (uint64_t)(kfirst + kt) * BK;
-        uint32_t go = 16 * gran;
-        if (kt == nk - 1 && (int)go >= tail) go = 0;
-        if (p < PA) {
-            const uint32_t d = dst + 1024 * (PA * wave + p);
-            if constexpr (EXPERTS)
-                copy16_at(aptr[p] + k0 + go, d);
-            else
-                copy16(abase0 + k0, aoff[p] + go, d);
-        } else {
-            p -= PA;
-            copy16(bbase + k0 + (bup[p] ? uphalf : 0), boff[p] + go, dst + BM * BK + 1024 * (PB * wave + p));
-        }
-    };
-    // Step kt's bytes past id become zero in the activations' rows.
-    auto clear_tail = [&](uint8_t *st) {
-        for (int i = tid; i < BM * 8; i += NW * 64) {
-            const int r = i >> 3, slot = i & 7;
-            const int left = tail - 16 * (slot ^ (r & 7));   // valid bytes of the granule
-            if (left >= 16) continue;
-            u32x4 *p = reinterpret_cast<u32x4 *>(st + 16 * i);
-            u32x4 v = *p;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int b = left - 4 * w;
-                v[w] = b >= 4 ? v[w] : (b <= 0 ? 0u : v[w] & ((1u << (8 * b)) - 1u));
-            }
-            *p = v;
-        }
-        __syncthreads();
-    };
-
     const int wm = wave / WN, wn = wave % WN;
     const int lrow = lane & 31, lhalf = lane >> 5;
-    i32x16 acc[TM][TN];
-#pragma unroll
-    for (int m = 0; m < TM; ++m)
-#pragma unroll
-        for (int n = 0; n < TN; ++n)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[m][n][i] = 0;
 
-    // Chunk c of a step is 32 bytes of every row: granules 2 c and 2 c + 1.
-    // Rows of one lane differ by multiples of 32, so its slot is the same in
-    // all of them.
-    constexpr int NC = BK / 32;
-    uint32_t aat[NC], bat[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const uint32_t slot = 16 * ((2 * c + lhalf) ^ (lrow & 7));
-        aat[c] = (wm * TM * 32 + lrow) * BK + slot;
-        bat[c] = (BM + wn * TN * 32 + lrow) * BK + slot;
-    }
-    struct Frag {
-        i32x4 a[TM], b[TN];
-    } f[S == 2 ? 2 : NC];
-    auto read = [&](Frag &o, int kt, int c, int i) {
-        const uint8_t *st = lds + buffer(kt) * STAGE;
-        if (i < TN)
-            o.b[i] = *reinterpret_cast<const i32x4 *>(st + bat[c] + i * 32 * BK);
-        else
-            o.a[i - TN] = *reinterpret_cast<const i32x4 *>(st + aat[c] + (i - TN) * 32 * BK);
-    };
-    constexpr int NM = TM * TN, NR = TM + TN, NP = PA + PB, P3 = NP / 2;
-    // One chunk's MFMAs, in issue order, behind them the reads of the next
-    // chunk (chunk rc of step rk) one by one, and the copies [P0, P1) of step
-    // ck, evenly spread.
-    auto chunk = [&](auto reads, auto p0, auto p1, const Frag &o, Frag &nx, int rk, int rc, int ck) {
-        constexpr int P0 = p0, N = p1 - p0;
-#pragma unroll
-        for (int i = 0; i < NM; ++i) {
-            acc[i / TN][i % TN] = mfma_i8(o.a[i / TN], o.b[i % TN], acc[i / TN][i % TN]);
-            if constexpr (reads) {
-                if (i < NR) read(nx, rk, rc, i);
-                if (i == NM - 1)
-#pragma unroll
-                    for (int r = NM; r < NR; ++r) read(nx, rk, rc, r);
-            }
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (j * NM / (N > 0 ? N : 1) == i) copy(ck, P0 + j);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    constexpr std::integral_constant<int, 0> c0;
-    constexpr std::integral_constant<int, P3> cm;
-    constexpr std::integral_constant<int, NP> cn;
-    constexpr std::true_type yes;
-    constexpr std::false_type no;
-    // All but the copies of the last S - 2 steps issued have landed, and
-    // everybody's reads before this point are done.
-    auto landed = [&](auto all) {
-        if constexpr (all)
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * NP) : "memory");
-        __syncthreads();
-    };
-    // Step kt, its first chunk in f[0]: with it go the copies of step
-    // kt + S - 1 from piece P3 on (`late`), and, once step kt + 1 has landed
-    // and the stage of step kt - 1 + S is free of readers, those of step
-    // kt + S up to P3 (`early`).
-    auto step = [&](auto late, auto early, int kt) {
-        if constexpr (late)
-            chunk(yes, cm, cn, f[0], f[1], kt, 1, kt + S - 1);
-        else
-            chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
-#pragma unroll
-        for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
-        landed(std::bool_constant<!late>{});
-        if constexpr (early) {
-            chunk(yes, c0, cm, f[(NC - 1) & 1], f[0], kt + 1, 0, kt + S);
-        } else {
-            if (kt + 1 == nk - 1 && tail < BK) clear_tail(lds + buffer(kt + 1) * STAGE);
-            chunk(yes, c0, c0, f[(NC - 1) & 1], f[0], kt + 1, 0, 0);
-        }
-    };
-
-    if constexpr (S == 2) {
-#pragma unroll
-        for (int k = 0; k < S - 1; ++k)
-            if (k < nk)
-#pragma unroll
-                for (int p = 0; p < NP; ++p) copy(k, p);
-        if (nk >= S - 1)
-            landed(no);
-        else
-            landed(yes);
-        if (nk == 1 && tail < BK) clear_tail(lds);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) read(f[0], 0, 0, i);
-        int kt = 0;
-        if (nk >= S) {
-#pragma unroll
-            for (int p = 0; p < P3; ++p) copy(S - 1, p);
-            for (; kt < nk - S; ++kt) step(yes, yes, kt);
-            step(yes, no, kt++);
-        }
-        for (; kt < nk - 1; ++kt) step(no, no, kt);
-        chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
-#pragma unroll
-        for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
-        chunk(no, c0, c0, f[(NC - 1) & 1], f[0], 0, 0, 0);
-    } else {
-        // Body kt multiplies step kt, held in registers, and reads step
-        // kt + 1 chunk by chunk into the registers as they come free, so
-        // nearly a whole step lies between a read and its use; it copies step
-        // kt + S - 1 into the stage of step kt - 1, whose reads every wave
-        // has used by then.
-        auto body = [&](auto copies, int kt) {
-            constexpr int N = copies ? NP : 0;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int i = 0; i < NM; ++i) {
-                    acc[i / TN][i % TN] = mfma_i8(f[c].a[i / TN], f[c].b[i % TN], acc[i / TN][i % TN]);
-#pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (i == NM - 1) read(f[c], kt + 1, c, r);
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (j * NM * NC / N == c * NM + i) copy(kt + S - 1, j);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            if constexpr (copies)
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
+    // The tile with TM x 32 of every wave's rows: only as many as have tokens
+    // (the last tile of the tokens, or of an expert's rows, is mostly smaller).
+    auto run = [&](auto frags) {
+        constexpr int TM = frags;
+        constexpr int PA = TM * WM * 32 / 8 / NW;   // pieces of the activations a wave copies
+        static_assert(PA * 8 * NW == TM * WM * 32, "whole pieces");
+        // The stage that holds step kt.
+        auto buffer = [&](int kt) -> uint32_t {
+            if constexpr ((S & (S - 1)) == 0)
+                return (uint32_t)kt & (S - 1);
             else
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
+                return (uint32_t)kt % S;
         };
+        // Copy piece p of step kt: first the wave's PA pieces of the activations,
+        // then its PB pieces of the weights.
+        auto copy = [&](int kt, int p) {
+            const uint32_t dst = l0 + buffer(kt) * STAGE;
+            const uint64_t k0 = (uint64_t)(kfirst + kt) * BK;
+            uint32_t go = 16 * gran;
+            if (kt == nk - 1 && (int)go >= tail) go = 0;
+            if (p < PA) {
+                const uint32_t d = dst + 1024 * (NW * p + wave);
+                if constexpr (EXPERTS)
+                    copy16_at(aptr[p] + k0 + go, d);
+                else
+                    copy16(abase0 + k0, aoff[p] + go, d);
+            } else {
+                p -= PA;
+                copy16(bbase + k0 + (bup[p] ? uphalf : 0), boff[p] + go, dst + BM * BK + 1024 * (NW * p + wave));
+            }
+        };
+        // Step kt's bytes past id become zero in the activations' rows.
+        auto clear_tail = [&](uint8_t *st) {
+            for (int i = tid; i < TM * WM * 32 * 8; i += NW * 64) {
+                const int r = i >> 3, slot = i & 7;
+                const int left = tail - 16 * (slot ^ (r & 7));   // valid bytes of the granule
+                if (left >= 16) continue;
+                u32x4 *p = reinterpret_cast<u32x4 *>(st + 16 * i);
+                u32x4 v = *p;
 #pragma unroll
-        for (int k = 0; k < S - 1; ++k)
-            if (k < nk)
-#pragma unroll
-                for (int p = 0; p < NP; ++p) copy(k, p);
-        if (nk >= S - 1)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (nk <= 2 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) read(f[c], 0, c, r);
-        int kt = 0;
-        for (; kt <= nk - S; ++kt) body(yes, kt);
-        for (; kt < nk - 1; ++kt) {
-            body(no, kt);
-            if (kt + 2 == nk - 1 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int i = 0; i < NM; ++i)
-                acc[i / TN][i % TN] = mfma_i8(f[c].a[i / TN], f[c].b[i % TN], acc[i / TN][i % TN]);
-    }
+                for (int w = 0; w < 4; ++w) {
+                    const int b = left - 4 * w;
+                    v[w] = b >= 4 ? v[w] : (b <= 0 ? 0u : v[w] & ((1u << (8 * b)) - 1u));
+                }
+                *p = v;
+            }
+            __syncthreads();
+        };
 
-    if constexpr (SPLIT) {
-        // Every share leaves its sums in its slot; the last to arrive at the
-        // tile adds the others' to its own (integers: in any order the same)
-        // and finishes.  Slots and counter go through agent-scope accesses:
-        // the shares run on XCDs whose L2s are not coherent.
-        constexpr int LANES = NW * 64;
-        const int tile = (int)(blockIdx.x / (unsigned)g.splits);
-        int32_t *slot = g.part + (int64_t)tile * g.splits * (BM * BN);
-        int32_t *mine = slot + (int64_t)split * (BM * BN) + tid;
+        i32x16 acc[TM][TN];
 #pragma unroll
         for (int m = 0; m < TM; ++m)
 #pragma unroll
             for (int n = 0; n < TN; ++n)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    __hip_atomic_store(mine + ((m * TN + n) * 16 + i) * LANES, acc[m][n][i], __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the sums are at the coherence point
-        __syncthreads();
-        __shared__ uint32_t s_before;
-        if (tid == 0) s_before = __hip_atomic_fetch_add(g.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (s_before != (uint32_t)g.splits - 1) return;
-        for (int o = 0; o < g.splits; ++o) {
-            if (o == split) continue;
-            int32_t *other = slot + (int64_t)o * (BM * BN) + tid;
+                for (int i = 0; i < 16; ++i) acc[m][n][i] = 0;
+
+        // Chunk c of a step is 32 bytes of every row: granules 2 c and 2 c + 1.
+        // Rows of one lane differ by multiples of 32, so its slot is the same in
+        // all of them.
+        constexpr int NC = BK / 32;
+        uint32_t aat[NC], bat[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const uint32_t slot = 16 * ((2 * c + lhalf) ^ (lrow & 7));
+            aat[c] = (wm * TM * 32 + lrow) * BK + slot;
+            bat[c] = (BM + wn * TN * 32 + lrow) * BK + slot;
+        }
+        struct Frag {
+            i32x4 a[TM], b[TN];
+        } f[S == 2 ? 2 : NC];
+        auto read = [&](Frag &o, int kt, int c, int i) {
+            const uint8_t *st = lds + buffer(kt) * STAGE;
+            if (i < TN)
+                o.b[i] = *reinterpret_cast<const i32x4 *>(st + bat[c] + i * 32 * BK);
+            else
+                o.a[i - TN] = *reinterpret_cast<const i32x4 *>(st + aat[c] + (i - TN) * 32 * BK);
+        };
+        constexpr int NM = TM * TN, NR = TM + TN, NP = PA + PB, P3 = NP / 2;
+        // One chunk's MFMAs, in issue order, behind them the reads of the next
+        // chunk (chunk rc of step rk) one by one, and the copies [P0, P1) of step
+        // ck, evenly spread.
+        auto chunk = [&](auto reads, auto p0, auto p1, const Frag &o, Frag &nx, int rk, int rc, int ck) {
+            constexpr int P0 = p0, N = p1 - p0;
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                acc[i / TN][i % TN] = mfma_i8(o.b[i % TN], o.a[i / TN], acc[i / TN][i % TN]);
+                if constexpr (reads) {
+                    if (i < NR) read(nx, rk, rc, i);
+                    if (i == NM - 1)
+#pragma unroll
+                        for (int r = NM; r < NR; ++r) read(nx, rk, rc, r);
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j * NM / (N > 0 ? N : 1) == i) copy(ck, P0 + j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        constexpr std::integral_constant<int, 0> c0;
+        constexpr std::integral_constant<int, P3> cm;
+        constexpr std::integral_constant<int, NP> cn;
+        constexpr std::true_type yes;
+        constexpr std::false_type no;
+        // All but the copies of the last S - 2 steps issued have landed, and
+        // everybody's reads before this point are done.
+        auto landed = [&](auto all) {
+            if constexpr (all)
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * NP) : "memory");
+            __syncthreads();
+        };
+        // Step kt, its first chunk in f[0]: with it go the copies of step
+        // kt + S - 1 from piece P3 on (`late`), and, once step kt + 1 has landed
+        // and the stage of step kt - 1 + S is free of readers, those of step
+        // kt + S up to P3 (`early`).
+        auto step = [&](auto late, auto early, int kt) {
+            if constexpr (late)
+                chunk(yes, cm, cn, f[0], f[1], kt, 1, kt + S - 1);
+            else
+                chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
+#pragma unroll
+            for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
+            landed(std::bool_constant<!late>{});
+            if constexpr (early) {
+                chunk(yes, c0, cm, f[(NC - 1) & 1], f[0], kt + 1, 0, kt + S);
+            } else {
+                if (kt + 1 == nk - 1 && tail < BK) clear_tail(lds + buffer(kt + 1) * STAGE);
+                chunk(yes, c0, c0, f[(NC - 1) & 1], f[0], kt + 1, 0, 0);
+            }
+        };
+
+        if constexpr (S == 2) {
+#pragma unroll
+            for (int k = 0; k < S - 1; ++k)
+                if (k < nk)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) copy(k, p);
+            if (nk >= S - 1)
+                landed(no);
+            else
+                landed(yes);
+            if (nk == 1 && tail < BK) clear_tail(lds);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) read(f[0], 0, 0, i);
+            int kt = 0;
+            if (nk >= S) {
+#pragma unroll
+                for (int p = 0; p < P3; ++p) copy(S - 1, p);
+                for (; kt < nk - S; ++kt) step(yes, yes, kt);
+                step(yes, no, kt++);
+            }
+            for (; kt < nk - 1; ++kt) step(no, no, kt);
+            chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
+#pragma unroll
+            for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
+            chunk(no, c0, c0, f[(NC - 1) & 1], f[0], 0, 0, 0);
+        } else {
+            // Body kt multiplies step kt, held in registers, and reads step
+            // kt + 1 chunk by chunk into the registers as they come free, so
+            // nearly a whole step lies between a read and its use; it copies step
+            // kt + S - 1 into the stage of step kt - 1, whose reads every wave
+            // has used by then.
+            auto body = [&](auto copies, int kt) {
+                constexpr int N = copies ? NP : 0;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int i = 0; i < NM; ++i) {
+                        acc[i / TN][i % TN] = mfma_i8(f[c].b[i % TN], f[c].a[i / TN], acc[i / TN][i % TN]);
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+                            if (i == NM - 1) read(f[c], kt + 1, c, r);
+#pragma unroll
+                        for (int j = 0; j < N; ++j)
+                            if (j * NM * NC / N == c * NM + i) copy(kt + S - 1, j);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                if constexpr (copies)
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            };
+#pragma unroll
+            for (int k = 0; k < S - 1; ++k)
+                if (k < nk)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) copy(k, p);
+            if (nk >= S - 1)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (nk <= 2 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) read(f[c], 0, c, r);
+            int kt = 0;
+            for (; kt <= nk - S; ++kt) body(yes, kt);
+            for (; kt < nk - 1; ++kt) {
+                body(no, kt);
+                if (kt + 2 == nk - 1 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < NM; ++i)
+                    acc[i / TN][i % TN] = mfma_i8(f[c].b[i % TN], f[c].a[i / TN], acc[i / TN][i % TN]);
+        }
+
+        if constexpr (SPLIT) {
+            // Every share leaves its sums in its slot; the last to arrive at the
+            // tile adds the others' to its own (integers: in any order the same)
+            // and finishes.  Slots and counter go through agent-scope accesses:
+            // the shares run on XCDs whose L2s are not coherent.
+            constexpr int LANES = NW * 64;
+            const int tile = (int)(blockIdx.x / (unsigned)g.splits);
+            int32_t *slot = g.part + (int64_t)tile * g.splits * (BM * BN);
+            int32_t *mine = slot + (int64_t)split * (BM * BN) + tid;
 #pragma unroll
             for (int m = 0; m < TM; ++m)
 #pragma unroll
                 for (int n = 0; n < TN; ++n)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[m][n][i] += __hip_atomic_load(other + ((m * TN + n) * 16 + i) * LANES, __ATOMIC_RELAXED,
-                                                          __HIP_MEMORY_SCOPE_AGENT);
+                        __hip_atomic_store(mine + ((m * TN + n) * 16 + i) * LANES, acc[m][n][i], __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the sums are at the coherence point
+            __syncthreads();
+            __shared__ uint32_t s_before;
+            if (tid == 0) s_before = __hip_atomic_fetch_add(g.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (s_before != (uint32_t)g.splits - 1) return;
+            for (int o = 0; o < g.splits; ++o) {
+                if (o == split) continue;
+                int32_t *other = slot + (int64_t)o * (BM * BN) + tid;
+#pragma unroll
+                for (int m = 0; m < TM; ++m)
+#pragma unroll
+                    for (int n = 0; n < TN; ++n)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[m][n][i] += __hip_atomic_load(other + ((m * TN + n) * 16 + i) * LANES, __ATOMIC_RELAXED,
+                                                              __HIP_MEMORY_SCOPE_AGENT);
+            }
+            if (tid == 0) __hip_atomic_store(g.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (tid == 0) __hip_atomic_store(g.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
 
-    // Lane l, register i: token 8 (i / 4) + 4 (l / 32) + i % 4, weight row l % 32.
-    constexpr int NO = GLU ? TN / 2 : TN;
+        // The weights are the rows of the result: lane l, register i holds token
+        // l % 32 and weight row 8 (i / 4) + 4 (l / 32) + i % 4, so four neighbouring
+        // registers are four neighbouring outputs of one token.  Every wave turns
+        // 32 tokens at a time through its own part of the stages' LDS, so that its
+        // stores are whole rows of 64 to 256 bytes (stored straight from the
+        // registers, 16 bytes a row, fp32 outputs cost 12% of the time at 8192^3).
+        constexpr int NO = GLU ? TN / 2 : TN;
+        constexpr int EB = YT == T_F32 ? 4 : 2;            // bytes of an output
+        constexpr int PITCH = NO * 32 * EB + 16;           // 16 more: the rows' writes on different banks
+        constexpr int CH = NO * 32 * EB / 16;              // 16-byte chunks a row
+        constexpr int PER = 16 / EB;                       // outputs of a chunk
+        static_assert(NW * 32 * PITCH <= S * STAGE, "the waves' parts");
+        __syncthreads();   // nobody reads the stages any more
+        uint8_t *mine = lds + wave * (32 * PITCH);
+        const int64_t jw = j0 + wn * NO * 32;
 #pragma unroll
-    for (int n = 0; n < NO; ++n) {
-        const int64_t j = j0 + (wn * NO + n) * 32 + lrow;
-        const bool jok = j < g.od;
-        const int64_t jc = jok ? j : 0;
-        const float w0 = sw[jc], b0 = bias ? bias[jc] : 0.0f;
-        float w1 = 0.0f, b1 = 0.0f;
-        if constexpr (GLU) {
-            w1 = sw[g.od + jc];
-            b1 = bias ? bias[g.od + jc] : 0.0f;
-        }
+        for (int m = 0; m < TM; ++m) {
+            const int r0 = (wm * TM + m) * 32;
+            const float s = s_sq[r0 + lrow];
 #pragma unroll
-        for (int m = 0; m < TM; ++m)
+            for (int n = 0; n < NO; ++n)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int r = (wm * TM + m) * 32 + mfma_row(i, lhalf);
-                const float s = s_sq[r];
-                float v;
-                if constexpr (GLU) {
-                    const float a = (float)acc[m][2 * n][i] * s * w0 + b0;
-                    const float b = (float)acc[m][2 * n + 1][i] * s * w1 + b1;
-                    v = silu_mul(a, b);
-                } else {
-                    v = (float)acc[m][n][i] * s * w0 + b0;
+                for (int q = 0; q < 4; ++q) {
+                    const int o = 8 * q + 4 * lhalf;   // outputs o .. o + 3 of the 32
+                    const int at = GLU ? (wn * NO + n) * 64 + o : (wn * NO + n) * 32 + o;
+                    const f32x4 w = *reinterpret_cast<const f32x4 *>(s_sw + at);
+                    const f32x4 b = *reinterpret_cast<const f32x4 *>(s_bias + at);
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (GLU) {
+                            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(s_sw + at + 32);
+                            const f32x4 b1 = *reinterpret_cast<const f32x4 *>(s_bias + at + 32);
+                            const float ga = (float)acc[m][2 * n][4 * q + i] * s * w[i] + b[i];
+                            const float up = (float)acc[m][2 * n + 1][4 * q + i] * s * w1[i] + b1[i];
+                            v[i] = silu_mul(ga, up);
+                        } else {
+                            v[i] = (float)acc[m][n][4 * q + i] * s * w[i] + b[i];
+                        }
+                    }
+                    uint8_t *to = mine + lrow * PITCH + (n * 32 + o) * EB;
+                    if constexpr (EB == 4) {
+                        *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
+                    } else {
+                        typedef elem_t<YT> four __attribute__((ext_vector_type(4)));
+                        *reinterpret_cast<four *>(to) =
+                            four{(elem_t<YT>)v[0], (elem_t<YT>)v[1], (elem_t<YT>)v[2], (elem_t<YT>)v[3]};
+                    }
                 }
-                if (r < count && jok) {
-                    const int64_t row = EXPERTS ? (int64_t)s_row[r] : t0 + r;
-                    y[row * g.ldy + j] = (elem_t<YT>)v;
+#pragma unroll
+            for (int c = 0; c < CH / 2; ++c) {
+                const int i = c * 64 + lane, row = i / CH, ch = i % CH;
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(mine + row * PITCH + 16 * ch);
+                const int r = r0 + row;
+                const int64_t j = jw + ch * PER;
+                if (r >= count || j >= g.od) continue;
+                elem_t<YT> *out = y + (EXPERTS ? (int64_t)s_row[r] : t0 + r) * g.ldy + j;
+                if (j + PER <= g.od) {
+                    store16<YT>(out, v);
+                } else {
+                    const int left = (int)(g.od - j);
+#pragma unroll
+                    for (int i = 0; i < PER - 1; ++i) {
+                        if (i >= left) break;
+                        if constexpr (EB == 4)
+                            out[i] = __builtin_bit_cast(float, (uint32_t)v[i]);
+                        else
+                            out[i] = __builtin_bit_cast(elem_t<YT>, (uint16_t)(v[i / 2] >> (16 * (i & 1))));
+                    }
                 }
             }
-    }
+        }
+    };
+    if constexpr (TMAX >= 2)
+        if (count <= WM * 32) return run(std::integral_constant<int, 1>{});
+    if constexpr (TMAX >= 3)
+        if (count <= WM * 64) return run(std::integral_constant<int, 2>{});
+    if constexpr (TMAX >= 4)
+        if (count <= WM * 96) return run(std::integral_constant<int, 3>{});
+    run(std::integral_constant<int, TMAX>{});
 }
 
 // ---------------------------------------------------------------------------
@@ -544,6 +635,8 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int jt = (int)(blockIdx.x % (unsigned)g.nbj), mt = (int)(blockIdx.x / (unsigned)g.nbj);
+    if constexpr (EXPERTS)
+        if (mt >= count_tiles<BM>(g.plan, g.ne)) return;
     const int64_t j0 = (int64_t)jt * GEMV_ROWS;
     const uint8_t *W = g.W;
     const float *sw = g.sw, *bias = g.bias;
@@ -552,7 +645,6 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
     elem_t<YT> *y = static_cast<elem_t<YT> *>(g.y);
     if constexpr (EXPERTS) {
         const Rows r = find_rows<BM>(g.plan, g.ne, mt);
-        if (r.count == 0) return;
         count = r.count;
         const int32_t *order = g.plan + g.ne + 2 + r.first;
         if (r.e == g.ne) {
@@ -695,73 +787,97 @@ static int launch_tile(I8Args a, int64_t od, int64_t nt, hipStream_t stream)
                          dim3(WM * WN * 64), stream, a);
 }
 
-// What a tile shape costs, in us per 128-byte step of one tile.  `alone`: a
-// round of tiles (one a CU; two for 128 x 128) whose CUs are not all busy;
-// `full`: a CU's share when all are, where the card's power holds the clock
-// down (1.75 GHz measured under the 256 x 256 tiles against 2.4).  Measured at
-// 8192^3 (full) and at 3584 x 18944 with 2630 tokens (alone).
+// What a tile shape costs, in us per 128-byte step of one tile: `alone` in a
+// round of tiles that leaves CUs without one, `full` as a CU's share when all
+// are busy, where the card's power holds the clock down (1.75 GHz under the
+// 256 x 256 tiles against 2.4); `ends` are a round's first loads and epilogue.
+// Measured at 8192^3 (full), 2630 tokens of 18944 -> 3584 and 64 to 512 tokens
+// of 3584 -> 3584 (alone).
 struct TileCost {
     int bm, bn, per_cu;
-    double alone, full, ends;   // ends: first loads and epilogue of a round, us
+    double alone, full, ends;
 };
-constexpr TileCost COST_256 = {256, 256, 1, 1.25, 1.9, 8.0};
-constexpr TileCost COST_192 = {192, 256, 1, 0.95, 1.48, 7.0};
-constexpr TileCost COST_64 = {64, 128, 1, 0.30, 0.36, 6.0};
+constexpr TileCost COST_256 = {256, 256, 1, 1.14, 1.72, 6.0};
+constexpr TileCost COST_192 = {192, 256, 1, 0.86, 1.34, 5.0};
+constexpr TileCost COST_64 = {64, 128, 1, 0.31, 0.33, 3.0};
+constexpr TileCost COST_64S = {64, 128, 3, 0.54, 0.33, 3.0};   // two stages: three workgroups a CU
 
-template <bool GLU, bool EXPERTS>
+template <bool GLU>
 static double cost(const TileCost &c, const I8Args &a)
 {
-    const double nbj = (double)((a.od + (GLU ? c.bn / 2 : c.bn) - 1) / (GLU ? c.bn / 2 : c.bn));
-    // experts: half a tile lost in each that has rows
-    const double nbt = EXPERTS ? (double)a.nt / c.bm + 0.5 * (double)(a.nt < a.ne ? a.nt : a.ne)
-                               : (double)((a.nt + c.bm - 1) / c.bm);
-    const double tiles = nbt * nbj, rounds = __builtin_ceil(tiles / (256.0 * c.per_cu));
-    const double nk = (double)((a.id + BK - 1) / BK);
+    const int64_t bj = GLU ? c.bn / 2 : c.bn;
+    const double tiles = (double)((a.od + bj - 1) / bj) * (double)((a.nt + c.bm - 1) / c.bm);
+    const double rounds = __builtin_ceil(tiles / (256.0 * c.per_cu));
     const double busy = tiles / 256.0 * c.full, alone = rounds * c.alone;
-    return nk * (busy > alone ? busy : alone) + rounds * c.ends;
+    return (double)((a.id + BK - 1) / BK) * (busy > alone ? busy : alone) + rounds * c.ends;
 }
 
-// Bytes of weights (times passes over them) up to which the few-token kernel
-// is taken whatever the number of tokens: at 12.8 MB (3584 x 3584) it measured
-// 7.7 us against the tiles' 13 us at 16 tokens and level with them at 64; at
-// 68 MB and 32 tokens 37 us against 24 us.
+// The few-token kernel is taken for up to 16 tokens, and up to this many bytes
+// of weights (times passes over them) for up to 64: 3584 x 3584 with 16 tokens
+// 7.5 us against the tiles' 11 us, level with them at 64 tokens; at 68 MB and 32
+// tokens 38 us against 21 us.
 constexpr int64_t GEMV_BYTES = int64_t(40) << 20;
+// For experts: weights of the experts that have rows, and rows of each.  Above
+// it tiles keep more of the weights' loads in flight: 12 experts' 4736 x 3584
+// with one row each 41 us against 33 us, but 6 experts' 1000 x 2000 8 us against
+// 12 us.
+constexpr int64_t EXPERTS_GEMV_BYTES = int64_t(24) << 20, EXPERTS_GEMV_ROWS = 16;
+// Rows of an expert, on average, from which the larger tiles are faster, and
+// the tiles it takes for that.  64 experts' 4736 x 3584, us for 64 x 128,
+// 128 x 128 and 256 x 256: 1.5 rows each 144, 147, 163; 12 rows 204, 200, 216;
+// 48 rows 221, 216, 229; 246 rows 610, 509, 438.
+constexpr double ROWS_128 = 8, ROWS_256 = 96, TILES_128 = 256, TILES_256 = 192;
 // Split sums: shares of at least SPLIT_STEPS steps, a workgroup a CU, and at
 // most SPLIT_MOST shares: the last share to arrive reads the others' sums one
-// after the other (18944 -> 3584, 32 tokens: 48 us whole, 24 us in four, 28 us
+// after the other (18944 -> 3584, 32 tokens: 45 us whole, 21 us in four, 28 us
 // in nine).  SPLIT_SLOTS and SPLIT_TILES are what the workspace holds.
 constexpr int SPLIT_STEPS = 16, SPLIT_MOST = 4, SPLIT_SLOTS = 1024, SPLIT_TILES = 4096, SPLIT_CUS = 256;
 
-template <bool GLU, bool EXPERTS, int YT>
-static int pick(I8Args a, hipStream_t stream)
+template <bool GLU, int YT>
+static int pick_dense(I8Args a, hipStream_t stream)
 {
     const int64_t wbytes = (GLU ? 2 : 1) * a.od * (int64_t)a.id;
-    if (EXPERTS ? a.nt <= 10 * (int64_t)a.ne
-                : a.nt <= 16 || (a.nt <= 64 && (a.nt + 15) / 16 * wbytes <= GEMV_BYTES))
-        return launch_gemv<GLU, EXPERTS, YT>(a, stream);
-    const double c256 = cost<GLU, EXPERTS>(COST_256, a), c192 = cost<GLU, EXPERTS>(COST_192, a);
-    const double c64 = cost<GLU, EXPERTS>(COST_64, a);
-    if (c64 < c256 && c64 < c192) {
-        if constexpr (!EXPERTS) {
-            const int64_t tiles = (a.nt + 63) / 64 * ((a.od + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
-            const int64_t nk = (a.id + BK - 1) / BK;
-            const int64_t splits = std::min<int64_t>(std::min<int64_t>(nk / SPLIT_STEPS, SPLIT_MOST), SPLIT_CUS / tiles);
-            if (a.part && splits >= 2 && tiles * splits <= SPLIT_SLOTS && tiles <= SPLIT_TILES) {
-                a.splits = (int)splits;
-                return launch_tile<64, 128, 2, 2, 4, true, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
-            }
-        }
-        return launch_tile<64, 128, 2, 2, 4, false, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
+    if (a.nt <= 16 || (a.nt <= 64 && (a.nt + 15) / 16 * wbytes <= GEMV_BYTES))
+        return launch_gemv<GLU, false, YT>(a, stream);
+    const double c256 = cost<GLU>(COST_256, a), c192 = cost<GLU>(COST_192, a);
+    const double c64 = cost<GLU>(COST_64, a), c64s = cost<GLU>(COST_64S, a);
+    if (std::min(c64, c64s) >= std::min(c192, c256)) {
+        if (c192 < c256) return launch_tile<192, 256, 2, 4, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
+        return launch_tile<256, 256, 2, 4, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
     }
-    if (c192 < c256) return launch_tile<192, 256, 2, 4, 2, false, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
-    return launch_tile<256, 256, 2, 4, 2, false, GLU, EXPERTS, YT>(a, a.od, a.nt, stream);
+    if (c64s < c64) return launch_tile<64, 128, 2, 2, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    const int64_t tiles = (a.nt + 63) / 64 * ((a.od + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
+    const int64_t nk = (a.id + BK - 1) / BK;
+    const int64_t splits = std::min<int64_t>(std::min<int64_t>(nk / SPLIT_STEPS, SPLIT_MOST), SPLIT_CUS / tiles);
+    if (a.part && splits >= 2 && tiles * splits <= SPLIT_SLOTS && tiles <= SPLIT_TILES) {
+        a.splits = (int)splits;
+        return launch_tile<64, 128, 2, 2, 4, true, GLU, false, YT>(a, a.od, a.nt, stream);
+    }
+    return launch_tile<64, 128, 2, 2, 4, false, GLU, false, YT>(a, a.od, a.nt, stream);
+}
+
+template <bool GLU, int YT>
+static int pick_experts(const I8Args &a, hipStream_t stream)
+{
+    const int64_t used = a.nt < a.ne ? a.nt : a.ne, rows = (GLU ? 2 : 1) * a.od;
+    const double each = (double)a.nt / (double)used;
+    if (each <= EXPERTS_GEMV_ROWS && used * rows * a.id <= EXPERTS_GEMV_BYTES)
+        return launch_gemv<GLU, true, YT>(a, stream);
+    auto tiles = [&](int bm, int bn) {   // half a tile lost in each expert
+        return ((double)a.nt / bm + 0.5 * (double)used) * (double)((rows + bn - 1) / bn);
+    };
+    if (each >= ROWS_256 && tiles(256, 256) >= TILES_256)
+        return launch_tile<256, 256, 2, 4, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    if (each >= ROWS_128 && tiles(128, 128) >= TILES_128)
+        return launch_tile<128, 128, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    return launch_tile<64, 128, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
 }
 
 template <int YT>
 static int pick_form(const I8Args &a, bool glu, hipStream_t stream)
 {
-    if (a.plan) return glu ? pick<true, true, YT>(a, stream) : pick<false, true, YT>(a, stream);
-    return glu ? pick<true, false, YT>(a, stream) : pick<false, false, YT>(a, stream);
+    if (a.plan) return glu ? pick_experts<true, YT>(a, stream) : pick_experts<false, YT>(a, stream);
+    return glu ? pick_dense<true, YT>(a, stream) : pick_dense<false, YT>(a, stream);
 }
 
 int launch_i8_gemm(const I8Gemm &g, hipStream_t stream)
