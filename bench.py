@@ -58,11 +58,13 @@ def parse():
     # clocks and measured up to ~10% slow, depending on what ran first
     p.add_argument("--warmup", type=int, default=300)
     p.add_argument("--no-cpu-baseline", action="store_true")
-    p.add_argument("--workload", choices=["proj", "ffn", "layer", "layer_q6v", "down", "kv"], default="proj",
+    p.add_argument("--workload", choices=["proj", "ffn", "layer", "layer_q6v", "down", "kv", "ffn_i8", "experts"], default="proj",
                    help="proj: the q4_K and q6_K 3584x3584 nt=512 GEMMs (the headline); ffn: the 7B-class "
                         "FFN GEMMs at nt=512; layer: all seven GEMMs of a 7B-class layer at nt=2630; down: "
                         "the layer's q6_K down projection alone (3584x18944, nt=2630); kv: the layer's k and v "
-                        "projections; layer_q6v: the layer with a q6_K v projection")
+                        "projections; layer_q6v: the layer with a q6_K v projection; ffn_i8: the layer's FFN at "
+                        "nt=2630 in int8 with scales per token and channel; experts: the same FFN as 64 experts of "
+                        "an eighth of its width, six a token, routing included")
     p.add_argument("--activations", choices=["tiled", "pad40"], default="tiled",
                    help="ffn / layer workloads: activation plane of the timed step")
     p.add_argument("--copy-calibration", action="store_true",
@@ -542,6 +544,93 @@ def run_gemm_set(args):
     print(json.dumps(out), flush=True)
 
 
+def run_int8(args):
+    """The int8 FFN workloads at nt=2630, bf16 activations, synthetic weights:
+    ffn_i8: the gated product (gate and up rows 2 x 18944 x 3584), its outputs
+    quantized, the down product; experts: softmax routing of each token to six
+    of 64 experts of 2368 hidden values, the plan, both grouped products and
+    the weighted sum.  Every call of the step is also timed alone."""
+    import torch
+    import quant_integer_gemm_amd as qig
+    dev = torch.device("cuda:0")
+    nt, id_ = 2630, 3584
+    g = torch.Generator(device=dev).manual_seed(SEED4)
+
+    def weights(shape):
+        w = torch.randn(shape, generator=g, device=dev).mul_(36).round_().clamp_(-127, 127).to(torch.int8)
+        return w, torch.rand(shape[:-1], generator=g, device=dev).add_(0.5) / (36 * shape[-1] ** 0.5)
+
+    x = torch.randn((nt, id_), generator=g, device=dev).bfloat16()
+    qx = torch.empty((nt, id_), dtype=torch.int8, device=dev)
+    sx = torch.empty(nt, device=dev)
+    experts = args.workload == "experts"
+    ne, k, ff = (64, 6, 2368) if experts else (1, 1, 18944)
+    rows = nt * k
+    W1, s1 = weights((ne, 2 * ff, id_))
+    W2, s2 = weights((ne, id_, ff))
+    h = torch.empty((rows, ff), dtype=torch.bfloat16, device=dev)
+    qh = torch.empty((rows, ff), dtype=torch.int8, device=dev)
+    sh = torch.empty(rows, device=dev)
+    y = torch.empty((nt, id_), dtype=torch.bfloat16, device=dev)
+    calls = {"quantize_x": lambda: qig.quantize_i8(x, q=qx, s=sx)}
+    if experts:
+        logits = torch.randn((nt, ne), generator=g, device=dev) * 1.5
+        ids = torch.empty((nt, k), dtype=torch.int32, device=dev)
+        rw = torch.empty((nt, k), device=dev)
+        plan = torch.empty(qig.expert_plan_bytes(rows, ne) // 4, dtype=torch.int32, device=dev)
+        o = torch.empty((rows, id_), dtype=torch.bfloat16, device=dev)
+        calls["route_experts"] = lambda: qig.route_experts(logits, k, ids=ids, w=rw)
+        calls["plan_experts"] = lambda: qig.plan_experts(ids, ne, out=plan)
+        calls["gate_up"] = lambda: qig.mm_i8_experts(W1, s1, qx, sx, plan, rows, glu=True, y=h)
+        calls["quantize_h"] = lambda: qig.quantize_i8(h, q=qh, s=sh)
+        calls["down"] = lambda: qig.mm_i8_experts(W2, s2, qh, sh, plan, rows, y=o)
+        calls["combine_experts"] = lambda: qig.combine_experts(o, rw, y=y)
+    else:
+        ws = qig.new_workspace(dev)
+        calls["gate_up"] = lambda: qig.mm_i8(W1[0], s1[0], qx, sx, glu=True, y=h, ws=ws)
+        calls["quantize_h"] = lambda: qig.quantize_i8(h, q=qh, s=sh)
+        calls["down"] = lambda: qig.mm_i8(W2[0], s2[0], qh, sh, y=y, ws=ws)
+
+    def step():
+        for fn in calls.values():
+            fn()
+
+    spun, clocks = spin_up(step, args.spinup_s)
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        step()
+    torch.cuda.synchronize()
+    ms_per_step = (time.perf_counter() - t0) / args.steps * 1e3
+    per = {n: gpu_avg_us(fn, args.steps) for n, fn in calls.items()}
+    ops = {"gate_up": 4.0 * rows * ff * id_, "down": 2.0 * rows * ff * id_}
+    total = sum(ops.values())
+    print(json.dumps({
+        "metric": METRIC,
+        "value": round(total / (ms_per_step * 1e-3) / 1e12, 2),
+        "unit": "TOPS",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms_per_step, 4),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": "int8",
+        "data": "synthetic",
+        "config": {"workload": args.workload, "nt": nt, "id": id_, "hidden": ff, "experts": ne, "per_token": k,
+                   "weights": "int8, one scale per output channel", "activations": "bf16, quantized per token"},
+        "per_kernel_us": {n: round(v, 3) for n, v in per.items()},
+        "summed_us": round(sum(per.values()), 2),
+        "per_gemm_tops": {n: round(v / (per[n] * 1e-6) / 1e12, 1) for n, v in ops.items()},
+        "weight_gbs": {n: round(w.numel() / (per[n] * 1e-6) / 1e9, 1) for n, w in (("gate_up", W1), ("down", W2))},
+        "spinup": {"seconds": args.spinup_s, "steps": spun},
+        "clocks_mhz": clocks,
+    }), flush=True)
+
+
 # rocprofv3 kernel names -> the names bench.py reports
 PROFILE_NAMES = {
     "qig::mmq_kernel<4, 0, 0, 0>": "mmq_q4k", "qig::mmq_kernel<6, 0, 0, 0>": "mmq_q6k_raw",
@@ -746,6 +835,9 @@ def main():
 
     assert torch.cuda.is_available(), "bench.py needs a GPU"
     qig.load()
+    if args.workload in ("ffn_i8", "experts"):
+        run_int8(args)
+        return
     if args.workload != "proj":
         run_gemm_set(args)
         return

@@ -22,11 +22,11 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 def _start():
     """torch and the library, on the first call (importing the package needs
     neither)."""
-    global torch, _lib, _empty, _current
+    global torch, _lib, _empty, _current, _f32
     import torch as t
     _lib = load()
     _TYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
-    _empty = t.empty
+    _empty, _f32 = t.empty, t.float32
     # the current stream's handle without the Stream object (1 us a call)
     _current = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda dev: t.cuda.current_stream(dev).cuda_stream)
     torch = t
@@ -64,6 +64,8 @@ def _sized(t, name, rows, cols):
 
 
 def _vector(t, n, name):
+    if t.dtype is _f32 and t.numel() == n and t.is_contiguous():
+        return
     _is(t, torch.float32, name)
     if t.numel() != n or not t.is_contiguous():
         raise QigError(f"{name} must be contiguous with {n} elements, not {list(t.shape)}")
@@ -87,19 +89,25 @@ def _int8_rows(t, name):
     return rows, cols, ld
 
 
-def _call(fn, what, named, stream, args):
-    """Check that the tensors are on one GPU and call fn there."""
+def _refuse_devices(names, tensors):
     dev = None
-    for name, t in named.items():
+    for name, t in zip(names, tensors):
         if t is None:
             continue
-        d = t.get_device()
-        if d < 0:
+        if not t.is_cuda:
             raise QigError(f"{name} must be a GPU tensor")
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise QigError(f"{name} is on cuda:{d}, other tensors of the call on cuda:{dev}")
+        if dev is not None and t.device != dev:
+            raise QigError(f"{name} is on {t.device}, other tensors of the call on {dev}")
+        dev = t.device
+
+
+def _call(fn, what, names, tensors, stream, args):
+    """Check that the tensors (the first of them not None) are on one GPU and
+    call fn there."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            _refuse_devices(names, tensors)
     if stream is None:
         handle = _current(dev)
     else:
@@ -136,7 +144,7 @@ def quantize_i8(x, q=None, s=None, stream=None):
         s = _empty((nt,), dtype=torch.float32, device=x.device)
     else:
         _vector(s, nt, "s")
-    _call(_lib.quantize_i8, "quantize_i8", {"x": x, "q": q, "s": s}, stream,
+    _call(_lib.quantize_i8, "quantize_i8", ("x", "q", "s"), (x, q, s), stream,
           (x.data_ptr(), xt, nt, id_, ldx, q.data_ptr(), ldq, s.data_ptr()))
     return q, s
 
@@ -183,7 +191,7 @@ def mm_i8(W, sw, q, sq, bias=None, glu=False, y=None, dtype=None, ws=None, strea
     if ws is not None and (ws.numel() * ws.element_size() < _lib.mmq_workspace_bytes() or not ws.is_contiguous()):
         raise QigError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs "
                        f"{_lib.mmq_workspace_bytes()}, contiguous")
-    _call(_lib.mm_i8, "mm_i8", {"W": W, "sw": sw, "q": q, "sq": sq, "bias": bias, "y": y, "ws": ws}, stream,
+    _call(_lib.mm_i8, "mm_i8", ("W", "sw", "q", "sq", "bias", "y", "ws"), (W, sw, q, sq, bias, y, ws), stream,
           (W.data_ptr(), ldw, sw.data_ptr(), od, id_, q.data_ptr(), ldq, sq.data_ptr(), nt,
            None if bias is None else bias.data_ptr(), 1 if glu else 0, y.data_ptr(), yt, ldy,
            None if ws is None else ws.data_ptr()))
@@ -216,7 +224,7 @@ def route_experts(logits, k, score="softmax", bias=None, groups=1, topk_groups=1
         w = _empty((nt, max(k, 0)), dtype=torch.float32, device=logits.device)
     else:
         _vector(w, nt * k, "w")
-    _call(_lib.route_experts, "route_experts", {"logits": logits, "bias": bias, "ids": ids, "w": w}, stream,
+    _call(_lib.route_experts, "route_experts", ("logits", "bias", "ids", "w"), (logits, bias, ids, w), stream,
           (logits.data_ptr(), lt, nt, ne, ldl, None if bias is None else bias.data_ptr(), _SCORES[score], groups,
            topk_groups, group_top, k, 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr()))
     return ids, w
@@ -245,7 +253,7 @@ def plan_experts(ids, ne, out=None, stream=None):
         _is(out, torch.int32, "out")
         if out.numel() < words or not out.is_contiguous():
             raise QigError(f"out must be contiguous with at least {words} words")
-    _call(_lib.plan_experts, "plan_experts", {"ids": ids, "out": out}, stream,
+    _call(_lib.plan_experts, "plan_experts", ("ids", "out"), (ids, out), stream,
           (ids.data_ptr(), n, ne, out.data_ptr()))
     return out
 
@@ -286,7 +294,7 @@ def mm_i8_experts(W, sw, q, sq, plan, nrows, bias=None, glu=False, y=None, dtype
         raise QigError(f"plan is not one of {nrows} rows and {ne} experts")
     y, yt, ldy = _output(y, dtype, nrows, od, q.device)
     _call(_lib.mm_i8_experts, "mm_i8_experts",
-          {"W": W, "sw": sw, "q": q, "sq": sq, "plan": plan, "bias": bias, "y": y}, stream,
+          ("W", "sw", "q", "sq", "plan", "bias", "y"), (W, sw, q, sq, plan, bias, y), stream,
           (W.data_ptr(), ldw, sw.data_ptr(), ne, od, id_, q.data_ptr(), ldq, sq.data_ptr(), nrows, slots,
            plan.data_ptr(), None if bias is None else bias.data_ptr(), 1 if glu else 0, y.data_ptr(), yt, ldy))
     return y
@@ -307,6 +315,6 @@ def combine_experts(h, w, y=None, dtype=None, stream=None):
     if n != nt * k:
         raise QigError(f"h must be [{nt * k}][any], not {list(h.shape)}")
     y, yt, ldy = _output(y, h.dtype if y is None and dtype is None else dtype, nt, od, h.device)
-    _call(_lib.combine_experts, "combine_experts", {"h": h, "w": w, "y": y}, stream,
+    _call(_lib.combine_experts, "combine_experts", ("h", "w", "y"), (h, w, y), stream,
           (h.data_ptr(), ht, ldh, w.data_ptr(), nt, k, od, y.data_ptr(), yt, ldy))
     return y

@@ -103,16 +103,28 @@ struct Rows {
     int e, first, count;   // expert, first position in the order, rows of the tile
 };
 
-// Token tiles of all experts.
+// Token tiles of all experts, at most the `most` that the grid was made for.
 template <int BM>
-__device__ __forceinline__ int count_tiles(const int32_t *plan, int ne)
+__device__ __forceinline__ int count_tiles(const int32_t *plan, int ne, int most)
 {
     const int lane = threadIdx.x & 63;
     int n = 0;
     for (int e = lane; e <= ne; e += 64) n += (plan[e + 1] - plan[e] + BM - 1) / BM;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
-    return __builtin_amdgcn_readfirstlane(n);
+    n = __builtin_amdgcn_readfirstlane(n);
+    return n < 0 ? 0 : (n < most ? n : most);
+}
+
+// Flat row number i of the order, for a tile of `count` rows.  The host cannot
+// see whether a plan belongs to the call: one made for other rows gives wrong
+// rows here, but none outside [0, nrows).
+__device__ __forceinline__ int row_of(const int32_t *plan, int ne, const Rows &r, int i, int nrows)
+{
+    int at = r.first + (i < r.count ? i : r.count - 1);
+    at = at < 0 ? 0 : (at < nrows ? at : nrows - 1);
+    const int row = plan[ne + 2 + at];
+    return (unsigned)row < (unsigned)nrows ? row : nrows - 1;
 }
 
 // Token tile mt, which exists.
@@ -179,7 +191,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     }
     if constexpr (EXPERTS) {
         unsigned i;
-        const unsigned nbt = (unsigned)count_tiles<BM>(g.plan, g.ne);
+        const unsigned nbt = (unsigned)count_tiles<BM>(g.plan, g.ne, g.nbt);
         if (!place_of(block, nbt * (unsigned)g.nbj, i)) return;
         tile_of<EXPERT_BAND>(i, nbt, (unsigned)g.nbj, mt, jt);
     } else {
@@ -197,11 +209,10 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     if constexpr (EXPERTS) {
         const Rows r = find_rows<BM>(g.plan, g.ne, mt);
         count = r.count;
-        const int32_t *order = g.plan + g.ne + 2 + r.first;
         if (r.e == g.ne) {
             // dropped rows: zeros
             for (int i = wave; i < count; i += NW) {
-                elem_t<YT> *row = y + (int64_t)order[i] * g.ldy;
+                elem_t<YT> *row = y + (int64_t)row_of(g.plan, g.ne, r, i, (int)g.nt) * g.ldy;
                 for (int64_t j = j0 + lane; j < j0 + BJ && j < g.od; j += 64) row[j] = (elem_t<YT>)0.0f;
             }
             return;
@@ -211,7 +222,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         sw += (int64_t)r.e * rows;
         if (bias) bias += (int64_t)r.e * rows;
         for (int i = tid; i < BM; i += NW * 64) {
-            const int32_t row = order[i < count ? i : count - 1];
+            const int row = row_of(g.plan, g.ne, r, i, (int)g.nt);
             s_row[i] = row;
             s_sq[i] = g.sq[row / g.slots];
         }
@@ -509,7 +520,8 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the sums are at the coherence point
             __syncthreads();
             __shared__ uint32_t s_before;
-            if (tid == 0) s_before = __hip_atomic_fetch_add(g.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (tid == 0)
+                s_before = __hip_atomic_fetch_add(g.cnt + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __syncthreads();
             if (s_before != (uint32_t)g.splits - 1) return;
             for (int o = 0; o < g.splits; ++o) {
@@ -636,7 +648,7 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int jt = (int)(blockIdx.x % (unsigned)g.nbj), mt = (int)(blockIdx.x / (unsigned)g.nbj);
     if constexpr (EXPERTS)
-        if (mt >= count_tiles<BM>(g.plan, g.ne)) return;
+        if (mt >= count_tiles<BM>(g.plan, g.ne, g.nbt)) return;
     const int64_t j0 = (int64_t)jt * GEMV_ROWS;
     const uint8_t *W = g.W;
     const float *sw = g.sw, *bias = g.bias;
@@ -646,12 +658,12 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
     if constexpr (EXPERTS) {
         const Rows r = find_rows<BM>(g.plan, g.ne, mt);
         count = r.count;
-        const int32_t *order = g.plan + g.ne + 2 + r.first;
         if (r.e == g.ne) {
             // dropped rows: zeros
             for (int i = tid; i < count * GEMV_ROWS; i += NW * 64)
                 if (j0 + i % GEMV_ROWS < g.od)
-                    y[(int64_t)order[i / GEMV_ROWS] * g.ldy + j0 + i % GEMV_ROWS] = (elem_t<YT>)0.0f;
+                    y[(int64_t)row_of(g.plan, g.ne, r, i / GEMV_ROWS, (int)g.nt) * g.ldy + j0 + i % GEMV_ROWS] =
+                        (elem_t<YT>)0.0f;
             return;
         }
         const int64_t rows = GLU ? 2 * g.od : g.od;
@@ -659,7 +671,7 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
         sw += (int64_t)r.e * rows;
         if (bias) bias += (int64_t)r.e * rows;
         if (tid < BM) {
-            const int32_t row = order[tid < count ? tid : count - 1];
+            const int row = row_of(g.plan, g.ne, r, tid, (int)g.nt);
             s_row[tid] = row;
             s_sq[tid] = g.sq[row / g.slots];
         }

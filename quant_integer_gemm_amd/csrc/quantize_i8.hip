@@ -97,10 +97,11 @@ __device__ __forceinline__ void quant_vec(const float (&x)[VEC<T>], const RowSca
 // THR threads a row (64: one wave, four rows a workgroup), the row read once
 // into NV vectors of 16 bytes a thread.
 //
-// Bound by memory: 2630 x 18944 bf16 (149 MB in and out) MEASURED_LONG, and
-// 15780 x 2368 bf16 (112 MB) MEASURED_SHORT.  A wave a row needs no barrier and
-// was the faster form where a wave holds the row and there are rows enough to
-// fill the card; with few rows 256 threads shorten the one row's latency.
+// Bound by memory: 2630 x 18944 bf16 (149 MB in and out) 26.8 us, 5.6 TB/s;
+// 15780 x 2368 bf16 (112 MB) 25 us; 2630 x 3584 bf16 (28 MB) 7 us, where loads
+// and the launch show.  256 threads for rows of 65 to 1024 vectors: a wave a
+// row, without a barrier, measured the same at 15780 rows and 15% slower at
+// 2630, and 512 threads slower at both.
 template <int T, int THR, int NV>
 __global__ __launch_bounds__(THR < 256 ? 256 : THR) void quantize_i8_kernel(const elem_t<T> *__restrict__ x,
                                                                             int64_t nt, int id, int64_t ldx,
@@ -229,11 +230,6 @@ static int launch(const void *xv, int64_t nt, int64_t id, int64_t ldx, int8_t *q
     const elem_t<T> *x = static_cast<const elem_t<T> *>(xv);
     const int64_t nv = (id + VEC<T> - 1) / VEC<T>;
     if (nv <= 64) return launch_rows<T, 64, 1>(x, nt, id, ldx, q, ldq, s, stream);
-    if (nv <= 512 && nt >= 1024) {
-        if (nv <= 128) return launch_rows<T, 64, 2>(x, nt, id, ldx, q, ldq, s, stream);
-        if (nv <= 256) return launch_rows<T, 64, 4>(x, nt, id, ldx, q, ldq, s, stream);
-        return launch_rows<T, 64, 8>(x, nt, id, ldx, q, ldq, s, stream);
-    }
     if (nv <= 256) return launch_rows<T, 256, 1>(x, nt, id, ldx, q, ldq, s, stream);
     if (nv <= 512) return launch_rows<T, 256, 2>(x, nt, id, ldx, q, ldq, s, stream);
     if (nv <= 1024) return launch_rows<T, 256, 4>(x, nt, id, ldx, q, ldq, s, stream);

@@ -440,3 +440,39 @@ def test_layer_on_other_streams_and_in_graphs(qig):
         torch.cuda.synchronize()
         assert torch.equal(y, eager[i % 3]) and torch.equal(z, lin[i % 3]), i
         assert torch.equal(_layer(qig, ls[0], xs[0], weights, 2)[1], eager[0])
+
+
+def test_nothing_to_do(qig):
+    """No tokens, no outputs, no rows."""
+    z = lambda *n, t=torch.float32: torch.zeros(n, dtype=t, device="cuda")  # noqa: E731
+    i8 = torch.int8
+    q, s = qig.quantize_i8(z(0, 40))
+    assert q.shape == (0, 40) and s.shape == (0,)
+    assert qig.mm_i8(z(8, 32, t=i8), z(8), z(0, 32, t=i8), z(0)).shape == (0, 8)
+    assert qig.mm_i8(z(0, 32, t=i8), z(0), z(3, 32, t=i8), z(3)).shape == (3, 0)
+    ids, w = qig.route_experts(z(0, 8), 2)
+    assert ids.shape == w.shape == (0, 2)
+    plan = qig.plan_experts(ids, 8)
+    assert plan.tolist() == [0] * 10
+    assert qig.mm_i8_experts(z(8, 4, 32, t=i8), z(8, 4), z(0, 32, t=i8), z(0), plan, 0).shape == (0, 4)
+    assert qig.combine_experts(z(0, 16), z(0, 2)).shape == (0, 16)
+    torch.cuda.synchronize()
+
+
+def test_given_stream_and_two_streams_at_once(qig):
+    """Calls on two streams, each with a workspace of its own, on shapes that
+    split their sums, interleaved on the host."""
+    g = _rng(12)
+    q, W, sq, sw, _ = _operands(g, 100, 300, 4000, False)
+    a = [_dev(v) for v in (W, sw, q, sq)]
+    y0 = qig.mm_i8(*a)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [qig.new_workspace(a[0].device) for _ in range(2)]
+    torch.cuda.synchronize()
+    ys = [[torch.empty_like(y0) for _ in range(5)] for _ in range(2)]
+    for i in range(5):
+        for s in range(2):
+            qig.mm_i8(*a, y=ys[s][i], ws=ws[s], stream=streams[s])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, y0) for r in ys for y in r)
