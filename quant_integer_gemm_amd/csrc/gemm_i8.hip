@@ -49,6 +49,14 @@ __device__ __forceinline__ uint64_t uniform64(const void *p)
     return (uint64_t)lo | ((uint64_t)hi << 32);
 }
 
+// 16 x 16 x 64: lane l supplies row l % 16 and 16 bytes (l / 16) of the 64 of
+// both operands; the result's column (b's row) is l % 16, its rows (a's)
+// 4 (l / 16) + i.
+__device__ __forceinline__ i32x4 mfma16(i32x4 a, i32x4 b, i32x4 c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
 // One 1 KB copy, 16 bytes a lane, to LDS byte address lds + 16 lane.  Issued
 // from inline assembly, unseen by the compiler's wait counts: its data is
 // read only after an explicit vmcnt wait and a barrier.  s_nop 4 covers the
@@ -161,9 +169,9 @@ __device__ __forceinline__ Rows find_rows(const int32_t *plan, int ne, int mt)
     return r;
 }
 
-// BM x BN tile, WM x WN waves, each BM/WM x BN/WN in 32 x 32 MFMA tiles.
-// GLU: of every 64 of the tile's weight rows the first 32 are gate rows and
-// the last 32 the up rows of the same outputs, so a wave holds both halves of
+// BM x BN tile, WM x WN waves, each BM/WM x BN/WN.
+// GLU: of every 32 of the tile's weight rows the first 16 are gate rows and
+// the last 16 the up rows of the same outputs, so a wave holds both halves of
 // an output in the same lane and register.
 template <int BM, int BN, int WM, int WN, int S, bool SPLIT, bool GLU, bool EXPERTS, int YT>
 __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
@@ -175,7 +183,6 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     constexpr int BJ = GLU ? BN / 2 : BN;               // outputs of a tile
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TMAX >= 1 && TMAX <= 4 && TN >= 1, "tile");
     static_assert(S == 2 || S >= 4, "stages");
-    static_assert(!GLU || TN % 2 == 0, "gate and up rows of an output in one wave");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S * STAGE];
     __shared__ float s_sq[BM];
     __shared__ __attribute__((aligned(16))) float s_sw[BN], s_bias[BN];
@@ -234,9 +241,9 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 
     // scales and biases of the tile's weight rows, in the order of its LDS rows
     for (int i = tid; i < BN; i += NW * 64) {
-        int64_t j = j0 + (GLU ? (i >> 6) * 32 + (i & 31) : i);
+        int64_t j = j0 + (GLU ? (i >> 5) * 16 + (i & 15) : i);
         j = j < g.od ? j : g.od - 1;
-        if (GLU && (i & 32)) j += g.od;
+        if (GLU && (i & 16)) j += g.od;
         s_sw[i] = sw[j];
         s_bias[i] = bias ? bias[j] : 0.0f;
     }
@@ -260,11 +267,11 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     bool bup[PB];
 #pragma unroll
     for (int p = 0; p < PB; ++p) {
-        // a piece's eight rows lie in one block of 32, so gate or up is the
+        // a piece's eight rows lie in one block of 16, so gate or up is the
         // same for the whole piece
         const int r = 8 * (NW * p + wave) + lr;
-        int j = GLU ? (r >> 6) * 32 + (r & 31) : r;
-        bup[p] = GLU && ((8 * (NW * p + wave)) & 32) != 0;
+        int j = GLU ? (r >> 5) * 16 + (r & 15) : r;
+        bup[p] = GLU && ((8 * (NW * p + wave)) & 16) != 0;
         const int64_t last = g.od - 1 - j0;
         if (j > last) j = (int)last;
         boff[p] = (uint32_t)j * (uint32_t)g.ldw;
@@ -284,7 +291,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     }
 
     const int wm = wave / WN, wn = wave % WN;
-    const int lrow = lane & 31, lhalf = lane >> 5;
+    const int l16 = lane & 15, quad = lane >> 4;
 
     // The tile with TM x 32 of every wave's rows: only as many as have tokens
     // (the last tile of the tokens, or of an expert's rows, is mostly smaller).
@@ -335,142 +342,142 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             __syncthreads();
         };
 
-        i32x16 acc[TM][TN];
+        // 16 x 16 x 64 MFMAs: FM blocks of 16 tokens, FN of 16 weight rows.  (The
+        // 32 x 32 x 32 form moves more accumulator bytes an operation and, where
+        // the card's power is the limit, is slower: from registers alone, random
+        // data, 3550 against 4150 TOPS.)
+        constexpr int FM = 2 * TM, FN = 2 * TN;
+        i32x4 acc[FM][FN];
 #pragma unroll
-        for (int m = 0; m < TM; ++m)
+        for (int m = 0; m < FM; ++m)
 #pragma unroll
-            for (int n = 0; n < TN; ++n)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[m][n][i] = 0;
+            for (int n = 0; n < FN; ++n) acc[m][n] = i32x4{0, 0, 0, 0};
 
-        // Chunk c of a step is 32 bytes of every row: granules 2 c and 2 c + 1.
-        // Rows of one lane differ by multiples of 32, so its slot is the same in
-        // all of them.
-        constexpr int NC = BK / 32;
+        // Chunk c of a step is 64 bytes of every row: granules 4 c .. 4 c + 3,
+        // one for each quarter of the wave.  Rows of one lane differ by multiples
+        // of 16, so its slot is the same in all of them.
+        constexpr int NC = BK / 64, NP = PA + PB, P3 = NP / 2;
         uint32_t aat[NC], bat[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const uint32_t slot = 16 * ((2 * c + lhalf) ^ (lrow & 7));
-            aat[c] = (wm * TM * 32 + lrow) * BK + slot;
-            bat[c] = (BM + wn * TN * 32 + lrow) * BK + slot;
+            const uint32_t slot = 16 * ((4 * c + quad) ^ (l16 & 7));
+            aat[c] = (wm * FM * 16 + l16) * BK + slot;
+            bat[c] = (BM + wn * FN * 16 + l16) * BK + slot;
         }
-        struct Frag {
-            i32x4 a[TM], b[TN];
-        } f[S == 2 ? 2 : NC];
-        auto read = [&](Frag &o, int kt, int c, int i) {
-            const uint8_t *st = lds + buffer(kt) * STAGE;
-            if (i < TN)
-                o.b[i] = *reinterpret_cast<const i32x4 *>(st + bat[c] + i * 32 * BK);
-            else
-                o.a[i - TN] = *reinterpret_cast<const i32x4 *>(st + aat[c] + (i - TN) * 32 * BK);
+        auto read_a = [&](int kt, int c, int m) {
+            return *reinterpret_cast<const i32x4 *>(lds + buffer(kt) * STAGE + aat[c] + m * 16 * BK);
         };
-        constexpr int NM = TM * TN, NR = TM + TN, NP = PA + PB, P3 = NP / 2;
-        // One chunk's MFMAs, in issue order, behind them the reads of the next
-        // chunk (chunk rc of step rk) one by one, and the copies [P0, P1) of step
-        // ck, evenly spread.
-        auto chunk = [&](auto reads, auto p0, auto p1, const Frag &o, Frag &nx, int rk, int rc, int ck) {
-            constexpr int P0 = p0, N = p1 - p0;
-#pragma unroll
-            for (int i = 0; i < NM; ++i) {
-                acc[i / TN][i % TN] = mfma_i8(o.b[i % TN], o.a[i / TN], acc[i / TN][i % TN]);
-                if constexpr (reads) {
-                    if (i < NR) read(nx, rk, rc, i);
-                    if (i == NM - 1)
-#pragma unroll
-                        for (int r = NM; r < NR; ++r) read(nx, rk, rc, r);
-                }
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j * NM / (N > 0 ? N : 1) == i) copy(ck, P0 + j);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        auto read_b = [&](int kt, int c, int n) {
+            return *reinterpret_cast<const i32x4 *>(lds + buffer(kt) * STAGE + bat[c] + n * 16 * BK);
         };
-        constexpr std::integral_constant<int, 0> c0;
-        constexpr std::integral_constant<int, P3> cm;
-        constexpr std::integral_constant<int, NP> cn;
         constexpr std::true_type yes;
         constexpr std::false_type no;
-        // All but the copies of the last S - 2 steps issued have landed, and
-        // everybody's reads before this point are done.
-        auto landed = [&](auto all) {
-            if constexpr (all)
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            else
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * NP) : "memory");
-            __syncthreads();
-        };
-        // Step kt, its first chunk in f[0]: with it go the copies of step
-        // kt + S - 1 from piece P3 on (`late`), and, once step kt + 1 has landed
-        // and the stage of step kt - 1 + S is free of readers, those of step
-        // kt + S up to P3 (`early`).
-        auto step = [&](auto late, auto early, int kt) {
-            if constexpr (late)
-                chunk(yes, cm, cn, f[0], f[1], kt, 1, kt + S - 1);
-            else
-                chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
-#pragma unroll
-            for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
-            landed(std::bool_constant<!late>{});
-            if constexpr (early) {
-                chunk(yes, c0, cm, f[(NC - 1) & 1], f[0], kt + 1, 0, kt + S);
-            } else {
-                if (kt + 1 == nk - 1 && tail < BK) clear_tail(lds + buffer(kt + 1) * STAGE);
-                chunk(yes, c0, c0, f[(NC - 1) & 1], f[0], kt + 1, 0, 0);
-            }
-        };
 
         if constexpr (S == 2) {
+            // A step is MS row steps: one block of tokens against the FN blocks of
+            // weights, chunk after chunk.  Token blocks are read LA row steps
+            // ahead into a ring of four, weight blocks while the chunk before
+            // theirs is multiplied.  In the last quarter (AFTER row steps) the
+            // next step has landed and its first blocks are read; the copies go
+            // out one by one in that quarter (pieces up to P3 of the step after
+            // the next, whose stage is free then) and in the first (the others).
+            constexpr int MS = NC * FM, AFTER = MS / 4, LA = AFTER < 3 ? AFTER : 3;
+            i32x4 ra[4], rb[NC][FN];
+            auto step = [&](auto late, auto early, auto next, int kt) {
 #pragma unroll
-            for (int k = 0; k < S - 1; ++k)
-                if (k < nk)
+                for (int s = 0; s < MS; ++s) {
+                    const int c = s / FM, m = s % FM;
+                    const int in = s - (MS - AFTER);   // row step of the last quarter
+                    if (next && in == 0) {
+                        // the next step has landed, and nobody reads this one any more
+                        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                        __syncthreads();
+                        if constexpr (!early)
+                            if (tail < BK) clear_tail(lds + buffer(kt + 1) * STAGE);
+                    }
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) copy(k, p);
-            if (nk >= S - 1)
-                landed(no);
-            else
-                landed(yes);
+                    for (int n = 0; n < FN; ++n) {
+                        acc[m][n] = mfma16(rb[c][n], ra[s & 3], acc[m][n]);
+                        if (n == 0) {
+                            const int t = s + LA;
+                            if (t < MS)
+                                ra[t & 3] = read_a(kt, t / FM, t % FM);
+                            else if (next)
+                                ra[t & 3] = read_a(kt + 1, 0, t - MS);
+                        }
+                        // weight block i of the coming chunk behind MFMA i of the quarter
+                        if (s < AFTER) {
+#pragma unroll
+                            for (int i = 0; i < FN; ++i)
+                                if (i * AFTER == s * FN + n) rb[1][i] = read_b(kt, 1, i);
+                        } else if (next && in >= 0) {
+#pragma unroll
+                            for (int i = 0; i < FN; ++i)
+                                if (i * AFTER == in * FN + n) rb[0][i] = read_b(kt + 1, 0, i);
+                        }
+                        if (late && s < AFTER) {
+#pragma unroll
+                            for (int i = 0; i < NP - P3; ++i)
+                                if (i * AFTER * FN / (NP - P3) == s * FN + n) copy(kt + 1, P3 + i);
+                        } else if (early && in >= 0) {
+#pragma unroll
+                            for (int i = 0; i < P3; ++i)
+                                if (i * AFTER * FN / P3 == in * FN + n) copy(kt + 2, i);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            };
+#pragma unroll
+            for (int p = 0; p < NP; ++p) copy(0, p);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
             if (nk == 1 && tail < BK) clear_tail(lds);
 #pragma unroll
-            for (int i = 0; i < NR; ++i) read(f[0], 0, 0, i);
-            int kt = 0;
-            if (nk >= S) {
+            for (int i = 0; i < FN; ++i) rb[0][i] = read_b(0, 0, i);
 #pragma unroll
-                for (int p = 0; p < P3; ++p) copy(S - 1, p);
-                for (; kt < nk - S; ++kt) step(yes, yes, kt);
-                step(yes, no, kt++);
+            for (int t = 0; t < LA; ++t) ra[t] = read_a(0, 0, t);
+            if (nk > 1) {
+#pragma unroll
+                for (int p = 0; p < P3; ++p) copy(1, p);
+                for (int kt = 0; kt < nk - 2; ++kt) step(yes, yes, yes, kt);
+                step(yes, no, yes, nk - 2);
             }
-            for (; kt < nk - 1; ++kt) step(no, no, kt);
-            chunk(yes, c0, c0, f[0], f[1], kt, 1, 0);
-#pragma unroll
-            for (int c = 1; c < NC - 1; ++c) chunk(yes, c0, c0, f[c & 1], f[(c + 1) & 1], kt, c + 1, 0);
-            chunk(no, c0, c0, f[(NC - 1) & 1], f[0], 0, 0, 0);
+            step(no, no, no, nk - 1);
         } else {
             // Body kt multiplies step kt, held in registers, and reads step
-            // kt + 1 chunk by chunk into the registers as they come free, so
+            // kt + 1 block by block into the registers as they come free, so
             // nearly a whole step lies between a read and its use; it copies step
             // kt + S - 1 into the stage of step kt - 1, whose reads every wave
             // has used by then.
-            auto body = [&](auto copies, int kt) {
+            i32x4 fa[NC][FM], fb[NC][FN];
+            constexpr int ALL = NC * FM * FN;
+            auto body = [&](auto copies, auto next, int kt) {
                 constexpr int N = copies ? NP : 0;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int i = 0; i < NM; ++i) {
-                        acc[i / TN][i % TN] = mfma_i8(f[c].b[i % TN], f[c].a[i / TN], acc[i / TN][i % TN]);
+                    for (int m = 0; m < FM; ++m)
 #pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            if (i == NM - 1) read(f[c], kt + 1, c, r);
+                        for (int n = 0; n < FN; ++n) {
+                            acc[m][n] = mfma16(fb[c][n], fa[c][m], acc[m][n]);
+                            if constexpr (next) {
+                                if (m == FM - 1) fb[c][n] = read_b(kt + 1, c, n);
+                                if (n == FN - 1) fa[c][m] = read_a(kt + 1, c, m);
+                            }
 #pragma unroll
-                        for (int j = 0; j < N; ++j)
-                            if (j * NM * NC / N == c * NM + i) copy(kt + S - 1, j);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                if constexpr (copies)
-                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
-                else
-                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
+                            for (int j = 0; j < N; ++j)
+                                if (j * ALL / N == (c * FM + m) * FN + n) copy(kt + S - 1, j);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                if constexpr (next) {
+                    if constexpr (copies)
+                        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * NP) : "memory");
+                    else
+                        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                }
             };
 #pragma unroll
             for (int k = 0; k < S - 1; ++k)
@@ -484,20 +491,19 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             __syncthreads();
             if (nk <= 2 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NC; ++c) {
 #pragma unroll
-                for (int r = 0; r < NR; ++r) read(f[c], 0, c, r);
+                for (int n = 0; n < FN; ++n) fb[c][n] = read_b(0, c, n);
+#pragma unroll
+                for (int m = 0; m < FM; ++m) fa[c][m] = read_a(0, c, m);
+            }
             int kt = 0;
-            for (; kt <= nk - S; ++kt) body(yes, kt);
+            for (; kt <= nk - S; ++kt) body(yes, yes, kt);
             for (; kt < nk - 1; ++kt) {
-                body(no, kt);
+                body(no, yes, kt);
                 if (kt + 2 == nk - 1 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
             }
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int i = 0; i < NM; ++i)
-                    acc[i / TN][i % TN] = mfma_i8(f[c].b[i % TN], f[c].a[i / TN], acc[i / TN][i % TN]);
+            body(no, no, kt);
         }
 
         if constexpr (SPLIT) {
@@ -510,12 +516,12 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             int32_t *slot = g.part + (int64_t)tile * g.splits * (BM * BN);
             int32_t *mine = slot + (int64_t)split * (BM * BN) + tid;
 #pragma unroll
-            for (int m = 0; m < TM; ++m)
+            for (int m = 0; m < FM; ++m)
 #pragma unroll
-                for (int n = 0; n < TN; ++n)
+                for (int n = 0; n < FN; ++n)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        __hip_atomic_store(mine + ((m * TN + n) * 16 + i) * LANES, acc[m][n][i], __ATOMIC_RELAXED,
+                    for (int i = 0; i < 4; ++i)
+                        __hip_atomic_store(mine + ((m * FN + n) * 4 + i) * LANES, acc[m][n][i], __ATOMIC_RELAXED,
                                            __HIP_MEMORY_SCOPE_AGENT);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the sums are at the coherence point
             __syncthreads();
@@ -528,58 +534,58 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
                 if (o == split) continue;
                 int32_t *other = slot + (int64_t)o * (BM * BN) + tid;
 #pragma unroll
-                for (int m = 0; m < TM; ++m)
+                for (int m = 0; m < FM; ++m)
 #pragma unroll
-                    for (int n = 0; n < TN; ++n)
+                    for (int n = 0; n < FN; ++n)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[m][n][i] += __hip_atomic_load(other + ((m * TN + n) * 16 + i) * LANES, __ATOMIC_RELAXED,
+                        for (int i = 0; i < 4; ++i)
+                            acc[m][n][i] += __hip_atomic_load(other + ((m * FN + n) * 4 + i) * LANES, __ATOMIC_RELAXED,
                                                               __HIP_MEMORY_SCOPE_AGENT);
             }
             if (tid == 0) __hip_atomic_store(g.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
 
         // The weights are the rows of the result: lane l, register i holds token
-        // l % 32 and weight row 8 (i / 4) + 4 (l / 32) + i % 4, so four neighbouring
-        // registers are four neighbouring outputs of one token.  Every wave turns
-        // 32 tokens at a time through its own part of the stages' LDS, so that its
-        // stores are whole rows of 64 to 256 bytes (stored straight from the
-        // registers, 16 bytes a row, fp32 outputs cost 12% of the time at 8192^3).
-        constexpr int NO = GLU ? TN / 2 : TN;
+        // l % 16 and weight row 4 (l / 16) + i, four neighbouring outputs of one
+        // token.  Every wave turns 32 tokens at a time through its own part of
+        // the stages' LDS, so that its stores are whole rows of 64 to 256 bytes
+        // (stored straight from the registers, 16 bytes a row, fp32 outputs cost
+        // 12% of the time at 8192^3).
+        constexpr int NO = GLU ? FN / 2 : FN;              // blocks of 16 outputs
         constexpr int EB = YT == T_F32 ? 4 : 2;            // bytes of an output
-        constexpr int PITCH = NO * 32 * EB + 16;           // 16 more: the rows' writes on different banks
-        constexpr int CH = NO * 32 * EB / 16;              // 16-byte chunks a row
+        constexpr int PITCH = NO * 16 * EB + 16;           // 16 more: the rows' writes on different banks
+        constexpr int CH = NO * EB;                        // 16-byte chunks a row
         constexpr int PER = 16 / EB;                       // outputs of a chunk
         static_assert(NW * 32 * PITCH <= S * STAGE, "the waves' parts");
         __syncthreads();   // nobody reads the stages any more
         uint8_t *mine = lds + wave * (32 * PITCH);
-        const int64_t jw = j0 + wn * NO * 32;
+        const int64_t jw = j0 + wn * NO * 16;
 #pragma unroll
-        for (int m = 0; m < TM; ++m) {
-            const int r0 = (wm * TM + m) * 32;
-            const float s = s_sq[r0 + lrow];
+        for (int m2 = 0; m2 < TM; ++m2) {
+            const int r0 = (wm * TM + m2) * 32;
 #pragma unroll
-            for (int n = 0; n < NO; ++n)
+            for (int h = 0; h < 2; ++h) {
+                const int m = 2 * m2 + h;
+                const float s = s_sq[r0 + 16 * h + l16];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int o = 8 * q + 4 * lhalf;   // outputs o .. o + 3 of the 32
-                    const int at = GLU ? (wn * NO + n) * 64 + o : (wn * NO + n) * 32 + o;
+                for (int n = 0; n < NO; ++n) {
+                    const int at = (wn * FN + (GLU ? 2 * n : n)) * 16 + 4 * quad;
                     const f32x4 w = *reinterpret_cast<const f32x4 *>(s_sw + at);
                     const f32x4 b = *reinterpret_cast<const f32x4 *>(s_bias + at);
                     float v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if constexpr (GLU) {
-                            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(s_sw + at + 32);
-                            const f32x4 b1 = *reinterpret_cast<const f32x4 *>(s_bias + at + 32);
-                            const float ga = (float)acc[m][2 * n][4 * q + i] * s * w[i] + b[i];
-                            const float up = (float)acc[m][2 * n + 1][4 * q + i] * s * w1[i] + b1[i];
+                            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(s_sw + at + 16);
+                            const f32x4 b1 = *reinterpret_cast<const f32x4 *>(s_bias + at + 16);
+                            const float ga = (float)acc[m][2 * n][i] * s * w[i] + b[i];
+                            const float up = (float)acc[m][2 * n + 1][i] * s * w1[i] + b1[i];
                             v[i] = silu_mul(ga, up);
                         } else {
-                            v[i] = (float)acc[m][n][4 * q + i] * s * w[i] + b[i];
+                            v[i] = (float)acc[m][n][i] * s * w[i] + b[i];
                         }
                     }
-                    uint8_t *to = mine + lrow * PITCH + (n * 32 + o) * EB;
+                    uint8_t *to = mine + (16 * h + l16) * PITCH + (n * 16 + 4 * quad) * EB;
                     if constexpr (EB == 4) {
                         *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
                     } else {
@@ -588,6 +594,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
                             four{(elem_t<YT>)v[0], (elem_t<YT>)v[1], (elem_t<YT>)v[2], (elem_t<YT>)v[3]};
                     }
                 }
+            }
 #pragma unroll
             for (int c = 0; c < CH / 2; ++c) {
                 const int i = c * 64 + lane, row = i / CH, ch = i % CH;
@@ -707,7 +714,7 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(p.w[b][h], p.x[h], acc[b], 0, 0, 0);
+                acc[b] = mfma16(p.w[b][h], p.x[h], acc[b]);
     };
     const int full = g.id / BK;
     Piece p[DEPTH];
