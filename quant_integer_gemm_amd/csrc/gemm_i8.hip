@@ -5,8 +5,21 @@
 // The sum over id is a plain int32 sum, so the whole contraction stays on the
 // int8 MFMA and both scales are applied once per output.  A workgroup owns a
 // BM x BN tile (tokens x weight rows) and walks id in steps of 128 bytes: both
-// operands are copied straight into LDS (global_load_lds), the next step's
-// copies in flight while this one is multiplied, one barrier a step.
+// operands are copied straight into LDS (global_load_lds), the next steps'
+// copies in flight while this one is multiplied, one barrier a step, the LDS
+// reads and the copies spread between the MFMAs.
+//
+// What bounds it, and what it reaches: large products are held by the card's
+// power (the clock falls from 2.4 to 1.75 GHz; zeros as data run at 2.4).  8192^3
+// 438 us, 2510 TOPS, the rate of a large product of the vendor's library on the
+// same card; 2630 tokens, 2 x 18944 x 3584 gated to bf16 312 us, 2290 TOPS; 18944
+// -> 3584 to fp32 154 us, 2320 TOPS.  Of the 8192^3 time, with 32 x 32 x 32 MFMAs,
+// a build without the copies took 16% less, one without the LDS reads 12%, one
+// with neither 27%.  Small products: launch, first loads and epilogue, 5 us, then
+// 0.25 us a step (3584 x 3584, 512 tokens 14.5 us).  Experts' products: the
+// weights' bytes up to about 50 rows an expert (5.0 TB/s), above that bytes and
+// power together (64 experts of 2 x 2368 x 3584, 15780 rows: 359 to 370 us; 300 us
+// with the weights of two experts for all, which stay in the caches).
 //
 // LDS rows are 128 bytes, eight 16-byte granules; granule g of row r is kept
 // at slot g ^ (r & 7), so that the eight lanes of a read phase (eight rows,
@@ -638,7 +651,9 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 // 16 x 16 x 64 MFMA (lane l: row l % 16, 16 bytes l / 16 of each 64), DEPTH
 // pieces before the first product, and their sums meet in LDS at the end.  The
 // weights are the rows of the result, so a lane holds four neighbouring
-// outputs of one token.
+// outputs of one token.  Bound by the weights' bytes: one token, 2 x 18944 x 3584
+// gated 24.6 us (5.5 TB/s), 3584 x 3584 5.0 us (2.6 TB/s: the launch and one
+// memory latency).
 constexpr int GEMV_WAVES = 8, GEMV_ROWS = 16;
 
 template <bool GLU, bool EXPERTS, int YT>
@@ -810,16 +825,17 @@ static int launch_tile(I8Args a, int64_t od, int64_t nt, hipStream_t stream)
 // round of tiles that leaves CUs without one, `full` as a CU's share when all
 // are busy, where the card's power holds the clock down (1.75 GHz under the
 // 256 x 256 tiles against 2.4); `ends` are a round's first loads and epilogue.
-// Measured at 8192^3 (full), 2630 tokens of 18944 -> 3584 and 64 to 512 tokens
-// of 3584 -> 3584 (alone).
+// Measured at 8192^3 (full: 438 us with 256 x 256, 464 with 192 x 256, 740 with
+// 64 x 128), and with 2630 tokens of 18944 -> 3584 (168, 154 and 244 us) and 64
+// to 512 of 3584 -> 3584 (alone).
 struct TileCost {
     int bm, bn, per_cu;
     double alone, full, ends;
 };
-constexpr TileCost COST_256 = {256, 256, 1, 1.14, 1.72, 6.0};
-constexpr TileCost COST_192 = {192, 256, 1, 0.86, 1.34, 5.0};
-constexpr TileCost COST_64 = {64, 128, 1, 0.31, 0.33, 3.0};
-constexpr TileCost COST_64S = {64, 128, 3, 0.54, 0.33, 3.0};   // two stages: three workgroups a CU
+constexpr TileCost COST_256 = {256, 256, 1, 1.05, 1.62, 6.0};
+constexpr TileCost COST_192 = {192, 256, 1, 0.84, 1.26, 6.0};
+constexpr TileCost COST_64 = {64, 128, 1, 0.30, 0.32, 3.0};
+constexpr TileCost COST_64S = {64, 128, 3, 0.54, 0.32, 3.0};   // two stages: three workgroups a CU
 
 template <bool GLU>
 static double cost(const TileCost &c, const I8Args &a)
@@ -843,8 +859,8 @@ constexpr int64_t GEMV_BYTES = int64_t(40) << 20;
 constexpr int64_t EXPERTS_GEMV_BYTES = int64_t(24) << 20, EXPERTS_GEMV_ROWS = 16;
 // Rows of an expert, on average, from which the larger tiles are faster, and
 // the tiles it takes for that.  64 experts' 4736 x 3584, us for 64 x 128,
-// 128 x 128 and 256 x 256: 1.5 rows each 144, 147, 163; 12 rows 204, 200, 216;
-// 48 rows 221, 216, 229; 246 rows 610, 509, 438.
+// 128 x 128 and 256 x 256: 1.5 rows each 144, 147, 163; 12 rows 203, 198, 214;
+// 48 rows 222, 215, 225; 246 rows 603, 440, 368.
 constexpr double ROWS_128 = 8, ROWS_256 = 96, TILES_128 = 256, TILES_256 = 192;
 // Split sums: shares of at least SPLIT_STEPS steps, a workgroup a CU, and at
 // most SPLIT_MOST shares: the last share to arrive reads the others' sums one
