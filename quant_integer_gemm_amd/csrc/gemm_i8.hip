@@ -11,15 +11,15 @@
 //
 // What bounds it, and what it reaches: large products are held by the card's
 // power (the clock falls from 2.4 to 1.75 GHz; zeros as data run at 2.4).  8192^3
-// 438 us, 2510 TOPS, the rate of a large product of the vendor's library on the
-// same card; 2630 tokens, 2 x 18944 x 3584 gated to bf16 312 us, 2290 TOPS; 18944
-// -> 3584 to fp32 154 us, 2320 TOPS.  Of the 8192^3 time, with 32 x 32 x 32 MFMAs,
-// a build without the copies took 16% less, one without the LDS reads 12%, one
-// with neither 27%.  Small products: launch, first loads and epilogue, 5 us, then
-// 0.25 us a step (3584 x 3584, 512 tokens 14.5 us).  Experts' products: the
+// 420 us, 2610 TOPS, above the vendor library's product on the same card (2500);
+// 2630 tokens, 2 x 18944 x 3584 gated to bf16 306 us, 2330 TOPS; 18944 -> 3584 to
+// fp32 148 us, 2420 TOPS (157 us with operands from HBM).  Of the 8192^3 time, an
+// earlier build without its copies took 16% less, one without the LDS reads 12%,
+// one with neither 27%.  Small products: launch, first loads and epilogue, 5 us,
+// then 0.25 us a step (3584 x 3584, 512 tokens 14.5 us).  Experts' products: the
 // weights' bytes up to about 50 rows an expert (5.0 TB/s), above that bytes and
-// power together (64 experts of 2 x 2368 x 3584, 15780 rows: 359 to 370 us; 300 us
-// with the weights of two experts for all, which stay in the caches).
+// power together (64 experts of 2 x 2368 x 3584, 15780 rows: 349 us; 300 us with
+// the weights of two experts for all, which stay in the caches).
 //
 // LDS rows are 128 bytes, eight 16-byte granules; granule g of row r is kept
 // at slot g ^ (r & 7), so that the eight lanes of a read phase (eight rows,
@@ -186,20 +186,18 @@ __device__ __forceinline__ Rows find_rows(const int32_t *plan, int ne, int mt)
 // GLU: of every 32 of the tile's weight rows the first 16 are gate rows and
 // the last 16 the up rows of the same outputs, so a wave holds both halves of
 // an output in the same lane and register.
-template <int BM, int BN, int WM, int WN, int S, bool SPLIT, bool GLU, bool EXPERTS, int YT>
+template <int BM, int BN, int WM, int WN, int S, int SB, bool SPLIT, bool GLU, bool EXPERTS, int YT>
 __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 {
     constexpr int NW = WM * WN;
     constexpr int TMAX = BM / WM / 32, TN = BN / WN / 32;
     constexpr int PAMAX = BM / 8 / NW, PB = BN / 8 / NW;   // 1 KB pieces a wave copies each step
-    constexpr int STAGE = (BM + BN) * BK;
+    constexpr int LDS = (S * BM + SB * BN) * BK;
     constexpr int BJ = GLU ? BN / 2 : BN;               // outputs of a tile
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TMAX >= 1 && TMAX <= 4 && TN >= 1, "tile");
-    static_assert(S == 2 || S >= 4, "stages");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[S * STAGE];
-    __shared__ float s_sq[BM];
-    __shared__ __attribute__((aligned(16))) float s_sw[BN], s_bias[BN];
-    __shared__ int32_t s_row[EXPERTS ? BM : 1];
+    static_assert((S == 2 && (SB == 2 || SB == 3)) || (S >= 4 && SB == S), "stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
+    static_assert(BM <= NW * 64 && BN <= NW * 64, "a thread a row");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -225,9 +223,11 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     int64_t t0 = (int64_t)mt * BM;
     int count;
     elem_t<YT> *y = static_cast<elem_t<YT> *>(g.y);
+    [[maybe_unused]] Rows rows = {0, 0, 0};
 
     if constexpr (EXPERTS) {
-        const Rows r = find_rows<BM>(g.plan, g.ne, mt);
+        rows = find_rows<BM>(g.plan, g.ne, mt);
+        const Rows &r = rows;
         count = r.count;
         if (r.e == g.ne) {
             // dropped rows: zeros
@@ -237,28 +237,12 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             }
             return;
         }
-        const int64_t rows = GLU ? 2 * g.od : g.od;
-        W += (int64_t)r.e * rows * g.ldw;
-        sw += (int64_t)r.e * rows;
-        if (bias) bias += (int64_t)r.e * rows;
-        for (int i = tid; i < BM; i += NW * 64) {
-            const int row = row_of(g.plan, g.ne, r, i, (int)g.nt);
-            s_row[i] = row;
-            s_sq[i] = g.sq[row / g.slots];
-        }
-        __syncthreads();
+        const int64_t wrows = GLU ? 2 * g.od : g.od;
+        W += (int64_t)r.e * wrows * g.ldw;
+        sw += (int64_t)r.e * wrows;
+        if (bias) bias += (int64_t)r.e * wrows;
     } else {
         count = (int)(g.nt - t0 < BM ? g.nt - t0 : BM);
-        for (int i = tid; i < BM; i += NW * 64) s_sq[i] = g.sq[t0 + (i < count ? i : count - 1)];
-    }
-
-    // scales and biases of the tile's weight rows, in the order of its LDS rows
-    for (int i = tid; i < BN; i += NW * 64) {
-        int64_t j = j0 + (GLU ? (i >> 5) * 16 + (i & 15) : i);
-        j = j < g.od ? j : g.od - 1;
-        if (GLU && (i & 16)) j += g.od;
-        s_sw[i] = sw[j];
-        s_bias[i] = bias ? bias[j] : 0.0f;
     }
 
     // The rows that this lane copies: piece p of the wave holds rows
@@ -271,7 +255,8 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
     for (int p = 0; p < PAMAX; ++p) {
         const int r = 8 * (NW * p + wave) + lr;
         if constexpr (EXPERTS)
-            aptr[p] = reinterpret_cast<uintptr_t>(g.q + (int64_t)(s_row[r] / g.slots) * g.ldq);
+            aptr[p] = reinterpret_cast<uintptr_t>(
+                g.q + (int64_t)(row_of(g.plan, g.ne, rows, r, (int)g.nt) / g.slots) * g.ldq);
         else
             aoff[p] = (uint32_t)(r < count ? r : count - 1) * (uint32_t)g.ldq;
     }
@@ -303,6 +288,29 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         if (kfirst + nk < all) tail = BK;
     }
 
+    // Scales, biases and rows for the epilogue, one of each a thread: loaded
+    // before the last step and put into LDS behind it, since the stages may take
+    // all of the LDS.  Weight rows in the order of their LDS rows.
+    float e_sq = 0.0f, e_sw = 0.0f, e_bias = 0.0f;
+    [[maybe_unused]] int e_row = 0;
+    auto fetch = [&]() {
+        if (tid < BM) {
+            if constexpr (EXPERTS) {
+                e_row = row_of(g.plan, g.ne, rows, tid, (int)g.nt);
+                e_sq = g.sq[e_row / g.slots];
+            } else {
+                e_sq = g.sq[t0 + (tid < count ? tid : count - 1)];
+            }
+        }
+        if (tid < BN) {
+            int64_t j = j0 + (GLU ? (tid >> 5) * 16 + (tid & 15) : tid);
+            j = j < g.od ? j : g.od - 1;
+            if (GLU && (tid & 16)) j += g.od;
+            e_sw = sw[j];
+            if (bias) e_bias = bias[j];
+        }
+    };
+
     const int wm = wave / WN, wn = wave % WN;
     const int l16 = lane & 15, quad = lane >> 4;
 
@@ -312,29 +320,24 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         constexpr int TM = frags;
         constexpr int PA = TM * WM * 32 / 8 / NW;   // pieces of the activations a wave copies
         static_assert(PA * 8 * NW == TM * WM * 32, "whole pieces");
-        // The stage that holds step kt.
-        auto buffer = [&](int kt) -> uint32_t {
-            if constexpr ((S & (S - 1)) == 0)
-                return (uint32_t)kt & (S - 1);
-            else
-                return (uint32_t)kt % S;
-        };
+        // Where step kt's activations and weights are kept: S and SB stages.
+        auto a_at = [&](int kt) -> uint32_t { return (uint32_t)kt % S * (BM * BK); };
+        auto b_at = [&](int kt) -> uint32_t { return S * BM * BK + (uint32_t)kt % SB * (BN * BK); };
         // Copy piece p of step kt: first the wave's PA pieces of the activations,
         // then its PB pieces of the weights.
         auto copy = [&](int kt, int p) {
-            const uint32_t dst = l0 + buffer(kt) * STAGE;
             const uint64_t k0 = (uint64_t)(kfirst + kt) * BK;
             uint32_t go = 16 * gran;
             if (kt == nk - 1 && (int)go >= tail) go = 0;
             if (p < PA) {
-                const uint32_t d = dst + 1024 * (NW * p + wave);
+                const uint32_t d = l0 + a_at(kt) + 1024 * (NW * p + wave);
                 if constexpr (EXPERTS)
                     copy16_at(aptr[p] + k0 + go, d);
                 else
                     copy16(abase0 + k0, aoff[p] + go, d);
             } else {
                 p -= PA;
-                copy16(bbase + k0 + (bup[p] ? uphalf : 0), boff[p] + go, dst + BM * BK + 1024 * (NW * p + wave));
+                copy16(bbase + k0 + (bup[p] ? uphalf : 0), boff[p] + go, l0 + b_at(kt) + 1024 * (NW * p + wave));
             }
         };
         // Step kt's bytes past id become zero in the activations' rows.
@@ -369,19 +372,19 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         // Chunk c of a step is 64 bytes of every row: granules 4 c .. 4 c + 3,
         // one for each quarter of the wave.  Rows of one lane differ by multiples
         // of 16, so its slot is the same in all of them.
-        constexpr int NC = BK / 64, NP = PA + PB, P3 = NP / 2;
+        constexpr int NC = BK / 64, NP = PA + PB, P3 = SB == 3 ? PA : NP / 2;
         uint32_t aat[NC], bat[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const uint32_t slot = 16 * ((4 * c + quad) ^ (l16 & 7));
             aat[c] = (wm * FM * 16 + l16) * BK + slot;
-            bat[c] = (BM + wn * FN * 16 + l16) * BK + slot;
+            bat[c] = (wn * FN * 16 + l16) * BK + slot;
         }
         auto read_a = [&](int kt, int c, int m) {
-            return *reinterpret_cast<const i32x4 *>(lds + buffer(kt) * STAGE + aat[c] + m * 16 * BK);
+            return *reinterpret_cast<const i32x4 *>(lds + a_at(kt) + aat[c] + m * 16 * BK);
         };
         auto read_b = [&](int kt, int c, int n) {
-            return *reinterpret_cast<const i32x4 *>(lds + buffer(kt) * STAGE + bat[c] + n * 16 * BK);
+            return *reinterpret_cast<const i32x4 *>(lds + b_at(kt) + bat[c] + n * 16 * BK);
         };
         constexpr std::true_type yes;
         constexpr std::false_type no;
@@ -394,6 +397,12 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             // next step has landed and its first blocks are read; the copies go
             // out one by one in that quarter (pieces up to P3 of the step after
             // the next, whose stage is free then) and in the first (the others).
+            // With three stages of weights (SB) they are copied two steps ahead
+            // in the first quarter, and the activations in the last: weights
+            // come from HBM, whose latency is longer than a step (18944 -> 3584,
+            // 2630 tokens, operands not in the caches: 192 us with two stages,
+            // 157 us with three; touching the lines ahead of the copies instead
+            // cost more than it hid).
             constexpr int MS = NC * FM, AFTER = MS / 4, LA = AFTER < 3 ? AFTER : 3;
             i32x4 ra[4], rb[NC][FN];
             auto step = [&](auto late, auto early, auto next, int kt) {
@@ -403,10 +412,11 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
                     const int in = s - (MS - AFTER);   // row step of the last quarter
                     if (next && in == 0) {
                         // the next step has landed, and nobody reads this one any more
-                        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                        // (all but the weights of the step after it, issued last)
+                        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(SB == 3 && late ? PB : 0) : "memory");
                         __syncthreads();
                         if constexpr (!early)
-                            if (tail < BK) clear_tail(lds + buffer(kt + 1) * STAGE);
+                            if (tail < BK) clear_tail(lds + a_at(kt + 1));
                     }
 #pragma unroll
                     for (int n = 0; n < FN; ++n) {
@@ -431,7 +441,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
                         if (late && s < AFTER) {
 #pragma unroll
                             for (int i = 0; i < NP - P3; ++i)
-                                if (i * AFTER * FN / (NP - P3) == s * FN + n) copy(kt + 1, P3 + i);
+                                if (i * AFTER * FN / (NP - P3) == s * FN + n) copy(kt + SB - 1, P3 + i);
                         } else if (early && in >= 0) {
 #pragma unroll
                             for (int i = 0; i < P3; ++i)
@@ -443,7 +453,13 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             };
 #pragma unroll
             for (int p = 0; p < NP; ++p) copy(0, p);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (SB == 3 && nk > 1) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p) copy(1, p);
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NP) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
             __syncthreads();
             if (nk == 1 && tail < BK) clear_tail(lds);
 #pragma unroll
@@ -451,11 +467,14 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
 #pragma unroll
             for (int t = 0; t < LA; ++t) ra[t] = read_a(0, 0, t);
             if (nk > 1) {
+                if constexpr (SB == 2) {
 #pragma unroll
-                for (int p = 0; p < P3; ++p) copy(1, p);
+                    for (int p = 0; p < P3; ++p) copy(1, p);
+                }
                 for (int kt = 0; kt < nk - 2; ++kt) step(yes, yes, yes, kt);
-                step(yes, no, yes, nk - 2);
+                step(std::bool_constant<SB == 2>{}, no, yes, nk - 2);
             }
+            fetch();
             step(no, no, no, nk - 1);
         } else {
             // Body kt multiplies step kt, held in registers, and reads step
@@ -502,7 +521,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             else
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             __syncthreads();
-            if (nk <= 2 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
+            if (nk <= 2 && tail < BK) clear_tail(lds + a_at(nk - 1));
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
 #pragma unroll
@@ -514,8 +533,9 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             for (; kt <= nk - S; ++kt) body(yes, yes, kt);
             for (; kt < nk - 1; ++kt) {
                 body(no, yes, kt);
-                if (kt + 2 == nk - 1 && tail < BK) clear_tail(lds + buffer(nk - 1) * STAGE);
+                if (kt + 2 == nk - 1 && tail < BK) clear_tail(lds + a_at(nk - 1));
             }
+            fetch();
             body(no, no, kt);
         }
 
@@ -569,8 +589,20 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
         constexpr int PITCH = NO * 16 * EB + 16;           // 16 more: the rows' writes on different banks
         constexpr int CH = NO * EB;                        // 16-byte chunks a row
         constexpr int PER = 16 / EB;                       // outputs of a chunk
-        static_assert(NW * 32 * PITCH <= S * STAGE, "the waves' parts");
+        float *s_sq = reinterpret_cast<float *>(lds + NW * 32 * PITCH);
+        float *s_sw = s_sq + BM, *s_bias = s_sw + BN;
+        int32_t *s_row = reinterpret_cast<int32_t *>(s_bias + BN);
+        static_assert(NW * 32 * PITCH + (2 * BM + 2 * BN) * 4 <= LDS, "the waves' parts and the scales");
         __syncthreads();   // nobody reads the stages any more
+        if (tid < BM) {
+            s_sq[tid] = e_sq;
+            if constexpr (EXPERTS) s_row[tid] = e_row;
+        }
+        if (tid < BN) {
+            s_sw[tid] = e_sw;
+            s_bias[tid] = e_bias;
+        }
+        __syncthreads();
         uint8_t *mine = lds + wave * (32 * PITCH);
         const int64_t jw = j0 + wn * NO * 16;
 #pragma unroll
@@ -806,7 +838,7 @@ static int launch_gemv(I8Args a, hipStream_t stream)
                          a);
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool SPLIT, bool GLU, bool EXPERTS, int YT>
+template <int BM, int BN, int WM, int WN, int S, int SB, bool SPLIT, bool GLU, bool EXPERTS, int YT>
 static int launch_tile(I8Args a, int64_t od, int64_t nt, hipStream_t stream)
 {
     constexpr int BJ = GLU ? BN / 2 : BN;
@@ -817,7 +849,7 @@ static int launch_tile(I8Args a, int64_t od, int64_t nt, hipStream_t stream)
     if (n > 0x7fffffff) return -1;
     a.nbt = (int)nbt;
     a.nbj = (int)nbj;
-    return launch_kernel(gemm_i8_kernel<BM, BN, WM, WN, S, SPLIT, GLU, EXPERTS, YT>, dim3((unsigned)n),
+    return launch_kernel(gemm_i8_kernel<BM, BN, WM, WN, S, SB, SPLIT, GLU, EXPERTS, YT>, dim3((unsigned)n),
                          dim3(WM * WN * 64), stream, a);
 }
 
@@ -825,15 +857,15 @@ static int launch_tile(I8Args a, int64_t od, int64_t nt, hipStream_t stream)
 // round of tiles that leaves CUs without one, `full` as a CU's share when all
 // are busy, where the card's power holds the clock down (1.75 GHz under the
 // 256 x 256 tiles against 2.4); `ends` are a round's first loads and epilogue.
-// Measured at 8192^3 (full: 438 us with 256 x 256, 464 with 192 x 256, 740 with
-// 64 x 128), and with 2630 tokens of 18944 -> 3584 (168, 154 and 244 us) and 64
+// Measured at 8192^3 (full: 420 us with 256 x 256, 452 with 192 x 256, 740 with
+// 64 x 128), and with 2630 tokens of 18944 -> 3584 (167, 148 and 244 us) and 64
 // to 512 of 3584 -> 3584 (alone).
 struct TileCost {
     int bm, bn, per_cu;
     double alone, full, ends;
 };
-constexpr TileCost COST_256 = {256, 256, 1, 1.05, 1.62, 6.0};
-constexpr TileCost COST_192 = {192, 256, 1, 0.84, 1.26, 6.0};
+constexpr TileCost COST_256 = {256, 256, 1, 1.05, 1.55, 6.0};
+constexpr TileCost COST_192 = {192, 256, 1, 0.84, 1.21, 6.0};
 constexpr TileCost COST_64 = {64, 128, 1, 0.30, 0.32, 3.0};
 constexpr TileCost COST_64S = {64, 128, 3, 0.54, 0.32, 3.0};   // two stages: three workgroups a CU
 
@@ -860,7 +892,7 @@ constexpr int64_t EXPERTS_GEMV_BYTES = int64_t(24) << 20, EXPERTS_GEMV_ROWS = 16
 // Rows of an expert, on average, from which the larger tiles are faster, and
 // the tiles it takes for that.  64 experts' 4736 x 3584, us for 64 x 128,
 // 128 x 128 and 256 x 256: 1.5 rows each 144, 147, 163; 12 rows 203, 198, 214;
-// 48 rows 222, 215, 225; 246 rows 603, 440, 368.
+// 48 rows 222, 214, 221; 246 rows 603, 435, 349.
 constexpr double ROWS_128 = 8, ROWS_256 = 96, TILES_128 = 256, TILES_256 = 192;
 // Split sums: shares of at least SPLIT_STEPS steps, a workgroup a CU, and at
 // most SPLIT_MOST shares: the last share to arrive reads the others' sums one
@@ -877,18 +909,18 @@ static int pick_dense(I8Args a, hipStream_t stream)
     const double c256 = cost<GLU>(COST_256, a), c192 = cost<GLU>(COST_192, a);
     const double c64 = cost<GLU>(COST_64, a), c64s = cost<GLU>(COST_64S, a);
     if (std::min(c64, c64s) >= std::min(c192, c256)) {
-        if (c192 < c256) return launch_tile<192, 256, 2, 4, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
-        return launch_tile<256, 256, 2, 4, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
+        if (c192 < c256) return launch_tile<192, 256, 2, 4, 2, 3, false, GLU, false, YT>(a, a.od, a.nt, stream);
+        return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, false, YT>(a, a.od, a.nt, stream);
     }
-    if (c64s < c64) return launch_tile<64, 128, 2, 2, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    if (c64s < c64) return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
     const int64_t tiles = (a.nt + 63) / 64 * ((a.od + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
     const int64_t nk = (a.id + BK - 1) / BK;
     const int64_t splits = std::min<int64_t>(std::min<int64_t>(nk / SPLIT_STEPS, SPLIT_MOST), SPLIT_CUS / tiles);
     if (a.part && splits >= 2 && tiles * splits <= SPLIT_SLOTS && tiles <= SPLIT_TILES) {
         a.splits = (int)splits;
-        return launch_tile<64, 128, 2, 2, 4, true, GLU, false, YT>(a, a.od, a.nt, stream);
+        return launch_tile<64, 128, 2, 2, 4, 4, true, GLU, false, YT>(a, a.od, a.nt, stream);
     }
-    return launch_tile<64, 128, 2, 2, 4, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    return launch_tile<64, 128, 2, 2, 4, 4, false, GLU, false, YT>(a, a.od, a.nt, stream);
 }
 
 template <bool GLU, int YT>
@@ -902,10 +934,10 @@ static int pick_experts(const I8Args &a, hipStream_t stream)
         return ((double)a.nt / bm + 0.5 * (double)used) * (double)((rows + bn - 1) / bn);
     };
     if (each >= ROWS_256 && tiles(256, 256) >= TILES_256)
-        return launch_tile<256, 256, 2, 4, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+        return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
     if (each >= ROWS_128 && tiles(128, 128) >= TILES_128)
-        return launch_tile<128, 128, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    return launch_tile<64, 128, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+        return launch_tile<128, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
 }
 
 template <int YT>
