@@ -891,8 +891,8 @@ constexpr int64_t GEMV_BYTES = int64_t(40) << 20;
 constexpr int64_t EXPERTS_GEMV_BYTES = int64_t(24) << 20, EXPERTS_GEMV_ROWS = 16;
 // Rows of an expert, on average, from which the larger tiles are faster, and
 // the tiles it takes for that.  64 experts' 4736 x 3584, us for 64 x 128,
-// 128 x 128 and 256 x 256: 1.5 rows each 144, 147, 163; 12 rows 203, 198, 214;
-// 48 rows 222, 214, 221; 246 rows 603, 435, 349.
+// 128 x 256 and 256 x 256: 4.5 rows each 173, 184, 208; 12 rows 204, 192, 214; 48
+// rows 220, 206, 221; 246 rows 599, 396, 349.
 constexpr double ROWS_128 = 8, ROWS_256 = 96, TILES_128 = 256, TILES_256 = 192;
 // Split sums: shares of at least SPLIT_STEPS steps, a workgroup a CU, and at
 // most SPLIT_MOST shares: the last share to arrive reads the others' sums one
@@ -935,8 +935,8 @@ static int pick_experts(const I8Args &a, hipStream_t stream)
     };
     if (each >= ROWS_256 && tiles(256, 256) >= TILES_256)
         return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    if (each >= ROWS_128 && tiles(128, 128) >= TILES_128)
-        return launch_tile<128, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    if (each >= ROWS_128 && tiles(128, 256) >= TILES_128)
+        return launch_tile<128, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
     return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
 }
 
