@@ -393,26 +393,27 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
             // A step is MS row steps: one block of tokens against the FN blocks of
             // weights, chunk after chunk.  Token blocks are read LA row steps
             // ahead into a ring of four, weight blocks while the chunk before
-            // theirs is multiplied.  In the last quarter (AFTER row steps) the
-            // next step has landed and its first blocks are read; the copies go
-            // out one by one in that quarter (pieces up to P3 of the step after
-            // the next, whose stage is free then) and in the first (the others).
+            // theirs is multiplied.  In the last LA row steps all of this step's
+            // blocks have been read, the next step has landed and its first blocks
+            // are read; the copies go out one by one there (pieces up to P3 of the
+            // step after the next, whose stage is free then) and in the first
+            // quarter, FIRST row steps (the others).
             // With three stages of weights (SB) they are copied two steps ahead
-            // in the first quarter, and the activations in the last: weights
+            // in the first quarter, and the activations at the end: weights
             // come from HBM, whose latency is longer than a step (18944 -> 3584,
             // 2630 tokens, operands not in the caches: 192 us with two stages,
             // 157 us with three; touching the lines ahead of the copies instead
             // cost more than it hid).
-            constexpr int MS = NC * FM, AFTER = MS / 4, LA = AFTER < 3 ? AFTER : 3;
+            constexpr int MS = NC * FM, FIRST = MS / 4, LA = FIRST < 3 ? FIRST : 3;
             i32x4 ra[4], rb[NC][FN];
             auto step = [&](auto late, auto early, auto next, int kt) {
 #pragma unroll
                 for (int s = 0; s < MS; ++s) {
                     const int c = s / FM, m = s % FM;
-                    const int in = s - (MS - AFTER);   // row step of the last quarter
+                    const int in = s - (MS - LA);   // row step of the last part
                     if (next && in == 0) {
-                        // the next step has landed, and nobody reads this one any more
-                        // (all but the weights of the step after it, issued last)
+                        // the next step has landed (all but the weights of the step
+                        // after it, issued last), and nobody reads this one any more
                         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(SB == 3 && late ? PB : 0) : "memory");
                         __syncthreads();
                         if constexpr (!early)
@@ -428,24 +429,24 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
                             else if (next)
                                 ra[t & 3] = read_a(kt + 1, 0, t - MS);
                         }
-                        // weight block i of the coming chunk behind MFMA i of the quarter
-                        if (s < AFTER) {
+                        // the weight blocks of the coming chunk, evenly spread
+                        if (s < FIRST) {
 #pragma unroll
                             for (int i = 0; i < FN; ++i)
-                                if (i * AFTER == s * FN + n) rb[1][i] = read_b(kt, 1, i);
+                                if (i * FIRST == s * FN + n) rb[1][i] = read_b(kt, 1, i);
                         } else if (next && in >= 0) {
 #pragma unroll
                             for (int i = 0; i < FN; ++i)
-                                if (i * AFTER == in * FN + n) rb[0][i] = read_b(kt + 1, 0, i);
+                                if (i * LA == in * FN + n) rb[0][i] = read_b(kt + 1, 0, i);
                         }
-                        if (late && s < AFTER) {
+                        if (late && s < FIRST) {
 #pragma unroll
                             for (int i = 0; i < NP - P3; ++i)
-                                if (i * AFTER * FN / (NP - P3) == s * FN + n) copy(kt + SB - 1, P3 + i);
+                                if (i * FIRST * FN / (NP - P3) == s * FN + n) copy(kt + SB - 1, P3 + i);
                         } else if (early && in >= 0) {
 #pragma unroll
                             for (int i = 0; i < P3; ++i)
-                                if (i * AFTER * FN / P3 == in * FN + n) copy(kt + 2, i);
+                                if (i * LA * FN / P3 == in * FN + n) copy(kt + 2, i);
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     }
