@@ -311,7 +311,9 @@ def workspace(device=None, stream=None):
     that may overlap on different streams from sharing its arrival counters.
     Every call leaves the counters at zero; a call interrupted by a device
     fault does not, but such a fault also ends the HIP context the workspace
-    lives in."""
+    lives in.  In a capture, a pair that has none yet gets a new one at each
+    call, zeroed by the graph itself; graphs that share one made before must
+    not be replayed at the same time."""
     import torch
     index = None if device is None else torch.device(device).index
     if index is None:
@@ -323,8 +325,12 @@ def workspace(device=None, stream=None):
     key = (index, int(raw(index) if stream is None else stream.cuda_stream))
     ws = _workspaces.get(key)
     if ws is None:
-        ws = new_workspace(torch.device("cuda", index))
-        _workspaces[key] = ws
+        # zeroed on the stream that uses it first
+        with torch.cuda.stream(stream or torch.cuda.current_stream(index)):
+            ws = new_workspace(torch.device("cuda", index))
+            # a captured fill has not run yet, and runs with its own graph alone
+            if not torch.cuda.is_current_stream_capturing():
+                _workspaces[key] = ws
     return ws
 
 

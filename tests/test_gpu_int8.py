@@ -476,3 +476,34 @@ def test_given_stream_and_two_streams_at_once(qig):
             qig.mm_i8(*a, y=ys[s][i], ws=ws[s], stream=streams[s])
     torch.cuda.synchronize()
     assert all(torch.equal(y, y0) for r in ys for y in r)
+
+
+def test_default_workspace_in_captures_and_on_a_given_stream(qig):
+    """Split products whose workspace is the default one of a stream that has
+    none yet: two captures on one stream, the second replayed first, and a
+    stream passed to the call while another is current."""
+    g = _rng(13)
+    nt, od, id_ = 70, 200, 8192
+    q, W, sq, sw, _ = _operands(g, nt, od, id_, False)
+    a = (_dev(W), _dev(sw), _dev(q), _dev(sq))
+    want = qig.mm_i8(*a)
+    outs = [torch.zeros_like(want) for _ in range(3)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    graphs = []
+    for y in outs[:2]:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            for _ in range(2):
+                qig.mm_i8(*a, y=y, ws=qig.workspace(a[0].device))
+        graphs.append(gr)
+    for i in (1, 0, 1, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want), i
+    t = torch.cuda.Stream()
+    qig.mm_i8(*a, y=outs[2], ws=qig.workspace(a[0].device, t), stream=t)
+    t.synchronize()
+    assert torch.equal(outs[2], want)
+    assert qig.workspace(a[0].device, t).data_ptr() == qig.workspace(a[0].device, t).data_ptr()
