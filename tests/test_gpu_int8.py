@@ -507,3 +507,77 @@ def test_default_workspace_in_captures_and_on_a_given_stream(qig):
     t.synchronize()
     assert torch.equal(outs[2], want)
     assert qig.workspace(a[0].device, t).data_ptr() == qig.workspace(a[0].device, t).data_ptr()
+
+
+def _same_up_to_rounding(got, want, what):
+    """fp32 results of two kernels on the same integer sum, |bias| <= 4: the
+    conversion and two products round by 2^-24 of |y| + |bias| each, the
+    addition by 2^-24 of |y|, in both, so they differ by at most 8 (|y| +
+    |bias|) 2^-24."""
+    err = ((got.double() - want.double()).abs() / (want.double().abs() + 4.0)).max().item()
+    _say(what, err)
+    assert err <= 8 * 2.0 ** -24, what
+
+
+def test_rows_behind_32_bit_offsets(qig):
+    """Tensors whose last rows lie more than 2^31 elements or 2^32 bytes behind
+    their first, each checked against the same rows alone."""
+    torch.manual_seed(5)
+    nt, id_ = 270000, 16384                                   # x: 8.8 GB, q: 4.4 GB
+    x = torch.empty((nt, id_), dtype=torch.bfloat16, device="cuda").normal_()
+    q, s = qig.quantize_i8(x)
+    for lo, hi in ((0, 40), (131000, 131100), (nt - 40, nt)):
+        q1, s1 = qig.quantize_i8(x[lo:hi].clone())
+        assert torch.equal(q1, q[lo:hi]) and torch.equal(s1, s[lo:hi]), lo
+    del x
+    W, sw = qig.quantize_i8(torch.randn(24, id_, device="cuda"))
+    bias = torch.randn(24, device="cuda").clamp_(-4, 4)
+    y = torch.zeros((nt, 8192), device="cuda")[:, :24]        # 2.2e9 elements, 8.8 GB
+    qig.mm_i8(W, sw, q, s, bias=bias, y=y)
+    for lo, hi in ((0, 8), (131000, 131070), (262130, 262160), (nt - 9, nt)):
+        _same_up_to_rounding(y[lo:hi], qig.mm_i8(W, sw, q[lo:hi], s[lo:hi], bias=bias), f"rows {lo}")
+    del y
+    # experts: the same rows, every fourth of a second expert, the last dropped
+    W2, sw2 = torch.stack([W, W.flip(0)]), torch.stack([sw, sw.flip(0)])
+    ids = (torch.arange(nt, device="cuda", dtype=torch.int32) % 4 == 3).int()
+    ids[-1] = -1
+    plan = qig.plan_experts(ids, 2)
+    y = torch.zeros((nt, 8192), device="cuda")[:, :24]
+    y[-1] = 7
+    qig.mm_i8_experts(W2, sw2, q, s, plan, nt, y=y)
+    for lo, hi in ((0, 8), (131000, 131070), (262130, 262160), (nt - 9, nt)):
+        r = torch.arange(lo, hi, device="cuda")
+        for e in range(2):
+            rows = r[ids[lo:hi] == e]
+            _same_up_to_rounding(y[rows], qig.mm_i8(W2[e], sw2[e], q[rows], s[rows]), f"expert {e}, rows {lo}")
+    assert int(torch.count_nonzero(y[-1])) == 0
+    # h [2 * 135000][8192] of the same storage
+    w = torch.rand(nt // 2, 2, device="cuda")
+    z = qig.combine_experts(y, w)
+    for lo, hi in ((0, 8), (131065, 131080), (nt // 2 - 8, nt // 2)):
+        assert torch.equal(z[lo:hi], qig.combine_experts(y[2 * lo:2 * hi].clone(), w[lo:hi])), lo
+    del y, q
+    # weights: 2 x 1100 x 16384 of 130 experts, 4.7 GB
+    W = torch.randint(-127, 128, (130, 2200, id_), dtype=torch.int8, device="cuda")
+    sw = torch.rand(130, 2200, device="cuda") * 1e-4
+    q, s = qig.quantize_i8(torch.randn(60, id_, device="cuda"))
+    for n in (3, 60):
+        ids = torch.tensor([129, 119, 0] * 20, dtype=torch.int32, device="cuda")[:n]
+        y = qig.mm_i8_experts(W, sw, q[:n], s[:n], qig.plan_experts(ids, 130), n, glu=True)
+        for e in (129, 119, 0):
+            rows = (ids == e).nonzero()[:, 0]
+            a, b = (qig.mm_i8(W[e, i:i + 1100], sw[e, i:i + 1100], q[rows], s[rows]).double() for i in (0, 1100))
+            want = a * torch.sigmoid(a) * b
+            # in 2^-24 of |a b|: a and b are 4 roundings off in either kernel
+            # (times silu's slope, 1.1, for a), the activation 8 + 3 |a|
+            err = ((y[rows].double() - want).abs() / ((26 + 3 * a.abs()) * (a * b).abs() + 2.0 ** -100)).max().item()
+            _say("expert", e, err)
+            assert err <= 2.0 ** -24, e
+    del W, y
+    # logits [8.5e6][512] fp16, 8.7 GB
+    nt = 8500000
+    l = torch.empty((nt, 512), dtype=torch.float16, device="cuda").normal_()
+    ids, w = qig.route_experts(l, 4)
+    for lo, hi in ((0, 40), (4194290, 4194320), (8388590, 8388620), (nt - 9, nt)):
+        i1, w1 = qig.route_experts(l[lo:hi].clone(), 4)
+        assert torch.equal(i1, ids[lo:hi]) and torch.equal(w1, w[lo:hi]), lo
