@@ -317,7 +317,8 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kerne
             const int w0 = __ffsll((unsigned long long)__ballot(rank == a.topk_groups - 1)) - 1;
             const int w1 = __ffsll((unsigned long long)__ballot(rank == a.topk_groups)) - 1;
             const float size12s = __builtin_fmaxf(lane_value(size12, w0), lane_value(size12, w1));
-            near_groups = lane_value(score, w0) - lane_value(score, w1) <= tol + 0x1p-21f * size12s;
+            // (sums that overflow 32 bits need 64, too: their difference is NaN)
+            near_groups = !(lane_value(score, w0) - lane_value(score, w1) > tol + 0x1p-21f * size12s);
         }
         lds_order();
 #pragma unroll

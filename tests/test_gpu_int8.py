@@ -581,3 +581,17 @@ def test_rows_behind_32_bit_offsets(qig):
     for lo, hi in ((0, 40), (4194290, 4194320), (8388590, 8388620), (nt - 9, nt)):
         i1, w1 = qig.route_experts(l[lo:hi].clone(), 4)
         assert torch.equal(i1, ids[lo:hi]) and torch.equal(w1, w[lo:hi]), lo
+
+
+def test_routing_group_sums_beyond_fp32(qig):
+    """Two largest biases whose sum no fp32 holds: the groups are told apart in
+    64 bits all the same, and infinite biases tie towards the lower group."""
+    logits = torch.zeros(1, 8, device="cuda")
+    route = lambda b, **kw: qig.route_experts(logits, 2, score="sigmoid", groups=4, topk_groups=1, group_top=2,  # noqa: E731
+                                              bias=torch.tensor(b, device="cuda"), **kw)[0].tolist()
+    assert route([3e38, 2e38, 3e38, 3.1e38, 3e38, 1.5e38, 0, 0]) == [[3, 2]]
+    assert route([-3.3e38, -3e38, -3.2e38, -3e38, -3.3e38, -3.1e38, -3.3e38, -3.2e38]) == [[3, 2]]
+    inf = float("inf")
+    assert route([0, 0, inf, 1, inf, 5, inf, inf]) == [[2, 3]]
+    assert route([-inf, -inf, -inf, -inf, -inf, 0, -inf, -inf]) == [[5, -1]]
+    assert route([-inf, -inf, float("nan"), -3e38, -inf, -inf, -3.3e38, -3.3e38]) == [[3, -1]]
