@@ -886,15 +886,21 @@ static double cost(const TileCost &c, const I8Args &a)
 // tokens 38 us against 21 us.
 constexpr int64_t GEMV_BYTES = int64_t(40) << 20;
 // For experts: weights of the experts that have rows, and rows of each.  Above
-// it tiles keep more of the weights' loads in flight: 12 experts' 4736 x 3584
-// with one row each 41 us against 33 us, but 6 experts' 1000 x 2000 8 us against
-// 12 us.
+// it tiles keep more of the weights' loads in flight: 6 experts' 4736 x 3584
+// with one row each 23.8 us against 19.4 us, but 6 experts' 1024 x 2048 8.5 us
+// against 9.3 us, 4 experts' 700 x 5000 8.4 us against 13.7 us.
 constexpr int64_t EXPERTS_GEMV_BYTES = int64_t(24) << 20, EXPERTS_GEMV_ROWS = 16;
 // Rows of an expert, on average, from which the larger tiles are faster, and
-// the tiles it takes for that.  64 experts' 4736 x 3584, us for 64 x 128,
-// 128 x 256 and 256 x 256: 4.5 rows each 173, 184, 208; 12 rows 204, 192, 214; 48
-// rows 220, 206, 221; 246 rows 599, 396, 349.
-constexpr double ROWS_128 = 8, ROWS_256 = 96, TILES_128 = 256, TILES_256 = 192;
+// the tiles it takes for that.  With few rows what counts is how evenly the
+// weights' bytes spread over the CUs and how many are in flight: 32 x 128 tiles
+// with four stages, two workgroups a CU.  64 experts' 4736 x 3584, us for
+// 32 x 128, 64 x 128, 128 x 256 and 256 x 256: 24 rows (23 experts) 73, 88, 85, -;
+// 4.5 rows each 175, 173, 184, 208; 15 rows 192, 205, 194, -; 48 rows -, 220, 206,
+// 221; 246 rows -, 599, 396, 349.  3584 x 2368, 6 rows: 98, 106, 111, -.  Where
+// 64 x 128 tiles are no more than the CUs (TILES_64) their deep form: 8 experts'
+// 2048 x 4096, 64 rows each 19.5 against 24.4 us; 2000 x 2048, 128 rows, 320 tiles,
+// 20.5 against 17.2.
+constexpr double ROWS_64 = 16, ROWS_256 = 96, TILES_64 = 256, TILES_128 = 256, TILES_256 = 192;
 // Split sums: shares of at least SPLIT_STEPS steps, a workgroup a CU, and at
 // most SPLIT_MOST shares: the last share to arrive reads the others' sums one
 // after the other (18944 -> 3584, 32 tokens: 45 us whole, 21 us in four, 28 us
@@ -936,9 +942,12 @@ static int pick_experts(const I8Args &a, hipStream_t stream)
     };
     if (each >= ROWS_256 && tiles(256, 256) >= TILES_256)
         return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    if (each >= ROWS_128 && tiles(128, 256) >= TILES_128)
+    if (each < ROWS_64) return launch_tile<32, 128, 1, 4, 4, 4, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    if (tiles(128, 256) >= TILES_128)
         return launch_tile<128, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    if (tiles(64, 128) > TILES_64)
+        return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    return launch_tile<64, 128, 2, 2, 4, 4, false, GLU, true, YT>(a, a.od, a.nt, stream);
 }
 
 template <int YT>
