@@ -595,3 +595,62 @@ def test_routing_group_sums_beyond_fp32(qig):
     assert route([0, 0, inf, 1, inf, 5, inf, inf]) == [[2, 3]]
     assert route([-inf, -inf, -inf, -inf, -inf, 0, -inf, -inf]) == [[5, -1]]
     assert route([-inf, -inf, float("nan"), -3e38, -inf, -inf, -3.3e38, -3.3e38]) == [[3, -1]]
+
+
+# (tokens, k, experts, weight rows): few rows of many experts (weights beyond the register kernel's range), few tiles,
+# more than the CUs, and enough for 128- and 256-row tiles
+EXPERT_TILES = {"few rows": (12, 6, 64, 0), "few tiles": (40, 2, 3, 406), "tiles": (100, 4, 8, 3350),
+                "128 rows": (80, 4, 16, 6430), "256 rows": (210, 4, 8, 7010)}
+
+
+@pytest.mark.parametrize("id_", [17, 129, 256, 300, 512, 600, 1000])
+@pytest.mark.parametrize("form", list(EXPERT_TILES))
+def test_experts_product_every_tile(qig, form, id_):
+    """Each tile form through one to eight steps, whole and with a tail, on
+    ragged rows and outputs: the first, middle and last experts' outputs."""
+    nt, k, ne, rows = EXPERT_TILES[form]
+    rows = rows or (25400000 // (ne * id_) + 7) // 2 * 2
+    glu = (id_ + ne) % 2 == 0
+    od = rows // 2 if glu else rows
+    torch.manual_seed(id_)
+    _say("mm_i8_experts", form, id_, rows, "glu" if glu else "")
+    W = torch.randint(-128, 128, (ne, rows, _pad(id_)), dtype=torch.int8, device="cuda")[:, :, :id_]
+    sw = torch.rand(ne, rows, device="cuda") * 0.02 + 1e-4
+    q = torch.randint(-127, 128, (nt, _pad(id_)), dtype=torch.int8, device="cuda")[:, :id_]
+    sq = (torch.rand(nt, device="cuda") * 0.02 + 1e-3) / max(1.0, id_ ** 0.5 / 4)
+    bias = torch.randn(ne, rows, device="cuda")
+    ids = torch.rand(nt, ne, device="cuda").argsort(1)[:, :k].int().contiguous()
+    ids[0] = ne - 1                                        # the same expert in every slot
+    ids[1, 0] = -1
+    y = torch.full((nt * k, od + 3), 7.0, device="cuda")
+    qig.mm_i8_experts(W, sw, q, sq, qig.plan_experts(ids, ne), nt * k, bias=bias, glu=glu, y=y[:, :od])
+    assert bool((y[:, od:] == 7.0).all()) and bool((y[k, :od] == 0).all())
+    flat = ids.flatten().cpu().numpy()
+    for e in (0, ne // 2, ne - 1):
+        mine = np.flatnonzero(flat == e)
+        want, allow = ref.product(q.cpu().numpy()[mine // k], sq.cpu().numpy()[mine // k], W[e].cpu().numpy(),
+                                  sw[e].cpu().numpy(), bias[e].cpu().numpy(), glu, "float32")
+        _check(y[torch.from_numpy(mine).cuda()][:, :od], want, allow, (form, e))
+
+
+@pytest.mark.parametrize("id_", [17, 129, 256, 300, 512, 600, 1000])
+@pytest.mark.parametrize("nt,rows", [(600, 4002), (1530, 7930), (2630, 4790)])
+def test_product_every_tile(qig, nt, rows, id_):
+    """The larger tiles through one to eight steps, whole and with a tail, on
+    ragged tokens and outputs: sampled tokens' outputs."""
+    glu = id_ % 3 == 0
+    od = rows // 2 if glu else rows
+    torch.manual_seed(id_)
+    _say("mm_i8", nt, rows, id_, "glu" if glu else "")
+    W = torch.randint(-128, 128, (rows, _pad(id_)), dtype=torch.int8, device="cuda")[:, :id_]
+    sw = torch.rand(rows, device="cuda") * 0.02 + 1e-4
+    q = torch.randint(-127, 128, (nt, _pad(id_)), dtype=torch.int8, device="cuda")[:, :id_]
+    sq = (torch.rand(nt, device="cuda") * 0.02 + 1e-3) / max(1.0, id_ ** 0.5 / 4)
+    bias = torch.randn(rows, device="cuda")
+    y = torch.full((nt + 1, od + 3), 7.0, device="cuda")
+    qig.mm_i8(W, sw, q, sq, bias=bias, glu=glu, y=y[:nt, :od])
+    assert bool((y[:, od:] == 7.0).all()) and bool((y[nt] == 7.0).all())
+    t = torch.cat([torch.arange(3), torch.randint(0, nt, (40,)), torch.arange(nt - 20, nt)])
+    want, allow = ref.product(q.cpu().numpy()[t], sq.cpu().numpy()[t], W.cpu().numpy(), sw.cpu().numpy(),
+                              bias.cpu().numpy(), glu, "float32")
+    _check(y[t.cuda()][:, :od], want, allow, (nt, rows, id_))
