@@ -97,6 +97,13 @@ __device__ __forceinline__ void load_run(const E *p, int n, float (&o)[NS])
     }
 }
 
+// The group of expert e.  e < 512, so the rounding of by_size adds less than
+// 2^-11 to e / size, which is at least 2^-9 below the next integer.
+__device__ __forceinline__ int group_of(const RouteArgs &a, int e)
+{
+    return (int)(((uint32_t)e * a.by_size) >> 20);
+}
+
 // One wave chooses a token's experts in 64 bits: lane l holds experts l,
 // l + 64, ...  Returns the expert of slot `lane` (-1: none).
 template <int NS, int T>
@@ -144,7 +151,7 @@ __device__ int route_exact(const RouteArgs &a, const elem_t<T> *l, double *s_c, 
             c[i] = -INFINITY;
         }
     if (a.groups > 1) {
-        const int size = a.ne / a.groups;
+        const int size = (int)a.size;
 #pragma unroll
         for (int i = 0; i < NS; ++i) s_c[lane + 64 * i] = c[i];
         lds_order();
@@ -168,7 +175,7 @@ __device__ int route_exact(const RouteArgs &a, const elem_t<T> *l, double *s_c, 
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int e = lane + 64 * i;
-            if (e < a.ne && !s_keep[e / size]) ok[i] = false;
+            if (e < a.ne && !s_keep[group_of(a, e)]) ok[i] = false;
         }
     }
     int my_id = -1;
@@ -273,26 +280,26 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kerne
     for (int i = 0; i < NS; ++i) key[i] = ok[i] && c[i] > -INFINITY ? order_key(c[i]) : 0u;
     bool near_groups = false;
     if (a.groups > 1) {
-        const int size = a.ne / a.groups;
+        const int size = (int)a.size;
         uint32_t *s_k = reinterpret_cast<uint32_t *>(s_all[wave]);
         uint8_t *s_keep = s_keeps[wave];
 #pragma unroll
         for (int i = 0; i < NS; ++i) s_k[lane * NS + i] = key[i];
         lds_order();
         // `lanes` lanes a group (a power of two), each over every lanes-th expert
-        int lanes = 1;
-        while (2 * lanes * a.groups <= 64) lanes *= 2;
-        const int g = lane / lanes;
+        const int lanes = 1 << a.lane_bits, g = lane >> a.lane_bits, in = lane & (lanes - 1);
         uint32_t b1 = 0, b2 = 0;
         if (g < a.groups)
-            for (int e = g * size + lane % lanes; e < (g + 1) * size; e += lanes) {
+            for (int e = g * size + in; e < (g + 1) * size; e += lanes) {
                 const uint32_t v = s_k[e];
                 const uint32_t low = b1 < v ? b1 : v;
                 b2 = low > b2 ? low : b2;
                 b1 = b1 > v ? b1 : v;
             }
         for (int d = 1; d < lanes; d *= 2) {
-            const uint32_t o1 = (uint32_t)__shfl_xor((int)b1, d), o2 = (uint32_t)__shfl_xor((int)b2, d);
+            const int from = (lane ^ d) * 4;
+            const uint32_t o1 = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)b1);
+            const uint32_t o2 = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)b2);
             const uint32_t low = b1 < o1 ? b1 : o1;
             b2 = b2 > o2 ? b2 : o2;
             b2 = low > b2 ? low : b2;
@@ -306,12 +313,12 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kerne
             size12 += __builtin_fabsf(key_value(b2));
         }
         int rank = 64;   // of the group, in its first lane
-        if (lane % lanes == 0 && g < a.groups) rank = 0;
+        if (in == 0 && g < a.groups) rank = 0;
         for (int o = 0; o < a.groups; ++o) {
             const float other = lane_value(score, o * lanes);
             rank += other > score || (other == score && o < g);
         }
-        if (lane % lanes == 0 && g < a.groups) s_keep[g] = rank < a.topk_groups;
+        if (in == 0 && g < a.groups) s_keep[g] = rank < a.topk_groups;
         if (!by_logit && a.topk_groups < a.groups) {
             // the last group that stays against the first that goes
             const int w0 = __ffsll((unsigned long long)__ballot(rank == a.topk_groups - 1)) - 1;
@@ -324,7 +331,7 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kerne
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int e = lane * NS + i;
-            if (e < a.ne && !s_keep[e / size]) key[i] = 0;
+            if (e < a.ne && !s_keep[group_of(a, e)]) key[i] = 0;
         }
     }
     // the lane's keys by falling value, equals in order
@@ -440,9 +447,13 @@ static int route_typed(const RouteArgs &a, hipStream_t stream)
     return launch_kernel(route_kernel<8, T>, grid, block, stream, a);
 }
 
-int launch_route(const RouteArgs &a, hipStream_t stream)
+int launch_route(const RouteArgs &args, hipStream_t stream)
 {
-    if (a.nt > 0x7fffffff) return -1;
+    if (args.nt > 0x7fffffff) return -1;
+    RouteArgs a = args;
+    a.size = (uint32_t)(a.ne / a.groups);
+    a.by_size = ((1u << 20) + a.size - 1) / a.size;
+    while ((2 << a.lane_bits) * a.groups <= 64) ++a.lane_bits;
     switch (a.ltype) {
     case T_F32: return route_typed<T_F32>(a, stream);
     case T_BF16: return route_typed<T_BF16>(a, stream);

@@ -41,6 +41,10 @@ struct RouteArgs {
     int64_t nt, ldl;
     int ltype, ne, score, groups, topk_groups, group_top, k, renorm;
     float scale;
+    // set by launch_route: experts of a group, 2^20 over that (rounded up), and
+    // log2 of the lanes that share a group
+    uint32_t size = 0, by_size = 0;
+    int lane_bits = 0;
 };
 
 // Plan: int32 words.  [0 .. ne] first position of each expert's rows in the
