@@ -220,16 +220,19 @@ constexpr int ROUTE_WAVES = 4;
 // plus 2^-21 |c| (a group's score: the sum of its |c|) are in their exact order.
 //
 // Bound by its instructions and their latencies, not by the logits' bytes:
-// 16384 tokens, 256 experts in 8 groups, k = 8 (17 MB) 26 us, without groups 18,
-// and 14 for k = 1.  Eight waves a SIMD (64 registers) against six: 26 and 30.
+// 16384 tokens, 256 experts in 8 groups, k = 8 (17 MB) 20 us, 610 vector
+// instructions a token; without groups 16 us (450), and 11 for k = 1 (300).  With
+// the weights formed by every wave 22 us (670).  Eight waves a SIMD (64
+// registers) against six, then: 26 and 30.
 template <int NS, int T>
 __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kernel(RouteArgs a)
 {
     __shared__ double s_all[ROUTE_WAVES][NS * 64 + 64];
     __shared__ uint8_t s_keeps[ROUTE_WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + wave;
-    if (t >= a.nt) return;
+    __shared__ float s_x[ROUTE_WAVES][ROUTE_MAX_K], s_top[ROUTE_WAVES];
+    __shared__ double s_sum[ROUTE_WAVES];
+    const int64_t t0 = (int64_t)blockIdx.x * ROUTE_WAVES, t = t0 + wave < a.nt ? t0 + wave : a.nt - 1;
     const elem_t<T> *l = static_cast<const elem_t<T> *>(a.logits) + t * a.ldl;
     float x[NS], c[NS];
     bool ok[NS];
@@ -407,34 +410,52 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kerne
     }
     if (lane >= a.k || my_key == 0) my_id = -1;
 
-    // weights in 64 bits, lane r the r-th chosen
-    double p = 0.0;
-    float xi = 0.0f;
-    if (my_id >= 0) take_logit(true, (float)l[my_id], xi);
+    if (lane < a.k && t0 + wave < a.nt) a.ids[t * a.k + lane] = my_id;
+
+    // Weights in 64 bits, a third of the instructions if every wave formed its
+    // own: the first waves form those of all four tokens, 16 or 32 lanes a token.
+    if (lane < ROUTE_MAX_K) {
+        float xi = -INFINITY;   // none
+        if (my_id >= 0) take_logit(true, (float)l[my_id], xi);
+        s_x[wave][lane] = xi;
+    }
     if (a.score == 0) {
-        p = my_id >= 0 ? exp((double)xi - (double)top) : 0.0;
+        double sum = 1.0;
         if (!a.renorm) {
-            double sum = 0.0;
+            sum = 0.0;
 #pragma unroll
             for (int i = 0; i < NS; ++i) sum += ok[i] ? exp((double)x[i] - (double)top) : 0.0;
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-            p = my_id >= 0 ? p / sum : 0.0;
         }
-    } else if (my_id >= 0) {
-        p = 1.0 / (1.0 + exp(-(double)xi));
+        if (lane == 0) {
+            s_top[wave] = top;
+            s_sum[wave] = sum;
+        }
+    }
+    __syncthreads();
+    const int bits = a.k <= 16 ? 4 : 5;   // log2 of the lanes a token
+    const int mine = (wave << (6 - bits)) + (lane >> bits), at = lane & ((1 << bits) - 1);
+    if (mine >= ROUTE_WAVES) return;   // the whole wave
+    const float xi = s_x[mine][at];
+    double p = 0.0;
+    if (xi > -INFINITY) {
+        if (a.score == 0) {
+            p = exp((double)xi - (double)s_top[mine]);
+            if (!a.renorm) p /= s_sum[mine];
+        } else {
+            p = 1.0 / (1.0 + exp(-(double)xi));
+        }
     }
     double scale = (double)a.scale;
     if (a.renorm) {
         double sum = p;
+        if (bits == 5) sum += __shfl_xor(sum, 16);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor(sum, d);   // k is at most 32
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
         scale = sum > 0.0 ? scale / sum : 0.0;
     }
-    if (lane < a.k) {
-        a.ids[t * a.k + lane] = my_id;
-        a.w[t * a.k + lane] = (float)(p * scale);
-    }
+    if (at < a.k && t0 + mine < a.nt) a.w[(t0 + mine) * a.k + at] = (float)(p * scale);
 }
 
 template <int T>

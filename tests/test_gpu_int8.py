@@ -654,3 +654,22 @@ def test_product_every_tile(qig, nt, rows, id_):
     want, allow = ref.product(q.cpu().numpy()[t], sq.cpu().numpy()[t], W.cpu().numpy(), sw.cpu().numpy(),
                               bias.cpu().numpy(), glu, "float32")
     _check(y[t.cuda()][:, :od], want, allow, (nt, rows, id_))
+
+
+@pytest.mark.parametrize("nt", [1, 2, 4, 5])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("ne,k,groups,keep", [(511, 16, 7, 3), (510, 17, 30, 5), (96, 24, 32, 20), (441, 32, 63, 40),
+                                              (33, 31, 11, 11), (512, 2, 2, 1)])
+def test_routing_many_chosen_and_odd_groups(qig, nt, score, ne, k, groups, keep):
+    """16 and more experts a token, groups of odd sizes, and token counts on
+    both sides of a workgroup's, with and without renormalisation."""
+    g = _rng(14, nt, ne)
+    l = g.standard_normal((nt, ne)).astype(np.float32) * 2
+    l[nt - 1, g.random(ne) < 0.5] = -np.inf
+    b = (g.standard_normal(ne) * 0.2).astype(np.float32)
+    for renorm in (True, False):
+        kw = dict(score=score, groups=groups, topk_groups=keep, group_top=2, renorm=renorm, scale=1.5)
+        ids, w = qig.route_experts(_dev(l), k, bias=_dev(b), **kw)
+        rids, rw = ref.route(l, k, bias=b, **kw)
+        assert np.array_equal(ids.cpu().numpy(), rids)
+        assert (np.abs(w.cpu().numpy() - rw) <= np.abs(rw) * 2.0 ** -23 + 2.0 ** -149).all()
