@@ -22,11 +22,13 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 def _start():
     """torch and the library, on the first call (importing the package needs
     neither)."""
-    global torch, _lib, _empty, _current, _f32
+    global torch, _lib, _empty, _current, _device, _f32, _i8, _u8, _ws_bytes
     import torch as t
     _lib = load()
     _TYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
-    _empty, _f32 = t.empty, t.float32
+    _empty, _f32, _i8, _u8 = t.empty, t.float32, t.int8, t.uint8
+    _ws_bytes = _lib.mmq_workspace_bytes()
+    _device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     # the current stream's handle without the Stream object (1 us a call)
     _current = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda dev: t.cuda.current_stream(dev).cuda_stream)
     torch = t
@@ -80,7 +82,8 @@ def _rows16(t, rows, cols, ld, name):
 
 
 def _int8_rows(t, name):
-    _is(t, torch.int8, name)
+    if t.dtype is not _i8:
+        _is(t, _i8, name)
     rows, cols, ld = _matrix(t, name)
     if rows <= 1:
         ld = (cols + 15) // 16 * 16
@@ -114,7 +117,7 @@ def _call(fn, what, names, tensors, stream, args):
         if stream.device.index != dev:
             raise QigError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _device() == dev:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -134,14 +137,14 @@ def quantize_i8(x, q=None, s=None, stream=None):
     nt, id_, ldx = _matrix(x, "x")
     if q is None:
         ldq = (id_ + 15) // 16 * 16
-        q = _empty((nt, ldq), dtype=torch.int8, device=x.device)
+        q = _empty((nt, ldq), dtype=_i8, device=x.device)
         if ldq != id_:
             q = q[:, :id_]
     else:
         _is(q, torch.int8, "q")
         ldq = _sized(q, "q", nt, id_)
     if s is None:
-        s = _empty((nt,), dtype=torch.float32, device=x.device)
+        s = _empty((nt,), dtype=_f32, device=x.device)
     else:
         _vector(s, nt, "s")
     _call(_lib.quantize_i8, "quantize_i8", ("x", "q", "s"), (x, q, s), stream,
@@ -188,9 +191,9 @@ def mm_i8(W, sw, q, sq, bias=None, glu=False, y=None, dtype=None, ws=None, strea
     if bias is not None:
         _vector(bias, rows, "bias")
     y, yt, ldy = _output(y, dtype, nt, od, q.device)
-    if ws is not None and (ws.numel() * ws.element_size() < _lib.mmq_workspace_bytes() or not ws.is_contiguous()):
-        raise QigError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs "
-                       f"{_lib.mmq_workspace_bytes()}, contiguous")
+    if ws is not None and (ws.numel() * (1 if ws.dtype is _u8 else ws.element_size()) < _ws_bytes
+                           or not ws.is_contiguous()):
+        raise QigError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs {_ws_bytes}, contiguous")
     _call(_lib.mm_i8, "mm_i8", ("W", "sw", "q", "sq", "bias", "y", "ws"), (W, sw, q, sq, bias, y, ws), stream,
           (W.data_ptr(), ldw, sw.data_ptr(), od, id_, q.data_ptr(), ldq, sq.data_ptr(), nt,
            None if bias is None else bias.data_ptr(), 1 if glu else 0, y.data_ptr(), yt, ldy,
