@@ -269,7 +269,8 @@ def _own(s):
     if c["op"] == "up":
         return qig.mm_i8_experts(s["w"], s["sw"], q, sx, plan, rows, glu=True, dtype=out)
     if c["op"] == "down":
-        h = qig.mm_i8_experts(s["w"], s["sw"], q, sx, plan, rows, dtype=out)
+        # the rows stay in fp32 until they are summed: one rounding at the end
+        h = qig.mm_i8_experts(s["w"], s["sw"], q, sx, plan, rows)
         return qig.combine_experts(h, rw, dtype=out)
     h = qig.mm_i8_experts(s["w"], s["sw"], q, sx, plan, rows, glu=True)
     q, sx = qig.quantize_i8(h)
