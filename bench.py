@@ -578,7 +578,7 @@ def run_int8(args):
         ids = torch.empty((nt, k), dtype=torch.int32, device=dev)
         rw = torch.empty((nt, k), device=dev)
         plan = torch.empty(qig.expert_plan_bytes(rows, ne) // 4, dtype=torch.int32, device=dev)
-        o = torch.empty((rows, id_), dtype=torch.bfloat16, device=dev)
+        o = torch.empty((rows, id_), device=dev)   # fp32: rounded to bf16 once, after the sum
         calls["route_experts"] = lambda: qig.route_experts(logits, k, ids=ids, w=rw)
         calls["plan_experts"] = lambda: qig.plan_experts(ids, ne, out=plan)
         calls["gate_up"] = lambda: qig.mm_i8_experts(W1, s1, qx, sx, plan, rows, glu=True, y=h)
