@@ -415,8 +415,9 @@ int quantize_i8(const void *x, int xtype, int64_t nt, int64_t id, int64_t ldx,
  *          is bit-identical with and without ws.
  * Errors: QIG_EINVAL (nt or od < 0 or >= 2^31 (od: 2^30), id <= 0 or > 131071
  *         (beyond which an int32 sum could overflow), ldw or ldq < id or >
- *         8388352, ldy < od, unknown ytype, glu not 0 or 1), QIG_EALIGN,
- *         QIG_ELAUNCH.
+ *         8388352, ldy < od, unknown ytype, glu not 0 or 1, or more output
+ *         tiles than one launch holds: 2^24 of at least 64 x 128 outputs,
+ *         64 x 64 with glu), QIG_EALIGN, QIG_ELAUNCH.
  */
 int mm_i8(const int8_t *W, int64_t ldw, const float *sw, int64_t od,
           int64_t id, const int8_t *q, int64_t ldq, const float *sq,
@@ -487,8 +488,10 @@ int plan_experts(const int32_t *ids, int64_t nrows, int64_t ne, void *plan,
  *          its activations (gate and up), 1 where each row has its own (down)
  *   plan   made by plan_experts for the same nrows and ne
  *   y      [nrows][ldy], in the order of the rows, not of the plan
- * Other arguments and errors as mm_i8; also QIG_EINVAL for nrows >= 2^29, ne
- * < 1 or > 512, slots < 1 or not a divisor of nrows.
+ * Other arguments and errors as mm_i8 (the tiles are of at least 32 x 128
+ * outputs, 32 x 64 with glu, and each expert's last one counts whole); also
+ * QIG_EINVAL for nrows >= 2^29, ne < 1 or > 512, slots < 1 or not a divisor of
+ * nrows.
  */
 int mm_i8_experts(const int8_t *W, int64_t ldw, const float *sw, int64_t ne,
                   int64_t od, int64_t id, const int8_t *q, int64_t ldq,

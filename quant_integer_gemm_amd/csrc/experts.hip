@@ -459,18 +459,24 @@ __global__ __launch_bounds__(ROUTE_WAVES * 64, NS <= 4 ? 8 : 1) void route_kerne
 }
 
 template <int T>
-static int route_typed(const RouteArgs &a, hipStream_t stream)
+static int route_typed(const RouteArgs &args, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.nt + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(ROUTE_WAVES * 64);
-    if (a.ne <= 64) return launch_kernel(route_kernel<1, T>, grid, block, stream, a);
-    if (a.ne <= 128) return launch_kernel(route_kernel<2, T>, grid, block, stream, a);
-    if (a.ne <= 256) return launch_kernel(route_kernel<4, T>, grid, block, stream, a);
-    return launch_kernel(route_kernel<8, T>, grid, block, stream, a);
+    return in_launches(args.nt, launch_groups(ROUTE_WAVES * 64) * ROUTE_WAVES, [&](int64_t r, int64_t n) {
+        RouteArgs a = args;
+        a.logits = static_cast<const elem_t<T> *>(args.logits) + r * args.ldl;
+        a.ids += r * a.k;
+        a.w += r * a.k;
+        a.nt = n;
+        const dim3 grid((unsigned)((n + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(ROUTE_WAVES * 64);
+        if (a.ne <= 64) return launch_kernel(route_kernel<1, T>, grid, block, stream, a);
+        if (a.ne <= 128) return launch_kernel(route_kernel<2, T>, grid, block, stream, a);
+        if (a.ne <= 256) return launch_kernel(route_kernel<4, T>, grid, block, stream, a);
+        return launch_kernel(route_kernel<8, T>, grid, block, stream, a);
+    });
 }
 
 int launch_route(const RouteArgs &args, hipStream_t stream)
 {
-    if (args.nt > 0x7fffffff) return -1;
     RouteArgs a = args;
     a.size = (uint32_t)(a.ne / a.groups);
     a.by_size = ((1u << 20) + a.size - 1) / a.size;
@@ -664,11 +670,13 @@ template <int TH, int TY>
 static int combine(const void *h, int64_t ldh, const float *w, int64_t nt, int64_t k, int64_t od, void *y,
                    int64_t ldy, hipStream_t stream)
 {
-    const int64_t per = (od + VEC<TH> - 1) / VEC<TH>, total = nt * per, grid = (total + 255) / 256;
-    if (grid > 0x7fffffff) return -1;
-    return launch_kernel(combine_kernel<TH, TY>, dim3((unsigned)grid), dim3(256), stream,
-                         static_cast<const elem_t<TH> *>(h), ldh, w, (int)k, od, per, total,
-                         static_cast<elem_t<TY> *>(y), ldy);
+    const int64_t per = (od + VEC<TH> - 1) / VEC<TH>, most = launch_groups(256) * 256 / per;
+    if (most == 0) return -1;
+    return in_launches(nt, most, [&](int64_t r, int64_t n) {
+        return launch_kernel(combine_kernel<TH, TY>, dim3((unsigned)((n * per + 255) / 256)), dim3(256), stream,
+                             static_cast<const elem_t<TH> *>(h) + r * k * ldh, ldh, w + r * k, (int)k, od, per,
+                             n * per, static_cast<elem_t<TY> *>(y) + r * ldy, ldy);
+    });
 }
 
 template <int TH>

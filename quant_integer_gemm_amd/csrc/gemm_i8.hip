@@ -911,7 +911,9 @@ template <bool GLU, int YT>
 static int pick_dense(I8Args a, hipStream_t stream)
 {
     const int64_t wbytes = (GLU ? 2 : 1) * a.od * (int64_t)a.id;
-    if (a.nt <= 16 || (a.nt <= 64 && (a.nt + 15) / 16 * wbytes <= GEMV_BYTES))
+    // (more weight rows than a launch of it holds, from 2^27 on, go to the tiles)
+    if ((a.nt <= 16 && (a.od + GEMV_ROWS - 1) / GEMV_ROWS <= launch_groups(GEMV_WAVES * 64)) ||
+        (a.nt <= 64 && (a.nt + 15) / 16 * wbytes <= GEMV_BYTES))
         return launch_gemv<GLU, false, YT>(a, stream);
     const double c256 = cost<GLU>(COST_256, a), c192 = cost<GLU>(COST_192, a);
     const double c64 = cost<GLU>(COST_64, a), c64s = cost<GLU>(COST_64S, a);

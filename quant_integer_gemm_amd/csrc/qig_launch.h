@@ -8,14 +8,21 @@
 
 namespace qig {
 
-// Enqueue kernel<<<grid, block, 0, stream>>>(args...) and return 0, or -3 if
-// the runtime refused this launch.  The status is hipLaunchKernel's own: a
-// triple-chevron launch followed by hipGetLastError() would also report, and
-// clear, an error left on the calling thread by an earlier, unrelated call.
+// A launch's threads are counted in 32 bits: the runtime takes a larger grid
+// without an error and runs a part of it (2^26 + 77 tokens of route_experts
+// left tokens out).
+constexpr uint64_t LAUNCH_THREADS = 0xffffffffu;
+
+// Enqueue kernel<<<grid, block, 0, stream>>>(args...) and return 0, -1 if the
+// grid is too large, or -3 if the runtime refused this launch.  The status is
+// hipLaunchKernel's own: a triple-chevron launch followed by hipGetLastError()
+// would also report, and clear, an error left on the calling thread by an
+// earlier, unrelated call.
 template <typename... Params, typename... Args>
 inline int launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, hipStream_t stream, Args... args)
 {
     static_assert(sizeof...(Params) == sizeof...(Args), "argument count");
+    if ((uint64_t)grid.x * block.x > LAUNCH_THREADS) return -1;
     std::tuple<Params...> held(static_cast<Params>(args)...);
     const hipError_t e = std::apply(
         [&](auto &...a) {
@@ -24,6 +31,21 @@ inline int launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, hipSt
         },
         held);
     return e == hipSuccess ? 0 : -3;
+}
+
+// Most workgroups of `threads` in a launch.
+constexpr int64_t launch_groups(int64_t threads) { return (int64_t)LAUNCH_THREADS / threads; }
+
+// f(first, count) for runs of at most `most` of `rows` rows, a launch each;
+// stops at a non-zero result.
+template <typename F>
+inline int in_launches(int64_t rows, int64_t most, F f)
+{
+    for (int64_t r = 0; r < rows; r += most) {
+        const int rc = f(r, rows - r < most ? rows - r : most);
+        if (rc != 0) return rc;
+    }
+    return 0;
 }
 
 struct MmqLaunch {

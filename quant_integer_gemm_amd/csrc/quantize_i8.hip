@@ -219,8 +219,11 @@ template <int T, int THR, int NV>
 static int launch_rows(const elem_t<T> *x, int64_t nt, int64_t id, int64_t ldx, int8_t *q, int64_t ldq, float *s,
                        hipStream_t stream)
 {
-    return launch_kernel(quantize_i8_kernel<T, THR, NV>, dim3((unsigned)(THR == 64 ? (nt + 3) / 4 : nt)),
-                         dim3(THR < 256 ? 256 : THR), stream, x, nt, (int)id, ldx, q, ldq, s);
+    constexpr int BLOCK = THR < 256 ? 256 : THR, ROWS = THR == 64 ? 4 : 1;
+    return in_launches(nt, launch_groups(BLOCK) * ROWS, [&](int64_t r, int64_t n) {
+        return launch_kernel(quantize_i8_kernel<T, THR, NV>, dim3((unsigned)((n + ROWS - 1) / ROWS)), dim3(BLOCK),
+                             stream, x + r * ldx, n, (int)id, ldx, q + r * ldq, ldq, s + r);
+    });
 }
 
 template <int T>
@@ -235,13 +238,15 @@ static int launch(const void *xv, int64_t nt, int64_t id, int64_t ldx, int8_t *q
     if (nv <= 1024) return launch_rows<T, 256, 4>(x, nt, id, ldx, q, ldq, s, stream);
     if (nv <= 2560) return launch_rows<T, 512, 5>(x, nt, id, ldx, q, ldq, s, stream);
     if (nv <= 5120) return launch_rows<T, 1024, 5>(x, nt, id, ldx, q, ldq, s, stream);
-    return launch_kernel(quantize_i8_long_kernel<T>, dim3((unsigned)nt), dim3(1024), stream, x, id, ldx, q, ldq, s);
+    return in_launches(nt, launch_groups(1024), [&](int64_t r, int64_t n) {
+        return launch_kernel(quantize_i8_long_kernel<T>, dim3((unsigned)n), dim3(1024), stream, x + r * ldx, id, ldx,
+                             q + r * ldq, ldq, s + r);
+    });
 }
 
 int launch_quantize_i8(const void *x, int xtype, int64_t nt, int64_t id, int64_t ldx, int8_t *q, int64_t ldq,
                        float *s, hipStream_t stream)
 {
-    if (nt > 0x7fffffff) return -1;
     switch (xtype) {
     case T_F32: return launch<T_F32>(x, nt, id, ldx, q, ldq, s, stream);
     case T_BF16: return launch<T_BF16>(x, nt, id, ldx, q, ldq, s, stream);
