@@ -11,7 +11,7 @@ and strides once, and name it only when they refuse it.
 """
 from __future__ import annotations
 
-from ._lib import QigError, _check, load
+from ._lib import QigError, _check, _empty as _empty_on, load
 
 torch = None
 _lib = None
@@ -32,6 +32,13 @@ def _start():
     # the current stream's handle without the Stream object (1 us a call)
     _current = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda dev: t.cuda.current_stream(dev).cuda_stream)
     torch = t
+
+
+def _new(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream`` (None: the current one)."""
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    return _empty_on(shape, dtype, device, stream)
 
 
 def _type(t, name):
@@ -114,8 +121,9 @@ def _call(fn, what, names, tensors, stream, args):
     if stream is None:
         handle = _current(dev)
     else:
-        if stream.device.index != dev:
-            raise QigError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+        on = getattr(stream, "device", None)   # a bare handle does not say
+        if on is not None and on.index != dev:
+            raise QigError(f"stream is on {on}, the tensors on cuda:{dev}")
         handle = stream.cuda_stream
     if _device() == dev:
         rc = fn(*args, handle)
@@ -137,14 +145,14 @@ def quantize_i8(x, q=None, s=None, stream=None):
     nt, id_, ldx = _matrix(x, "x")
     if q is None:
         ldq = (id_ + 15) // 16 * 16
-        q = _empty((nt, ldq), dtype=_i8, device=x.device)
+        q = _new((nt, ldq), _i8, x.device, stream)
         if ldq != id_:
             q = q[:, :id_]
     else:
         _is(q, torch.int8, "q")
         ldq = _sized(q, "q", nt, id_)
     if s is None:
-        s = _empty((nt,), dtype=_f32, device=x.device)
+        s = _new((nt,), _f32, x.device, stream)
     else:
         _vector(s, nt, "s")
     _call(_lib.quantize_i8, "quantize_i8", ("x", "q", "s"), (x, q, s), stream,
@@ -152,12 +160,12 @@ def quantize_i8(x, q=None, s=None, stream=None):
     return q, s
 
 
-def _output(y, dtype, nt, od, device):
+def _output(y, dtype, nt, od, device, stream):
     """(y, its type's code, row stride)."""
     if y is None:
         dtype = torch.float32 if dtype is None else dtype
         code = _type(dtype, "y")
-        return _empty((nt, od), dtype=dtype, device=device), code, od
+        return _new((nt, od), dtype, device, stream), code, od
     if dtype is not None and y.dtype != dtype:
         raise QigError(f"y is {y.dtype}, dtype asks for {dtype}")
     code = _type(y.dtype, "y")
@@ -190,7 +198,7 @@ def mm_i8(W, sw, q, sq, bias=None, glu=False, y=None, dtype=None, ws=None, strea
     _vector(sq, nt, "sq")
     if bias is not None:
         _vector(bias, rows, "bias")
-    y, yt, ldy = _output(y, dtype, nt, od, q.device)
+    y, yt, ldy = _output(y, dtype, nt, od, q.device, stream)
     if ws is not None and (ws.numel() * (1 if ws.dtype is _u8 else ws.element_size()) < _ws_bytes
                            or not ws.is_contiguous()):
         raise QigError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs {_ws_bytes}, contiguous")
@@ -218,13 +226,13 @@ def route_experts(logits, k, score="softmax", bias=None, groups=1, topk_groups=1
     if bias is not None:
         _vector(bias, ne, "bias")
     if ids is None:
-        ids = _empty((nt, max(k, 0)), dtype=torch.int32, device=logits.device)
+        ids = _new((nt, max(k, 0)), torch.int32, logits.device, stream)
     else:
         _is(ids, torch.int32, "ids")
         if ids.numel() != nt * k or not ids.is_contiguous():
             raise QigError(f"ids must be contiguous [{nt}][{k}], not {list(ids.shape)}")
     if w is None:
-        w = _empty((nt, max(k, 0)), dtype=torch.float32, device=logits.device)
+        w = _new((nt, max(k, 0)), _f32, logits.device, stream)
     else:
         _vector(w, nt * k, "w")
     _call(_lib.route_experts, "route_experts", ("logits", "bias", "ids", "w"), (logits, bias, ids, w), stream,
@@ -251,7 +259,7 @@ def plan_experts(ids, ne, out=None, stream=None):
     if words == 0:
         raise QigError(f"no plan for {n} rows and {ne} experts")
     if out is None:
-        out = _empty((words,), dtype=torch.int32, device=ids.device)
+        out = _new((words,), torch.int32, ids.device, stream)
     else:
         _is(out, torch.int32, "out")
         if out.numel() < words or not out.is_contiguous():
@@ -295,7 +303,7 @@ def mm_i8_experts(W, sw, q, sq, plan, nrows, bias=None, glu=False, y=None, dtype
     nbytes = _lib.expert_plan_bytes(nrows, ne)
     if nbytes == 0 or plan.numel() * 4 < nbytes or not plan.is_contiguous():
         raise QigError(f"plan is not one of {nrows} rows and {ne} experts")
-    y, yt, ldy = _output(y, dtype, nrows, od, q.device)
+    y, yt, ldy = _output(y, dtype, nrows, od, q.device, stream)
     _call(_lib.mm_i8_experts, "mm_i8_experts",
           ("W", "sw", "q", "sq", "plan", "bias", "y"), (W, sw, q, sq, plan, bias, y), stream,
           (W.data_ptr(), ldw, sw.data_ptr(), ne, od, id_, q.data_ptr(), ldq, sq.data_ptr(), nrows, slots,
@@ -317,7 +325,7 @@ def combine_experts(h, w, y=None, dtype=None, stream=None):
     n, od, ldh = _matrix(h, "h")
     if n != nt * k:
         raise QigError(f"h must be [{nt * k}][any], not {list(h.shape)}")
-    y, yt, ldy = _output(y, h.dtype if y is None and dtype is None else dtype, nt, od, h.device)
+    y, yt, ldy = _output(y, h.dtype if y is None and dtype is None else dtype, nt, od, h.device, stream)
     _call(_lib.combine_experts, "combine_experts", ("h", "w", "y"), (h, w, y), stream,
           (h.data_ptr(), ht, ldh, w.data_ptr(), nt, k, od, y.data_ptr(), yt, ldy))
     return y

@@ -102,6 +102,29 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _torch_stream(stream, device):
+    """``stream`` as a torch stream: whatever has a `cuda_stream` handle."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream``.  Its memory comes from that
+    stream's part of the allocator: a block freed on another stream may still
+    have that stream's work before it.  The current stream, where the caller
+    will mostly read it, is recorded too, so that the block does not return to
+    ``stream`` before the current stream is done with it."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _need(t, nbytes: int, name: str):
     """The library reads and writes through raw pointers: check here that a
     tensor holds the bytes a call will touch (contiguous, large enough)."""
@@ -180,17 +203,17 @@ def quantize_q8_pad40(x, id_: int | None = None, out=None, stream=None):
     nt, ldx, id_ = _x_rows(x, id_)
     nbytes = q8_pad40_bytes(nt, id_)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        out = _empty(nbytes, torch.uint8, x.device, stream)
     _need(out, nbytes, "out")
     _check(load().quantize_q8_pad40(_dev_ptr(x, "x"), nt, id_, ldx, _dev_ptr(out, "q8"), _stream(stream)),
            "quantize_q8_pad40")
     return out
 
 
-def _out_y(y, nt, od, ldy, device):
+def _out_y(y, nt, od, ldy, device, stream):
     import torch
     if y is None:
-        y = torch.empty((nt, od), dtype=torch.float32, device=device)
+        y = _empty((nt, od), torch.float32, device, stream)
         ldy = od
     elif ldy is None:
         ldy = y.stride(0) if y.dim() == 2 else od
@@ -199,7 +222,7 @@ def _out_y(y, nt, od, ldy, device):
 
 def mmq_q4k(W, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, stream=None):
     """y[nt][od] = pad40 activations x q4_K weights^T (fp32, overwritten)."""
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     _gemm_checks(W, _raw_bytes(od, id_, 144), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy)
     _check(load().mmq_q4k(_dev_ptr(W, "W"), od, id_, _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"), ldy,
                           _stream(stream)), "mmq_q4k")
@@ -209,7 +232,7 @@ def mmq_q4k(W, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, s
 def mmq_q6k(W, bstride: int, od: int, id_: int, q8, nt: int, W_exp=None, y=None, ldy: int | None = None,
             stream=None):
     """y[nt][od] = pad40 activations x q6_K weights^T; W_exp (dense plane) optional."""
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     _gemm_checks(W, _raw_bytes(od, id_, bstride), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy, W_exp, id_)
     _check(load().mmq_q6k(_dev_ptr(W, "W"), bstride, _dev_ptr(W_exp, "W_exp"), od, id_,
                           _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"), ldy, _stream(stream)), "mmq_q6k")
@@ -220,7 +243,7 @@ def expand_q6k_dense(W, bstride: int, od: int, id_: int, out=None, stream=None):
     """Raw q6_K plane -> dense centred int8 W_exp[od][id]."""
     import torch
     if out is None:
-        out = torch.empty((od, id_), dtype=torch.int8, device=W.device)
+        out = _empty((od, id_), torch.int8, W.device, stream)
     _need(W, _raw_bytes(od, id_, bstride), "W")
     _need(out, od * id_, "out")
     _check(load().expand_q6k_dense(_dev_ptr(W, "W"), bstride, od, id_, _dev_ptr(out, "W_exp"),
@@ -231,7 +254,7 @@ def expand_q6k_dense(W, bstride: int, od: int, id_: int, out=None, stream=None):
 def mmq_q4k_partials(W, od, id_, q8, nt, t0, t1, j0, j1, stream=None):
     """int32 P4[t1-t0][j1-j0][8*nsb] from the q4_K kernel (test export)."""
     import torch
-    P = torch.empty((t1 - t0, j1 - j0, 8 * (id_ // 256)), dtype=torch.int32, device=W.device)
+    P = _empty((t1 - t0, j1 - j0, 8 * (id_ // 256)), torch.int32, W.device, stream)
     _need(W, _raw_bytes(od, id_, 144), "W")
     _need(q8, q8_pad40_bytes(nt, id_), "q8")
     _check(load().mmq_q4k_partials(_dev_ptr(W, "W"), od, id_, _dev_ptr(q8, "q8"), nt, t0, t1, j0, j1,
@@ -242,7 +265,7 @@ def mmq_q4k_partials(W, od, id_, q8, nt, t0, t1, j0, j1, stream=None):
 def mmq_q6k_partials(W, bstride, od, id_, q8, nt, t0, t1, j0, j1, W_exp=None, stream=None):
     """int32 P6[t1-t0][j1-j0][16*nsb] from the q6_K kernel (test export)."""
     import torch
-    P = torch.empty((t1 - t0, j1 - j0, 16 * (id_ // 256)), dtype=torch.int32, device=W.device)
+    P = _empty((t1 - t0, j1 - j0, 16 * (id_ // 256)), torch.int32, W.device, stream)
     _need(W, _raw_bytes(od, id_, bstride), "W")
     _need(q8, q8_pad40_bytes(nt, id_), "q8")
     _need(W_exp, od * id_, "W_exp")
@@ -262,7 +285,7 @@ def prepare_q4k(W, od: int, id_: int, out=None, stream=None):
     """Raw q4_K plane -> prepared buffer (quant plane + fp32 scale plane)."""
     import torch
     if out is None:
-        out = torch.empty(prepared_bytes("q4_K", od, id_), dtype=torch.uint8, device=W.device)
+        out = _empty(prepared_bytes("q4_K", od, id_), torch.uint8, W.device, stream)
     _need(W, _raw_bytes(od, id_, 144), "W")
     _need(out, prepared_bytes("q4_K", od, id_), "out")
     _check(load().prepare_q4k(_dev_ptr(W, "W"), od, id_, _dev_ptr(out, "Wp"), _stream(stream)), "prepare_q4k")
@@ -273,7 +296,7 @@ def prepare_q6k(W, bstride: int, od: int, id_: int, out=None, stream=None):
     """Raw q6_K plane -> prepared buffer (quant plane + fp32 scale plane)."""
     import torch
     if out is None:
-        out = torch.empty(prepared_bytes("q6_K", od, id_), dtype=torch.uint8, device=W.device)
+        out = _empty(prepared_bytes("q6_K", od, id_), torch.uint8, W.device, stream)
     _need(W, _raw_bytes(od, id_, bstride), "W")
     _need(out, prepared_bytes("q6_K", od, id_), "out")
     _check(load().prepare_q6k(_dev_ptr(W, "W"), bstride, od, id_, _dev_ptr(out, "Wp"), _stream(stream)),
@@ -283,7 +306,7 @@ def prepare_q6k(W, bstride: int, od: int, id_: int, out=None, stream=None):
 
 def mmq_q4k_prepared(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, stream=None):
     """y[nt][od] from a prepared q4_K buffer (bit-identical to mmq_q4k on the raw blocks)."""
-    y, ldy = _out_y(y, nt, od, ldy, Wp.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wp.device, stream)
     _gemm_checks(Wp, prepared_bytes("q4_K", od, id_), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy)
     _check(load().mmq_q4k_prepared(_dev_ptr(Wp, "Wp"), od, id_, _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"), ldy,
                                    _stream(stream)), "mmq_q4k_prepared")
@@ -292,7 +315,7 @@ def mmq_q4k_prepared(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: int | None
 
 def mmq_q6k_prepared(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, stream=None):
     """y[nt][od] from a prepared q6_K buffer (bit-identical to mmq_q6k on the raw blocks)."""
-    y, ldy = _out_y(y, nt, od, ldy, Wp.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wp.device, stream)
     _gemm_checks(Wp, prepared_bytes("q6_K", od, id_), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy)
     _check(load().mmq_q6k_prepared(_dev_ptr(Wp, "Wp"), od, id_, _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"), ldy,
                                    _stream(stream)), "mmq_q6k_prepared")
@@ -342,7 +365,7 @@ def new_workspace(device):
 
 def mmq_q4k_streamk(W, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, ws=None, stream=None):
     """mmq_q4k with the work split by super-block over all CUs (stream-K)."""
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     ws = workspace(W.device, stream) if ws is None else ws
     _gemm_checks(W, _raw_bytes(od, id_, 144), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q4k_streamk(_dev_ptr(W, "W"), od, id_, _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"), ldy,
@@ -353,7 +376,7 @@ def mmq_q4k_streamk(W, od: int, id_: int, q8, nt: int, y=None, ldy: int | None =
 def mmq_q6k_streamk(W, bstride: int, od: int, id_: int, q8, nt: int, W_exp=None, y=None, ldy: int | None = None,
                     ws=None, stream=None):
     """mmq_q6k with the work split by super-block over all CUs (stream-K)."""
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     ws = workspace(W.device, stream) if ws is None else ws
     _gemm_checks(W, _raw_bytes(od, id_, bstride), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy, W_exp, id_, ws)
     _check(load().mmq_q6k_streamk(_dev_ptr(W, "W"), bstride, _dev_ptr(W_exp, "W_exp"), od, id_,
@@ -365,7 +388,7 @@ def mmq_q6k_streamk(W, bstride: int, od: int, id_: int, q8, nt: int, W_exp=None,
 def mmq_q4k_prepared_streamk(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, ws=None,
                              stream=None):
     """mmq_q4k_prepared, stream-K."""
-    y, ldy = _out_y(y, nt, od, ldy, Wp.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wp.device, stream)
     ws = workspace(Wp.device, stream) if ws is None else ws
     _gemm_checks(Wp, prepared_bytes("q4_K", od, id_), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q4k_prepared_streamk(_dev_ptr(Wp, "Wp"), od, id_, _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"),
@@ -376,7 +399,7 @@ def mmq_q4k_prepared_streamk(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: in
 def mmq_q6k_prepared_streamk(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, ws=None,
                              stream=None):
     """mmq_q6k_prepared, stream-K."""
-    y, ldy = _out_y(y, nt, od, ldy, Wp.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wp.device, stream)
     ws = workspace(Wp.device, stream) if ws is None else ws
     _gemm_checks(Wp, prepared_bytes("q6_K", od, id_), q8, q8_pad40_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q6k_prepared_streamk(_dev_ptr(Wp, "Wp"), od, id_, _dev_ptr(q8, "q8"), nt, _dev_ptr(y, "y"),
@@ -395,7 +418,7 @@ def quantize_q8_tiled(x, id_: int | None = None, out=None, stream=None):
     import torch
     nt, ldx, id_ = _x_rows(x, id_)
     if out is None:
-        out = torch.empty(q8_tiled_bytes(nt, id_), dtype=torch.uint8, device=x.device)
+        out = _empty(q8_tiled_bytes(nt, id_), torch.uint8, x.device, stream)
     _need(out, q8_tiled_bytes(nt, id_), "out")
     _check(load().quantize_q8_tiled(_dev_ptr(x, "x"), nt, id_, ldx, _dev_ptr(out, "q8t"), _stream(stream)),
            "quantize_q8_tiled")
@@ -404,7 +427,7 @@ def quantize_q8_tiled(x, id_: int | None = None, out=None, stream=None):
 
 def mmq_q4k_q8t(W, od: int, id_: int, q8t, nt: int, y=None, ldy: int | None = None, ws=None, stream=None):
     """mmq_q4k on a tiled activation plane; ws: None (whole tiles) or a stream-K workspace."""
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     _gemm_checks(W, _raw_bytes(od, id_, 144), q8t, q8_tiled_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q4k_q8t(_dev_ptr(W, "W"), od, id_, _dev_ptr(q8t, "q8t"), nt, _dev_ptr(y, "y"), ldy,
                               _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q4k_q8t")
@@ -416,7 +439,7 @@ def mmq_q4k_xf32(W, od: int, id_: int, x, y=None, ldy: int | None = None, ws=Non
     the GEMM: y bit-identical to quantize_q8_tiled then mmq_q4k_q8t.  ws:
     None (whole tiles) or a stream-K workspace."""
     nt, ldx, id_ = _x_rows(x, id_)
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     _gemm_checks(W, _raw_bytes(od, id_, 144), None, 0, nt, od, y, ldy, ws=ws)
     _check(load().mmq_q4k_xf32(_dev_ptr(W, "W"), od, id_, _dev_ptr(x, "x"), ldx, nt, _dev_ptr(y, "y"), ldy,
                                _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q4k_xf32")
@@ -426,7 +449,7 @@ def mmq_q4k_xf32(W, od: int, id_: int, x, y=None, ldy: int | None = None, ws=Non
 def mmq_q6k_q8t(W, bstride: int, od: int, id_: int, q8t, nt: int, W_exp=None, y=None, ldy: int | None = None,
                 ws=None, stream=None):
     """mmq_q6k on a tiled activation plane; ws: None (whole tiles) or a stream-K workspace."""
-    y, ldy = _out_y(y, nt, od, ldy, W.device)
+    y, ldy = _out_y(y, nt, od, ldy, W.device, stream)
     _gemm_checks(W, _raw_bytes(od, id_, bstride), q8t, q8_tiled_bytes(nt, id_), nt, od, y, ldy, W_exp, id_, ws)
     _check(load().mmq_q6k_q8t(_dev_ptr(W, "W"), bstride, _dev_ptr(W_exp, "W_exp"), od, id_, _dev_ptr(q8t, "q8t"),
                               nt, _dev_ptr(y, "y"), ldy, _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q6k_q8t")
@@ -436,7 +459,7 @@ def mmq_q6k_q8t(W, bstride: int, od: int, id_: int, q8t, nt: int, W_exp=None, y=
 def mmq_q4k_prepared_q8t(Wp, od: int, id_: int, q8t, nt: int, y=None, ldy: int | None = None, ws=None,
                          stream=None):
     """mmq_q4k_prepared on a tiled activation plane."""
-    y, ldy = _out_y(y, nt, od, ldy, Wp.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wp.device, stream)
     _gemm_checks(Wp, prepared_bytes("q4_K", od, id_), q8t, q8_tiled_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q4k_prepared_q8t(_dev_ptr(Wp, "Wp"), od, id_, _dev_ptr(q8t, "q8t"), nt, _dev_ptr(y, "y"),
                                        ldy, _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q4k_prepared_q8t")
@@ -446,7 +469,7 @@ def mmq_q4k_prepared_q8t(Wp, od: int, id_: int, q8t, nt: int, y=None, ldy: int |
 def mmq_q6k_prepared_q8t(Wp, od: int, id_: int, q8t, nt: int, y=None, ldy: int | None = None, ws=None,
                          stream=None):
     """mmq_q6k_prepared on a tiled activation plane."""
-    y, ldy = _out_y(y, nt, od, ldy, Wp.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wp.device, stream)
     _gemm_checks(Wp, prepared_bytes("q6_K", od, id_), q8t, q8_tiled_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q6k_prepared_q8t(_dev_ptr(Wp, "Wp"), od, id_, _dev_ptr(q8t, "q8t"), nt, _dev_ptr(y, "y"),
                                        ldy, _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q6k_prepared_q8t")
@@ -464,7 +487,7 @@ def prepare_q6k_limbs(W, bstride: int, od: int, id_: int, out=None, stream=None)
     """Raw q6_K plane -> limb buffer (v = sc*c6 = 128 H + L per element, and d)."""
     import torch
     if out is None:
-        out = torch.empty(q6k_limbs_bytes(od, id_), dtype=torch.uint8, device=W.device)
+        out = _empty(q6k_limbs_bytes(od, id_), torch.uint8, W.device, stream)
     _need(W, _raw_bytes(od, id_, bstride), "W")
     _need(out, q6k_limbs_bytes(od, id_), "out")
     _check(load().prepare_q6k_limbs(_dev_ptr(W, "W"), bstride, od, id_, _dev_ptr(out, "Wl"), _stream(stream)),
@@ -474,7 +497,7 @@ def prepare_q6k_limbs(W, bstride: int, od: int, id_: int, out=None, stream=None)
 
 def mmq_q6k_limbs_q8t(Wl, od: int, id_: int, q8t, nt: int, y=None, ldy: int | None = None, ws=None, stream=None):
     """y[nt][od] of the q6_K GEMM from a limb buffer and a tiled activation plane."""
-    y, ldy = _out_y(y, nt, od, ldy, Wl.device)
+    y, ldy = _out_y(y, nt, od, ldy, Wl.device, stream)
     _gemm_checks(Wl, q6k_limbs_bytes(od, id_), q8t, q8_tiled_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q6k_limbs_q8t(_dev_ptr(Wl, "Wl"), od, id_, _dev_ptr(q8t, "q8t"), nt, _dev_ptr(y, "y"), ldy,
                                     _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q6k_limbs_q8t")
@@ -491,7 +514,7 @@ def prepare_q4k_staged(W, od: int, id_: int, out=None, stream=None):
     bytes the GEMM stages into LDS)."""
     import torch
     if out is None:
-        out = torch.empty(q4k_staged_bytes(od, id_), dtype=torch.uint8, device=W.device)
+        out = _empty(q4k_staged_bytes(od, id_), torch.uint8, W.device, stream)
     _need(W, _raw_bytes(od, id_, 144), "W")
     _need(out, q4k_staged_bytes(od, id_), "out")
     _check(load().prepare_q4k_staged(_dev_ptr(W, "W"), od, id_, _dev_ptr(out, "Ws"), _stream(stream)),
@@ -502,7 +525,7 @@ def prepare_q4k_staged(W, od: int, id_: int, out=None, stream=None):
 def mmq_q4k_staged_q8t(Ws, od: int, id_: int, q8t, nt: int, y=None, ldy: int | None = None, ws=None, stream=None):
     """y[nt][od] of the q4_K GEMM from a staged buffer and a tiled activation
     plane (bit-identical to mmq_q4k_q8t)."""
-    y, ldy = _out_y(y, nt, od, ldy, Ws.device)
+    y, ldy = _out_y(y, nt, od, ldy, Ws.device, stream)
     _gemm_checks(Ws, q4k_staged_bytes(od, id_), q8t, q8_tiled_bytes(nt, id_), nt, od, y, ldy, ws=ws)
     _check(load().mmq_q4k_staged_q8t(_dev_ptr(Ws, "Ws"), od, id_, _dev_ptr(q8t, "q8t"), nt, _dev_ptr(y, "y"), ldy,
                                      _dev_ptr(ws, "ws"), _stream(stream)), "mmq_q4k_staged_q8t")
