@@ -349,7 +349,8 @@ def workspace(device=None, stream=None):
     ws = _workspaces.get(key)
     if ws is None:
         # zeroed on the stream that uses it first
-        with torch.cuda.stream(stream or torch.cuda.current_stream(index)):
+        on = torch.cuda.current_stream(index) if stream is None else _torch_stream(stream, torch.device("cuda", index))
+        with torch.cuda.stream(on):
             ws = new_workspace(torch.device("cuda", index))
             # a captured fill has not run yet, and runs with its own graph alone
             if not torch.cuda.is_current_stream_capturing():
