@@ -324,19 +324,31 @@ def mmq_q6k_prepared(Wp, od: int, id_: int, q8, nt: int, y=None, ldy: int | None
 
 # --- stream-K variants -------------------------------------------------------
 
-_workspaces = {}
+_workspaces = {}   # (device, stream) -> its workspace
+_captured = {}     # (device, stream) -> (id of its last capture without one, the workspace made in that)
+COUNTER_BYTES = 16384   # a workspace's arrival counters, its last bytes
+
+
+def _capture_id(handle: int) -> int:
+    """The id of the capture that a capturing stream is in."""
+    status, ident = ctypes.c_int(), ctypes.c_ulonglong()
+    # the HIP runtime that the library is linked with
+    rc = load().hipStreamGetCaptureInfo(ctypes.c_void_p(handle), ctypes.byref(status), ctypes.byref(ident))
+    if rc != 0:
+        raise QigError(f"hipStreamGetCaptureInfo failed (error {rc})")
+    return ident.value
 
 
 def workspace(device=None, stream=None):
     """The default stream-K workspace of a (device, stream) pair:
-    mmq_workspace_bytes() zero bytes, allocated on first use and kept.  Calls on
-    one stream run in order and may share it; keying it by stream keeps calls
-    that may overlap on different streams from sharing its arrival counters.
-    Every call leaves the counters at zero; a call interrupted by a device
-    fault does not, but such a fault also ends the HIP context the workspace
-    lives in.  In a capture, a pair that has none yet gets a new one at each
-    call, zeroed by the graph itself; graphs that share one made before must
-    not be replayed at the same time."""
+    mmq_workspace_bytes() bytes with zero arrival counters, allocated on first
+    use and kept.  Calls on one stream run in order and may share it; keying it
+    by stream keeps calls that may overlap on different streams from sharing its
+    counters.  Every call leaves the counters at zero; a call interrupted by a
+    device fault does not, but such a fault also ends the HIP context the
+    workspace lives in.  In a capture, a pair that has none yet gets one for
+    that capture's calls alone, its counters zeroed by the graph itself; graphs
+    that share one made before must not be replayed at the same time."""
     import torch
     index = None if device is None else torch.device(device).index
     if index is None:
@@ -351,17 +363,25 @@ def workspace(device=None, stream=None):
         # zeroed on the stream that uses it first
         on = torch.cuda.current_stream(index) if stream is None else _torch_stream(stream, torch.device("cuda", index))
         with torch.cuda.stream(on):
-            ws = new_workspace(torch.device("cuda", index))
-            # a captured fill has not run yet, and runs with its own graph alone
             if not torch.cuda.is_current_stream_capturing():
-                _workspaces[key] = ws
+                ws = _workspaces[key] = new_workspace(torch.device("cuda", index))
+                _captured.pop(key, None)
+            else:
+                # a captured fill has not run yet, and runs with its own graph alone
+                ident = _capture_id(key[1])
+                if key not in _captured or _captured[key][0] != ident:
+                    _captured[key] = (ident, new_workspace(torch.device("cuda", index)))
+                ws = _captured[key][1]
     return ws
 
 
 def new_workspace(device):
-    """A fresh zero-filled stream-K workspace (uint8, mmq_workspace_bytes() bytes)."""
+    """A fresh stream-K workspace (uint8, mmq_workspace_bytes() bytes): its
+    counters are zero, its partial sums are written before they are read."""
     import torch
-    return torch.zeros(int(load().mmq_workspace_bytes()), dtype=torch.uint8, device=device)
+    ws = torch.empty(int(load().mmq_workspace_bytes()), dtype=torch.uint8, device=device)
+    ws[-COUNTER_BYTES:].zero_()
+    return ws
 
 
 def mmq_q4k_streamk(W, od: int, id_: int, q8, nt: int, y=None, ldy: int | None = None, ws=None, stream=None):

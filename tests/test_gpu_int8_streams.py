@@ -1,9 +1,11 @@
-"""Default workspaces, and streams given by their handles."""
+"""Default workspaces, inside captures too, and streams given by their handles."""
 import pytest
 
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+
+COUNTERS = 16384   # a workspace's last bytes
 
 
 @pytest.fixture(scope="module")
@@ -21,6 +23,56 @@ def _split_operands(seed):
     W = torch.randint(-128, 128, (od, id_), dtype=torch.int8, device="cuda")
     q = torch.randint(-127, 128, (nt, id_), dtype=torch.int8, device="cuda")
     return W, torch.rand(od, device="cuda") * 0.02, q, torch.rand(nt, device="cuda") * 1e-3
+
+
+def test_one_default_workspace_a_capture(qig):
+    """The calls of a capture share one workspace, made in it and not known to
+    another capture; the graph zeroes its counters alone."""
+    a = _split_operands(1)
+    dev = a[0].device
+    want = qig.mm_i8(*a)
+    ys = [torch.zeros_like(want) for _ in range(4)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    graphs, spaces = [], []
+    for i in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            w0 = qig.workspace(dev)
+            qig.mm_i8(*a, y=ys[2 * i], ws=w0)
+            w1 = qig.workspace(dev)
+            qig.mm_i8(*a, y=ys[2 * i + 1], ws=w1)
+        assert w0.data_ptr() == w1.data_ptr(), "a second workspace in one capture"
+        graphs.append(gr)
+        spaces.append(w0)
+    assert spaces[0].data_ptr() != spaces[1].data_ptr()
+    partial = qig.load().mmq_workspace_bytes() - COUNTERS
+    for w in spaces:
+        assert w.numel() == partial + COUNTERS
+    for i in (1, 0, 0, 1):
+        for y in ys:
+            y.zero_()
+        spaces[i].fill_(0xA5)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ys[2 * i], want) and torch.equal(ys[2 * i + 1], want), i
+        assert int(torch.count_nonzero(spaces[i][partial:])) == 0, "counters"
+        assert bool((spaces[i][partial - 4096:partial] == 0xA5).all()), "the partial sums' slots were filled"
+        assert torch.equal(qig.mm_i8(*a), want)
+
+
+def test_new_workspace_has_zero_counters(qig):
+    """Also where its memory held something else."""
+    n = int(qig.load().mmq_workspace_bytes())
+    torch.cuda.empty_cache()
+    old = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    del old
+    ws = qig.new_workspace("cuda")
+    assert ws.numel() == n and ws.dtype == torch.uint8
+    assert int(torch.count_nonzero(ws[-COUNTERS:])) == 0
+    a = _split_operands(2)
+    assert torch.equal(qig.mm_i8(*a), qig.mm_i8(*a, ws=ws))
+    assert int(torch.count_nonzero(ws[-COUNTERS:])) == 0
 
 
 class Handle:
