@@ -436,8 +436,11 @@ int mm_i8(const int8_t *W, int64_t ldw, const float *sw, int64_t od,
  *   ids = the k experts with the largest c, largest first;
  *   w = p of those experts, divided by their sum if renorm, times scale.
  * Equal values go to the lower index.  p and c are formed and compared in 64
- * bits (softmax without a bias: the logits themselves are compared), w is
- * rounded once.  A logit of -infinity or NaN is an expert that may not be
+ * bits, w is rounded once.  For softmax without a bias the logits themselves
+ * are compared, so that scores which underflow to 0 (745 below the row's largest
+ * logit) keep their order; only where groups are ranked by two scores (groups
+ * > 1, group_top 2) are p and their sums compared throughout, and scores of 0
+ * are equal.  A logit of -infinity or NaN is an expert that may not be
  * chosen (+infinity counts as the largest fp32 number): where fewer than k
  * can be chosen the remaining ids are -1 with weight 0.  renorm over a sum of
  * 0 gives weights 0.

@@ -16,9 +16,10 @@ namespace qig {
 // expert wins is a comparison of near values: it is decided in 64 bits, since
 // in 32 the rounding of exp would decide about one row in ten thousand.
 // Softmax without a bias keeps the order of the logits, so there the choice
-// compares the logits themselves (also where the scores underflow).  A logit of
-// -infinity or NaN is an expert that may not be chosen; +infinity counts as the
-// largest finite number.
+// compares the logits themselves (also where the scores underflow), unless groups
+// are ranked by the sum of two scores: then groups and experts go by the scores.
+// A logit of -infinity or NaN is an expert that may not be chosen; +infinity
+// counts as the largest finite number.
 //
 // Only rows that need 64 bits pay for them: route_kernel first chooses by c in
 // 32 bits with a bound on its error.  Where neighbours among the first k + 1 are
