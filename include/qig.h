@@ -530,6 +530,16 @@ int mmq_q6k_partials(const void *W, int64_t bstride, const int8_t *W_exp,
                      int64_t t0, int64_t t1, int64_t j0, int64_t j1, int32_t *P,
                      hipStream_t stream);
 
+/*
+ * Test export: which kernel a product of these sizes takes (ne = 0: mm_i8,
+ * with or without a workspace; ne > 0: mm_i8_experts of nt rows), as
+ *   100 * (token rows of a tile) + 10 * (stages of its activations in LDS)
+ *   + (shares that the sums are split into),
+ * 1601 for the few-token kernel.  QIG_EINVAL for sizes that the calls refuse or
+ * that have no work.
+ */
+int mm_i8_form(int64_t ne, int64_t od, int64_t id, int64_t nt, int glu, int ws);
+
 #ifdef __cplusplus
 }
 #endif

@@ -64,6 +64,7 @@ SIGNATURES = {
     "mm_i8_experts": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _int,
                                      _vp, _int, _i64, _vp]),
     "combine_experts": (ctypes.c_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _vp, _int, _i64, _vp]),
+    "mm_i8_form": (ctypes.c_int, [_i64, _i64, _i64, _i64, _int, _int]),
 }
 
 

@@ -121,4 +121,16 @@ int combine_experts(const void *h, int htype, int64_t ldh, const float *w, int64
     return rc_from_launch(qig::launch_combine(h, htype, ldh, w, nt, k, od, y, ytype, ldy, stream));
 }
 
+int mm_i8_form(int64_t ne, int64_t od, int64_t id, int64_t nt, int glu, int ws)
+{
+    if (ne < 0 || ne > qig::EXPERTS_MAX || od < 1 || od >= INT_LIM / 2 || id < 1 || id > qig::I8_MAX_ID || nt < 1 ||
+        nt >= INT_LIM || (glu != 0 && glu != 1))
+        return QIG_EINVAL;
+    qig::I8Gemm g = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, id, id, od, od, id, nt, glu, QIG_F32};
+    g.ne = ne;
+    int held = 0;
+    g.ws = ws ? &held : nullptr;   // there or not: never read
+    return qig::i8_form(g);
+}
+
 }  // extern "C"

@@ -907,49 +907,71 @@ constexpr double ROWS_64 = 16, ROWS_256 = 96, TILES_64 = 256, TILES_128 = 256, T
 // in nine).  SPLIT_SLOTS and SPLIT_TILES are what the workspace holds.
 constexpr int SPLIT_STEPS = 16, SPLIT_MOST = 4, SPLIT_SLOTS = 1024, SPLIT_TILES = 4096, SPLIT_CUS = 256;
 
-template <bool GLU, int YT>
-static int pick_dense(I8Args a, hipStream_t stream)
+// The kernels' forms: 100 * token rows of a tile + 10 * stages of activations
+// (0: the few-token kernel).
+enum Form { FEW = 1600, T32 = 3240, T64S = 6420, T64 = 6440, T128 = 12820, T192 = 19220, T256 = 25620 };
+
+// The form of a product, and into how many shares its sums are split.
+template <bool GLU>
+static Form dense_form(const I8Args &a, int &splits)
 {
+    splits = 1;
     const int64_t wbytes = (GLU ? 2 : 1) * a.od * (int64_t)a.id;
     // (more weight rows than a launch of it holds, from 2^27 on, go to the tiles)
     if ((a.nt <= 16 && (a.od + GEMV_ROWS - 1) / GEMV_ROWS <= launch_groups(GEMV_WAVES * 64)) ||
         (a.nt <= 64 && (a.nt + 15) / 16 * wbytes <= GEMV_BYTES))
-        return launch_gemv<GLU, false, YT>(a, stream);
+        return FEW;
     const double c256 = cost<GLU>(COST_256, a), c192 = cost<GLU>(COST_192, a);
     const double c64 = cost<GLU>(COST_64, a), c64s = cost<GLU>(COST_64S, a);
-    if (std::min(c64, c64s) >= std::min(c192, c256)) {
-        if (c192 < c256) return launch_tile<192, 256, 2, 4, 2, 3, false, GLU, false, YT>(a, a.od, a.nt, stream);
-        return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, false, YT>(a, a.od, a.nt, stream);
-    }
-    if (c64s < c64) return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    if (std::min(c64, c64s) >= std::min(c192, c256)) return c192 < c256 ? T192 : T256;
+    if (c64s < c64) return T64S;
     const int64_t tiles = (a.nt + 63) / 64 * ((a.od + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
     const int64_t nk = (a.id + BK - 1) / BK;
-    const int64_t splits = std::min<int64_t>(std::min<int64_t>(nk / SPLIT_STEPS, SPLIT_MOST), SPLIT_CUS / tiles);
-    if (a.part && splits >= 2 && tiles * splits <= SPLIT_SLOTS && tiles <= SPLIT_TILES) {
-        a.splits = (int)splits;
-        return launch_tile<64, 128, 2, 2, 4, 4, true, GLU, false, YT>(a, a.od, a.nt, stream);
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(nk / SPLIT_STEPS, SPLIT_MOST), SPLIT_CUS / tiles);
+    if (a.part && most >= 2 && tiles * most <= SPLIT_SLOTS && tiles <= SPLIT_TILES) splits = (int)most;
+    return T64;
+}
+
+template <bool GLU, int YT>
+static int pick_dense(I8Args a, hipStream_t stream)
+{
+    switch (dense_form<GLU>(a, a.splits)) {
+    case FEW: return launch_gemv<GLU, false, YT>(a, stream);
+    case T192: return launch_tile<192, 256, 2, 4, 2, 3, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    case T256: return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    case T64S: return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, false, YT>(a, a.od, a.nt, stream);
+    default: break;
     }
+    if (a.splits > 1) return launch_tile<64, 128, 2, 2, 4, 4, true, GLU, false, YT>(a, a.od, a.nt, stream);
     return launch_tile<64, 128, 2, 2, 4, 4, false, GLU, false, YT>(a, a.od, a.nt, stream);
+}
+
+template <bool GLU>
+static Form experts_form(const I8Args &a)
+{
+    const int64_t used = a.nt < a.ne ? a.nt : a.ne, rows = (GLU ? 2 : 1) * a.od;
+    const double each = (double)a.nt / (double)used;
+    if (each <= EXPERTS_GEMV_ROWS && used * rows * a.id <= EXPERTS_GEMV_BYTES) return FEW;
+    auto tiles = [&](int bm, int bn) {   // half a tile lost in each expert
+        return ((double)a.nt / bm + 0.5 * (double)used) * (double)((rows + bn - 1) / bn);
+    };
+    if (each >= ROWS_256 && tiles(256, 256) >= TILES_256) return T256;
+    if (each < ROWS_64) return T32;
+    if (tiles(128, 256) >= TILES_128) return T128;
+    return tiles(64, 128) > TILES_64 ? T64S : T64;
 }
 
 template <bool GLU, int YT>
 static int pick_experts(const I8Args &a, hipStream_t stream)
 {
-    const int64_t used = a.nt < a.ne ? a.nt : a.ne, rows = (GLU ? 2 : 1) * a.od;
-    const double each = (double)a.nt / (double)used;
-    if (each <= EXPERTS_GEMV_ROWS && used * rows * a.id <= EXPERTS_GEMV_BYTES)
-        return launch_gemv<GLU, true, YT>(a, stream);
-    auto tiles = [&](int bm, int bn) {   // half a tile lost in each expert
-        return ((double)a.nt / bm + 0.5 * (double)used) * (double)((rows + bn - 1) / bn);
-    };
-    if (each >= ROWS_256 && tiles(256, 256) >= TILES_256)
-        return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    if (each < ROWS_64) return launch_tile<32, 128, 1, 4, 4, 4, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    if (tiles(128, 256) >= TILES_128)
-        return launch_tile<128, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    if (tiles(64, 128) > TILES_64)
-        return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
-    return launch_tile<64, 128, 2, 2, 4, 4, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    switch (experts_form<GLU>(a)) {
+    case FEW: return launch_gemv<GLU, true, YT>(a, stream);
+    case T256: return launch_tile<256, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    case T32: return launch_tile<32, 128, 1, 4, 4, 4, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    case T128: return launch_tile<128, 256, 2, 4, 2, 3, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    case T64S: return launch_tile<64, 128, 2, 2, 2, 2, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    default: return launch_tile<64, 128, 2, 2, 4, 4, false, GLU, true, YT>(a, a.od, a.nt, stream);
+    }
 }
 
 template <int YT>
@@ -959,7 +981,7 @@ static int pick_form(const I8Args &a, bool glu, hipStream_t stream)
     return glu ? pick_dense<true, YT>(a, stream) : pick_dense<false, YT>(a, stream);
 }
 
-int launch_i8_gemm(const I8Gemm &g, hipStream_t stream)
+static I8Args args_of(const I8Gemm &g)
 {
     I8Args a;
     a.W = reinterpret_cast<const uint8_t *>(g.W);
@@ -982,11 +1004,26 @@ int launch_i8_gemm(const I8Gemm &g, hipStream_t stream)
     a.nbt = a.nbj = 0;
     a.ne = (int)g.ne;
     a.slots = (int)g.slots;
+    return a;
+}
+
+int launch_i8_gemm(const I8Gemm &g, hipStream_t stream)
+{
+    const I8Args a = args_of(g);
     switch (g.ytype) {
     case T_F32: return pick_form<T_F32>(a, g.glu != 0, stream);
     case T_BF16: return pick_form<T_BF16>(a, g.glu != 0, stream);
     default: return pick_form<T_F16>(a, g.glu != 0, stream);
     }
+}
+
+int i8_form(const I8Gemm &g)
+{
+    const I8Args a = args_of(g);
+    if (g.ne > 0) return (g.glu ? experts_form<true>(a) : experts_form<false>(a)) + 1;
+    int splits;
+    const Form f = g.glu ? dense_form<true>(a, splits) : dense_form<false>(a, splits);
+    return f + splits;
 }
 
 }  // namespace qig

@@ -56,6 +56,8 @@ constexpr int64_t plan_words(int64_t nrows, int64_t ne) { return ne + 2 + nrows;
 int launch_quantize_i8(const void *x, int xtype, int64_t nt, int64_t id, int64_t ldx, int8_t *q, int64_t ldq,
                        float *s, hipStream_t stream);
 int launch_i8_gemm(const I8Gemm &g, hipStream_t stream);
+// The kernel that launch_i8_gemm takes (ne > 0: experts), as mm_i8_form codes it.
+int i8_form(const I8Gemm &g);
 int launch_route(const RouteArgs &a, hipStream_t stream);
 int launch_plan(const int32_t *ids, int64_t nrows, int64_t ne, int32_t *plan, hipStream_t stream);
 int launch_combine(const void *h, int htype, int64_t ldh, const float *w, int64_t nt, int64_t k, int64_t od,
