@@ -282,9 +282,9 @@ def mm_i8_experts(W, sw, q, sq, plan, nrows, bias=None, glu=False, y=None, dtype
         raise QigError("W must be [experts][rows][id] with unit stride in the last dimension")
     ne, rows, id_ = shape
     ldw = stride[1] if rows > 1 else stride[0]
-    if ne > 1 and stride[0] != rows * ldw:
+    if ne > 1 and rows > 0 and stride[0] != rows * ldw:
         raise QigError("W's experts must follow each other: stride(0) == shape[1] * stride(1)")
-    if rows <= 1 and ne <= 1:
+    if ne * rows <= 1:
         ldw = (id_ + 15) // 16 * 16
     if id_ % 16:
         _rows16(W, ne * rows, id_, ldw, "W")

@@ -2,6 +2,8 @@
 (the runtime would run a part of them without an error)."""
 import ctypes
 
+import pytest
+
 import quant_integer_gemm_amd as qig
 
 P = ctypes.c_void_p(0x10000)   # never dereferenced: the calls are refused
@@ -24,3 +26,13 @@ def test_k_quant_calls_too():
     assert lib.quantize_q8_tiled(P, 1 << 22, 8192, 8192, P, None) == -1
     # 64 x 64 tiles of 256 threads
     assert lib.mmq_q4k(P, 1 << 20, 256, P, 1 << 16, P, 1 << 20, None) == -1
+
+
+def test_experts_without_weight_rows_pass_the_stride_check():
+    """Four experts of no rows have no stride to get wrong: on the CPU the call
+    ends at its check of the device."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    with pytest.raises(qig.QigError, match="GPU tensor"):
+        qig.mm_i8_experts(z(4, 0, 32, dtype=torch.int8), z(4, 0), z(3, 32, dtype=torch.int8), z(3),
+                          z(12, dtype=torch.int32), 6)
