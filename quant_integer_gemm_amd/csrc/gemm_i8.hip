@@ -626,7 +626,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gemm_i8_kernel(I8Args g)
                             const f32x4 b1 = *reinterpret_cast<const f32x4 *>(s_bias + at + 16);
                             const float ga = (float)acc[m][2 * n][i] * s * w[i] + b[i];
                             const float up = (float)acc[m][2 * n + 1][i] * s * w1[i] + b1[i];
-                            v[i] = silu_mul(ga, up);
+                            v[i] = silu_mul<YT>(ga, up);
                         } else {
                             v[i] = (float)acc[m][n][i] * s * w[i] + b[i];
                         }
@@ -822,7 +822,7 @@ __global__ __launch_bounds__(GEMV_WAVES * 64) void gemv_i8_kernel(I8Args g)
     if (l16 >= count || o >= g.od) return;
     const float s = s_sq[l16];
     float r = (float)v[0] * s * sw[o] + (bias ? bias[o] : 0.0f);
-    if constexpr (GLU) r = silu_mul(r, (float)v[NB - 1] * s * sw[g.od + o] + (bias ? bias[g.od + o] : 0.0f));
+    if constexpr (GLU) r = silu_mul<YT>(r, (float)v[NB - 1] * s * sw[g.od + o] + (bias ? bias[g.od + o] : 0.0f));
     const int64_t row = EXPERTS ? (int64_t)s_row[l16] : t0 + l16;
     y[row * g.ldy + o] = (elem_t<YT>)r;
 }

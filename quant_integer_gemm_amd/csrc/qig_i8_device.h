@@ -71,22 +71,31 @@ __device__ __forceinline__ void store16(elem_t<T> *p, u32x4 v)
     *reinterpret_cast<u32x4u *>(p) = v;
 }
 
-// a * sigmoid(a) * b in fp32 from the hardware's exp2 and reciprocal (each
-// within an ulp).  t = a * -log2(e) loses up to 2^-18 to its rounding, which
-// would be that much of the exponential: the product's low part (and that of
-// log2(e)) is added behind exp2, as the factor 1 + low * ln 2.  With it all
-// roundings together are below 10 * 2^-24 of the value, whatever a is.  For a far
-// below zero exp2 overflows and the reciprocal of infinity gives the limit 0
-// (below -87.3 it is already below the smallest normal number); beyond +-128 the
-// exponential is 0 or infinity, so a is held there, where no product overflows.
+// a * sigmoid(a) * b in fp32, for an output of type T, from the hardware's exp2
+// and reciprocal (each within an ulp).  t = a * -log2(e) loses up to 2^-18 to its
+// rounding, which would be that much of the exponential (59 * 2^-24 of the value
+// at a = -63).  For fp32 outputs the product's low part, and that of log2(e), is
+// added behind exp2 as the factor 1 + low * ln 2: all roundings together are below
+// 10 * 2^-24 of the value, whatever a is.  16-bit outputs, whose own rounding is
+// 2^-12 or more, go without (four instructions an output: 2630 tokens of 2 x 18944
+// x 3584 to bf16 would take 320 us for 315).  For a far below zero exp2 overflows
+// and the reciprocal of infinity gives the limit 0 (below -87.3 it is already below
+// the smallest normal number); beyond +-128 the exponential is 0 or infinity, so a
+// is held there, where the low part is small.
+template <int T>
 __device__ __forceinline__ float silu_mul(float a, float b)
 {
     constexpr float L = -1.44269502f, L_LOW = -1.92596303e-8f;   // -log2(e) = L + L_LOW
-    const float x = __builtin_amdgcn_fmed3f(a, -128.0f, 128.0f);
-    const float t = x * L;
-    const float low = __builtin_fmaf(x, L_LOW, __builtin_fmaf(x, L, -t));
-    const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, 0.693147181f, 1.0f);
-    return a * __builtin_amdgcn_rcpf(1.0f + e) * b;
+    float e1;
+    if constexpr (T == T_F32) {
+        const float x = __builtin_amdgcn_fmed3f(a, -128.0f, 128.0f);
+        const float t = x * L;
+        const float low = __builtin_fmaf(x, L_LOW, __builtin_fmaf(x, L, -t));
+        e1 = __builtin_fmaf(__builtin_amdgcn_exp2f(t), __builtin_fmaf(low, 0.693147181f, 1.0f), 1.0f);
+    } else {
+        e1 = 1.0f + __builtin_amdgcn_exp2f(a * L);
+    }
+    return a * __builtin_amdgcn_rcpf(e1) * b;
 }
 
 }  // namespace qig
