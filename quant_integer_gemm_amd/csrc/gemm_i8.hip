@@ -12,8 +12,8 @@
 // What bounds it, and what it reaches: large products are held by the card's
 // power (the clock falls from 2.4 to 1.75 GHz; zeros as data run at 2.4).  8192^3
 // 420 us, 2610 TOPS, above the vendor library's product on the same card (2500);
-// 2630 tokens, 2 x 18944 x 3584 gated to bf16 306 us, 2330 TOPS; 18944 -> 3584 to
-// fp32 148 us, 2420 TOPS (157 us with operands from HBM).  Of the 8192^3 time, an
+// 2630 tokens, 2 x 18944 x 3584 gated to bf16 306 us, 2330 TOPS (317 on another
+// card); 18944 -> 3584 to fp32 148 us, 2420 TOPS (157 us with operands from HBM).  Of the 8192^3 time, an
 // earlier build without its copies took 16% less, one without the LDS reads 12%,
 // one with neither 27%.  Small products: launch, first loads and epilogue, 5 us,
 // then 0.25 us a step (3584 x 3584, 512 tokens 14.5 us).  Experts' products: the
@@ -890,8 +890,9 @@ constexpr int64_t GEMV_BYTES = int64_t(40) << 20;
 // with one row each 23.8 us against 19.4 us, but 6 experts' 1024 x 2048 8.5 us
 // against 9.3 us, 4 experts' 700 x 5000 8.4 us against 13.7 us.
 constexpr int64_t EXPERTS_GEMV_BYTES = int64_t(24) << 20, EXPERTS_GEMV_ROWS = 16;
-// Rows of an expert, on average, from which the larger tiles are faster, and
-// the tiles it takes for that.  With few rows what counts is how evenly the
+// Rows of an expert, on average (the host knows no more: where routing is skewed,
+// a few experts with most rows walk small tiles), from which the larger tiles are
+// faster, and the tiles it takes for that.  With few rows what counts is how evenly the
 // weights' bytes spread over the CUs and how many are in flight: 32 x 128 tiles
 // with four stages, two workgroups a CU.  64 experts' 4736 x 3584, us for
 // 32 x 128, 64 x 128, 128 x 256 and 256 x 256: 24 rows (23 experts) 73, 88, 85, -;
