@@ -515,6 +515,183 @@ int combine_experts(const void *h, int htype, int64_t ldh, const float *w,
                     int64_t ldy, hipStream_t stream);
 
 /*
+ * Attention and its cache, between a layer's q / k / v products and its o
+ * product: over whole prompts (attend_prompt), and over a paged cache of
+ * keys and values in 4 bits (write_kv4, read_kv4, attend_kv4), whose pages are
+ * given to sequences, shared, copied and packed by the pages' calls.
+ *
+ * Tokens are packed: sequence s has the rows starts[s] .. starts[s + 1] - 1
+ * (starts [nseq + 1] int32 on the device, not decreasing, inside [0, rows]).
+ * Starts that break this give unspecified results, but nothing outside of the
+ * tensors is touched.  Tensors of heads are [token][head][d] with unit stride in
+ * d; the other strides are in elements, >= 0, and any address aligned to an
+ * element will do (so q, k and v may be parts of one product's output).  hq is a
+ * multiple of hkv, both at most 1024; query heads [i * hq / hkv, (i + 1) * hq /
+ * hkv) share key head i.
+ */
+
+/*
+ * attend_prompt -- attention over whole prompts:
+ *   y[i] = sum over j of p_j v[j],  p = softmax over j of scale * q[i] . k[j],
+ * j the keys of the query's sequence that it sees: all of them, or with causal =
+ * 1 those at positions up to its own, where the last query stands at the last key's
+ * position (n queries and nk keys: query i sees keys 0 .. nk - n + i; with more
+ * keys than queries the first ones are a prefix).  A query that sees nothing gets
+ * zeros.  What a query does not see has no effect; a NaN or an infinity among what
+ * it sees makes its results NaN or infinite (a value's, those of its channel).
+ * fp32 operands are multiplied in fp32.  16-bit operands are multiplied exactly and
+ * summed in fp32; p is rounded to their type for the second product.  y is rounded
+ * once.
+ *
+ *   q      [nt][hq][d], k and v [nk][hkv][d], elements of type
+ *   d      a multiple of 8 from 8 to 256
+ *   starts of q's rows, k_starts of k's and v's (the same array for whole prompts)
+ *   scale  0 for 1 / sqrt(d), else above 0 and at most 1e30
+ *   y      [nt][hq][d] elements of ytype; rows outside of every sequence are left as
+ *          they were; rows must not overlap
+ * Errors: QIG_EINVAL (unknown type, nt, nk or nseq < 0 or >= 2^31 - 1, heads, d, a
+ *         negative stride, causal not 0 or 1, scale, or more tiles than a launch
+ *         holds: nt / 128 + nseq tiles of queries by hq, at most 2^23),
+ *         QIG_EALIGN, QIG_ELAUNCH.
+ */
+int attend_prompt(const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token, int64_t k_head,
+                  const void *v, int64_t v_token, int64_t v_head, int type, int64_t nt, int64_t nk, int64_t hq,
+                  int64_t hkv, int64_t d, const int32_t *starts, const int32_t *k_starts, int64_t nseq, int causal,
+                  float scale, void *y, int64_t y_token, int64_t y_head, int ytype, hipStream_t stream);
+
+/*
+ * The 4-bit cache.  A row of d values (one token, one head, its keys or its
+ * values) is kept in groups of 32.  With lo and hi the lowest and highest of a
+ * group,
+ *   m = the largest bf16 <= lo,  s = the smallest bf16 >= (hi - m) / 15,
+ *   c = floor((x - m) / s + 1/2) held to 0 .. 15   (0 where s = 0),
+ * decided exactly in 64 bits, and the group stands for m + s * c (formed in fp32):
+ * no value is off by more than s / 2.  A group with a NaN or an infinity in it, or a
+ * value beyond the bf16 range, stands for NaN.
+ *
+ * A page holds `page` tokens of hkv heads: [hkv][page / 32] blocks of 32 tokens,
+ * 10 d words each (1.25 d bytes a token and head, keys and values together).  In a
+ * block, token 16 u + 4 h + i (u < 2; h, i < 4) has
+ *   keys, words 0 .. 4 d:      channel 32 g + 8 e + 2 b + a in the 4 bits from 16 a +
+ *     4 b on of word ((w / 4) * 64 + e * 16 + 4 h + i) * 4 + w % 4, w = u d / 32 + g
+ *   values, words 4 d .. 8 d:  channel 16 (4 n + b) + l in the 4 bits from 16 (i % 2)
+ *     + 4 b on of word ((w / 4) * 64 + h * 16 + l) * 4 + w % 4, w = (2 u + i / 2) d / 64 + n
+ *   scales, words 8 d .. 9 d for keys and 9 d .. 10 d for values: group g in word
+ *     (h * 8 + u * 4 + i) * d / 32 + g, s in its low and m in its high half,
+ * the order in which attend_kv4's lanes take their operands.
+ *
+ * Arguments shared by the calls:
+ *   pages    [npages], page_stride bytes from one to the next (a multiple of 16, at
+ *            least kv4_page_bytes), 16-byte aligned
+ *   page     tokens of a page: a multiple of 32, at most 65536
+ *   d        64, 128 or 256
+ *   tables   [nseq][ld] int32, ld >= width: the pages of a sequence's tokens, page
+ *            tables[s][p / page] for position p.  An entry outside [0, npages) (-1 by
+ *            custom) is no page.
+ *   lengths  [nseq] int32: the tokens of each sequence, the new ones included
+ *   starts   of the new tokens, the last ones of their sequences: row starts[s] + i of
+ *            n stands at position lengths[s] - n + i.  NULL: row s is sequence s's
+ *            only one (nt = nseq).
+ * Errors of all: QIG_EINVAL (sizes and strides outside of the above, an unknown
+ * type, nt != nseq without starts), QIG_EALIGN, QIG_ELAUNCH.
+ */
+
+/* Bytes of a page, 0 for invalid arguments. */
+size_t kv4_page_bytes(int64_t page, int64_t hkv, int64_t d);
+
+/* write_kv4 -- rows k, v [nt][hkv][d] into the cache.  Rows at a position below 0,
+ * beyond the table or without a page are left out.  Two sequences that share a
+ * page must not both write to it (fork_pages gives each its own). */
+int write_kv4(const void *k, int64_t k_token, int64_t k_head, const void *v, int64_t v_token, int64_t v_head, int type,
+              int64_t nt, int64_t hkv, int64_t d, void *pages, int64_t npages, int64_t page_stride, int64_t page,
+              const int32_t *tables, int64_t ld, int64_t width, const int32_t *lengths, const int32_t *starts,
+              int64_t nseq, hipStream_t stream);
+
+/* read_kv4 -- the same rows back, rounded once to type; rows that stand nowhere are
+ * zeros, those outside of every sequence are left as they were. */
+int read_kv4(void *k, int64_t k_token, int64_t k_head, void *v, int64_t v_token, int64_t v_head, int type, int64_t nt,
+             int64_t hkv, int64_t d, const void *pages, int64_t npages, int64_t page_stride, int64_t page,
+             const int32_t *tables, int64_t ld, int64_t width, const int32_t *lengths, const int32_t *starts,
+             int64_t nseq, hipStream_t stream);
+
+/*
+ * attend_kv4 -- attention of the new tokens over all cached ones of their
+ * sequences: y[i] = sum over j of p_j v[j] for the values that the cache stands
+ * for, the row at position p seeing the positions up to p.  Tokens without a page
+ * are left out; a row that sees nothing gets zeros.  fp32 sums; 22 bits or more of
+ * every product's operands are kept, for bf16 outputs 11 of p_j s_j; y is rounded
+ * once.
+ *   q      [nt][hq][d] elements of type;  y [nt][hq][d] of ytype
+ *   scale  as attend_prompt
+ *   ws     NULL, or a workspace as for the stream-K calls (the same rules): lets the
+ *          sequences be split over the GPU in equal parts whatever their lengths.
+ *          Without it each (sequence, head, 16 rows) is one workgroup's.  y differs in
+ *          the order of fp32 sums alone.
+ * Also QIG_EINVAL without ws for 2^24 or more of those.
+ */
+int attend_kv4(const void *q, int64_t q_token, int64_t q_head, int type, int64_t nt, int64_t hq, int64_t hkv, int64_t d,
+               const void *pages, int64_t npages, int64_t page_stride, int64_t page, const int32_t *tables, int64_t ld,
+               int64_t width, const int32_t *lengths, const int32_t *starts, int64_t nseq, float scale, void *y,
+               int64_t y_token, int64_t y_head, int ytype, void *ws, hipStream_t stream);
+
+/*
+ * Pages of a pool, whatever they hold: page_bytes each (a multiple of 16),
+ * page_stride bytes apart (the same), 16-byte aligned.  refs [npages] int32 counts
+ * who holds a page, rows of the table tables [rows][ld] (width entries each) or
+ * others; free is what has refs <= 0.  npages is at most 2^20, rows * width below
+ * 2^31.  Everything is int32 on the device, and the results are the same on every
+ * call.
+ *
+ * Scratch of the calls that give or move pages: pages_scratch_bytes(npages, n)
+ * bytes, 8-byte aligned, n the rows for take_pages, the pairs for fork_pages and 0
+ * for compact_pages; written before it is read.  0 for invalid arguments.
+ * Errors of all: QIG_EINVAL, QIG_EALIGN, QIG_ELAUNCH.
+ */
+size_t pages_scratch_bytes(int64_t npages, int64_t n);
+
+/* copy_pages -- page dst[i] = page src[i], i < n; pairs with an index outside of the
+ * pool are left out.  A page named twice in dst, or by different pairs in src and in
+ * dst, may end as a mixture. */
+int copy_pages(void *pages, int64_t npages, int64_t page_bytes, int64_t page_stride, const int32_t *src,
+               const int32_t *dst, int64_t n, hipStream_t stream);
+
+/* free_pages -- the rows which[0 .. n - 1] of the table give up their pages: a
+ * reference each, their entries become -1, their lengths 0.  A row named twice does
+ * so once; rows outside of the table are left out. */
+int free_pages(int32_t *tables, int64_t rows, int64_t ld, int64_t width, int32_t *lengths, int32_t *refs,
+               int64_t npages, const int32_t *which, int64_t n, hipStream_t stream);
+
+/* take_pages -- every entry below ceil(lengths[row] / page) that is no page gets a
+ * free one (refs = 1), the lowest first, in the order of rows and entries; missing
+ * [1] = how many got none (they become -1), entries beyond the table's width
+ * counted. */
+int take_pages(int32_t *tables, int64_t rows, int64_t ld, int64_t width, const int32_t *lengths, int32_t *refs,
+               int64_t npages, int64_t page, int32_t *missing, void *scratch, hipStream_t stream);
+
+/*
+ * fork_pages -- row children[i] becomes a copy of row parents[i], i < n: it gives up
+ * its pages, shares the parent's full ones (a reference more), and the parent's last
+ * page, where lengths[parent] % page != 0, is copied to the lowest free page, in the
+ * order of i.  lengths[child] = lengths[parent].  missing [1] = the copies that found
+ * no free page (the child's entry stays -1).  A pair is left out where a row lies
+ * outside of the table, a later pair names the same child, or any pair names its parent
+ * as child.
+ */
+int fork_pages(void *pages, int64_t page_bytes, int64_t page_stride, int32_t *tables, int64_t rows, int64_t ld,
+               int64_t width, int32_t *lengths, int32_t *refs, int64_t npages, int64_t page, const int32_t *parents,
+               const int32_t *children, int64_t n, int32_t *missing, void *scratch, hipStream_t stream);
+
+/*
+ * compact_pages -- the U pages in use (refs > 0) move to the front: the k-th of them at
+ * U or above goes to the k-th free page below U.  refs and the table's entries follow;
+ * used [1] = U; to [npages], or NULL, = each page's place (its own where it did not
+ * move).
+ */
+int compact_pages(void *pages, int64_t page_bytes, int64_t page_stride, int32_t *tables, int64_t rows, int64_t ld,
+                  int64_t width, int32_t *refs, int64_t npages, int32_t *used, int32_t *to, void *scratch,
+                  hipStream_t stream);
+
+/*
  * Test exports: the int32 sub-block partials of the same kernels, for the
  * window of tokens [t0, t1) and rows [j0, j1), written to
  * P[(t - t0)][(j - j0)][sub] (int32, 4-byte aligned), where sub runs over all

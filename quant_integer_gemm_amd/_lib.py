@@ -65,6 +65,22 @@ SIGNATURES = {
                                      _vp, _int, _i64, _vp]),
     "combine_experts": (ctypes.c_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _vp, _int, _i64, _vp]),
     "mm_i8_form": (ctypes.c_int, [_i64, _i64, _i64, _i64, _int, _int]),
+    "attend_prompt": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _i64, _i64, _i64,
+                                     _i64, _vp, _vp, _i64, _int, ctypes.c_float, _vp, _i64, _i64, _int, _vp]),
+    "kv4_page_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "write_kv4": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
+                                 _i64, _i64, _vp, _vp, _i64, _vp]),
+    "read_kv4": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
+                                _i64, _i64, _vp, _vp, _i64, _vp]),
+    "attend_kv4": (ctypes.c_int, [_vp, _i64, _i64, _int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64,
+                                  _vp, _vp, _i64, ctypes.c_float, _vp, _i64, _i64, _int, _vp, _vp]),
+    "copy_pages": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp]),
+    "pages_scratch_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "free_pages": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "take_pages": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "fork_pages": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
+                                  _vp, _vp]),
+    "compact_pages": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
 }
 
 
