@@ -18,33 +18,32 @@
 namespace qig {
 namespace {
 
-// Which sequence a workgroup works on.  Sequence i's tiles of BM queries have the
-// slots from starts[i] / BM + i on: those of the next begin behind its last one,
-// whatever its length, so that nt / BM + nseq slots are enough and no sum over the
-// sequences before is needed.  Some slots stay empty.
+// Which sequence a workgroup works on.  With `per` rows a query, sequence i's tiles of
+// BM rows have the slots from starts[i] * per / BM + i on: those of the next begin
+// behind its last one, whatever its length, so that nt * per / BM + nseq slots are
+// enough and no sum over the sequences before is needed.  Some slots stay empty.
 struct Tile {
     int q0, nq;      // first packed query of the sequence, queries
     int k0, nk;
-    int first;       // first query of the tile in its sequence
+    int64_t row0;    // first (query, head) row of the tile in its sequence
 };
 
 template <int BM>
-__device__ __forceinline__ bool find_tile(const PromptArgs &a, int slot, Tile &t)
+__device__ __forceinline__ bool find_rows(const PromptArgs &a, int slot, int per, Tile &t)
 {
     const int32_t *starts = a.starts;
     const int64_t nt = a.nt;
+    const auto first_slot = [&](int s) { return (int64_t)held(starts[s], nt) * per / BM + s; };
     const int i = __builtin_amdgcn_readfirstlane(
-        count_first((int)a.nseq, [&](int s) { return held(starts[s], nt) / BM + s <= slot; }) - 1);
+        count_first((int)a.nseq, [&](int s) { return first_slot(s) <= slot; }) - 1);
     if (i < 0) return false;
     t.q0 = held(a.starts[i], a.nt);
     t.nq = held(a.starts[i + 1], a.nt) - t.q0;
     t.k0 = held(a.k_starts[i], a.nk);
     t.nk = held(a.k_starts[i + 1], a.nk) - t.k0;
     if (t.nk < 0) t.nk = 0;
-    const int64_t first = (int64_t)(slot - (t.q0 / BM + i)) * BM;
-    if (first < 0 || first >= t.nq) return false;   // below 0: starts that decrease
-    t.first = (int)first;
-    return true;
+    t.row0 = (slot - first_slot(i)) * BM;
+    return t.row0 >= 0 && t.row0 < (int64_t)t.nq * per;   // below 0: starts that decrease
 }
 
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < INFINITY; }
@@ -59,8 +58,8 @@ __device__ __forceinline__ void poison_tile(f32x16 &o, const E *vp, int64_t step
                                                       int end, int h)
 {
     f32x16 hits = 0.0f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
+#pragma unroll 1
+    for (int r = 0; r < 16; ++r) {   // a loop: it hardly ever runs, and its registers would be the kernel's
         const int key = k0 + mfma_row(r, h);
         const bool bad = key < nk && c < d && !finite((float)vp[(int64_t)key * step + c]);
         hits = __builtin_amdgcn_mfma_f32_32x32x2f32(bad ? 1.0f : 0.0f, key < end ? 1.0f : 0.0f, hits, 0, 0, 0);
@@ -101,13 +100,14 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
     constexpr int V = VEC<T>, CH = D / V;        // elements and units of 16 bytes in a row
     const int head = blockIdx.x % a.hq;
     Tile t;
-    if (!find_tile<128>(a, slots - 1 - (int)(blockIdx.x / a.hq), t)) return;
+    if (!find_rows<128>(a, slots - 1 - (int)(blockIdx.x / a.hq), 1, t)) return;
+    const int first = (int)t.row0;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
     const int kvh = head / per, d = a.d;
     const E *kp = static_cast<const E *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
     const E *vp = static_cast<const E *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
 
-    const int mine = t.first + wave * 32 + n;    // this lane's query in its sequence
+    const int mine = first + wave * 32 + n;    // this lane's query in its sequence
     const int row = mine < t.nq ? mine : t.nq - 1;
     const E *qp = static_cast<const E *>(a.q.p) + (int64_t)(t.q0 + row) * a.q.token + (int64_t)head * a.q.head;
     float q[D / 2];
@@ -126,17 +126,17 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
         return e < 0 ? 0 : e > t.nk ? t.nk : e;
     };
     const int end = end_of(row);
-    const int last = t.first + 127 < t.nq ? t.first + 127 : t.nq - 1;
+    const int last = first + 127 < t.nq ? first + 127 : t.nq - 1;
     const int kend = end_of(last);
-    const int wave_last = t.first + wave * 32 + 31 < t.nq ? t.first + wave * 32 + 31 : t.nq - 1;
-    const int wave_end = end_of(wave_last), wave_full = end_of(t.first + wave * 32 < t.nq ? t.first + wave * 32 : t.nq - 1);
+    const int wave_last = first + wave * 32 + 31 < t.nq ? first + wave * 32 + 31 : t.nq - 1;
+    const int wave_end = end_of(wave_last), wave_full = end_of(first + wave * 32 < t.nq ? first + wave * 32 : t.nq - 1);
 
     f32x16 o[D / 32];
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    const int all_full = end_of(t.first);
+    const int all_full = end_of(first);
     for (int k0 = 0; k0 < kend; k0 += 32) {
         const bool masks = k0 + 32 > all_full;   // some query of the workgroup does not see some key
         int bad = 0;
@@ -219,6 +219,235 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
         }
 }
 
+// 16-bit operands on v_mfma_f32_32x32x16 (bf16 or f16).  Rows are (query, head of the
+// group) pairs of one key head, heads fastest, 32 a wave: all heads that share a key
+// head read one copy of it from LDS, and a tile of 32 W rows spans few queries, so
+// that little of its last steps is masked.
+//   S^T: lane (n, h) gives key n's and row n's channels 16 x + 8 h .. + 7.
+//   S^T's registers 8 y .. 8 y + 7 of lane (n, h), rounded, are row n's operand for the
+//   keys 16 y + {4 h + i, 8 + 4 h + i}, i < 4; V's, four keys of a channel at a time, come
+//   from ds_read_b64_tr_b16, which turns 4 keys by 16 channels in each 16 lanes.
+// LDS: 16-byte units of a row of K stand at unit ^ (row & 15) (rows of 128 bytes: ^ (row /
+// 2 & 7)), so that 16 lanes reading one unit of 16 rows meet in no bank; those of V at
+// unit ^ 4 (row & 3) (^ 4 (row / 2 & 1)), so that the four keys' 64 bytes of a
+// transposing read do not either.
+// The reference of a row's exponents follows its maximum only when that is 2^LAZY above
+// it: most steps then correct nothing.  P <= 2^LAZY, times 2^6 in f16, where it
+// then loses bits only below 2^-20 of the reference (and no more than 2^-31 of it).
+constexpr float LAZY = 8.0f;
+
+template <int T> struct Mfma16;
+template <> struct Mfma16<T_BF16> {
+    typedef bf16x8 type;
+    static constexpr uint32_t EXP = 0x7f80;
+    static constexpr float UP = 0.0f;
+    static __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(type, a), __builtin_bit_cast(type, b), c, 0, 0,
+                                                       0);
+    }
+};
+template <> struct Mfma16<T_F16> {
+    typedef f16x8 type;
+    static constexpr uint32_t EXP = 0x7c00;
+    static constexpr float UP = 6.0f;
+    static __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(type, a), __builtin_bit_cast(type, b), c, 0, 0, 0);
+    }
+};
+
+// Four keys of one channel: 16 lanes hand in the addresses of 4 keys' 16 channels.
+__device__ __forceinline__ u32x2 read_turned(const uint16_t *p)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
+}
+
+template <int D> __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
+template <int D> __device__ __forceinline__ int swz_v(int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
+
+template <int T, int D, int W, int KT>
+__global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs a, int slots, int per)
+{
+    typedef elem_t<T> E;
+    typedef Mfma16<T> M;
+    constexpr int NT = 64 * W, BM = 32 * W, CH = D / 8, N = KT * CH / NT;
+    __shared__ __align__(16) uint16_t lds_k[2][KT * D], lds_v[2][KT * D];
+    const int kvh = blockIdx.x % a.hkv;
+    Tile t;
+    if (!find_rows<BM>(a, slots - 1 - (int)(blockIdx.x / a.hkv), per, t)) return;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+    const int d = a.d;
+    const E *kp = static_cast<const E *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
+    const E *vp = static_cast<const E *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
+
+    const int64_t rows = (int64_t)t.nq * per;
+    const int64_t mine = t.row0 + wave * 32 + n;
+    const int64_t row = mine < rows ? mine : rows - 1;
+    const int query = (int)(row / per), head = kvh * per + (int)(row % per);
+    const E *qp = static_cast<const E *>(a.q.p) + (int64_t)(t.q0 + query) * a.q.token + (int64_t)head * a.q.head;
+    u32x4 q[D / 16];
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+        const int c = 16 * x + 8 * h;
+        q[x] = c < d ? load16<T>(qp + c) : u32x4{0, 0, 0, 0};
+    }
+
+    const int off = t.nk - t.nq;
+    const auto end_of = [&](int i) {
+        const int e = a.causal ? off + i + 1 : t.nk;
+        return e < 0 ? 0 : e > t.nk ? t.nk : e;
+    };
+    const auto query_of = [&](int64_t r) { return (int)((r < rows ? r : rows - 1) / per); };
+    const int end = end_of(query);
+    const int kend = end_of(query_of(t.row0 + BM - 1)), all_full = end_of(query_of(t.row0));
+    const int wave_end = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32 + 31)));
+    const int wave_full = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32)));
+
+    u32x4 ks[N], vs[N];
+    const auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = i * NT + threadIdx.x, r = u / CH, c = (u % CH) * 8;
+            ks[i] = vs[i] = u32x4{0, 0, 0, 0};
+            if (k0 + r < t.nk && c < d) {
+                ks[i] = load16<T>(kp + (int64_t)(k0 + r) * a.k.token + c);
+                vs[i] = load16<T>(vp + (int64_t)(k0 + r) * a.v.token + c);
+            }
+        }
+    };
+    // returns whether a value was not finite (looked for in steps with masks alone)
+    const auto store = [&](int buf, bool masks) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = i * NT + threadIdx.x, r = u / CH, c = u % CH;
+            *reinterpret_cast<u32x4 *>(&lds_k[buf][(r * CH + (c ^ swz_k<D>(r))) * 8]) = ks[i];
+            if (masks) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = vs[i][j], lo = (w & M::EXP) == M::EXP, hi = ((w >> 16) & M::EXP) == M::EXP;
+                    bad |= lo | hi;
+                    vs[i][j] = w & ~((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
+                }
+            }
+            *reinterpret_cast<u32x4 *>(&lds_v[buf][(r * CH + (c ^ swz_v<D>(r))) * 8]) = vs[i];
+        }
+        return (int)bad;
+    };
+    const auto masks_at = [&](int k0) { return k0 + KT > all_full; };
+
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
+    float ref = -INFINITY, l = 0.0f;
+    const int turned = ((lane >> 5) * 4 + ((lane & 15) >> 2)) * D;         // this lane's key in a transposing read
+    const int turned_c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);         // its unit within 32 channels
+    const int turned_x = swz_v<D>((lane & 15) >> 2);
+
+    int bad = 0;
+    if (kend > 0) {
+        load(0);
+        bad = store(0, masks_at(0));
+    }
+    if (masks_at(0)) bad = __syncthreads_or(bad);
+    else __syncthreads();
+    for (int k0 = 0, buf = 0; k0 < kend; k0 += KT, buf ^= 1) {
+        const bool more = k0 + KT < kend;
+        if (more) load(k0 + KT);
+        if (k0 < wave_end) {
+            f32x16 s[KT / 32];
+#pragma unroll
+            for (int y = 0; y < KT / 32; ++y) {
+                s[y] = 0.0f;
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const u32x4 kv = *reinterpret_cast<const u32x4 *>(
+                        &lds_k[buf][((y * 32 + n) * CH + ((2 * x + h) ^ swz_k<D>(n))) * 8]);
+                    s[y] = M::mul(kv, q[x], s[y]);
+                }
+            }
+            if (k0 + KT > wave_full) {
+#pragma unroll
+                for (int y = 0; y < KT / 32; ++y)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (k0 + y * 32 + mfma_row(r, h) >= end) s[y][r] = -INFINITY;
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int y = 0; y < KT / 32; ++y)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[y][r]);
+            top *= a.c;
+            if (__any(top > ref + LAZY)) {          // also the first time
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float to = fmaxf(ref, top);
+                const float fix = __builtin_amdgcn_exp2f(ref - (to == -INFINITY ? 0.0f : to));
+                ref = to;
+                l *= fix;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) o[x] *= fix;
+            }
+            const float base = ref == -INFINITY ? 0.0f : ref - M::UP;
+            u32x4 p[KT / 16];
+#pragma unroll
+            for (int y = 0; y < KT / 16; ++y) {
+                float f[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    f[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[y / 2][8 * (y % 2) + r], a.c, -base));
+                    l += f[r];
+                }
+                p[y] = pack16<T>(f);
+            }
+#pragma unroll
+            for (int y = 0; y < KT / 16; ++y)
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const uint16_t *at = &lds_v[buf][turned + 16 * y * D + (((4 * x + turned_c) ^ turned_x) * 8) + (lane & 1) * 4];
+                    const u32x2 v0 = read_turned(at), v1 = read_turned(at + 8 * D);
+                    o[x] = M::mul(u32x4{v0[0], v0[1], v1[0], v1[1]}, p[y], o[x]);
+                }
+            if (bad) {
+#pragma unroll
+                for (int y = 0; y < KT / 32; ++y) poison<D, E>(o, vp, a.v.token, k0 + 32 * y, t.nk, d, end, n, h);
+            }
+        }
+        bad = more ? store(buf ^ 1, masks_at(k0 + KT)) : 0;
+        if (masks_at(k0 + KT)) bad = __syncthreads_or(bad);
+        else __syncthreads();
+    }
+    l += __shfl_xor(l, 32);
+    if (mine >= rows) return;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    const int64_t at = (int64_t)(t.q0 + query) * a.y_token + (int64_t)head * a.y_head;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const int c = 32 * x + mfma_row(r, h);
+            const float f[4] = {o[x][r] * inv, o[x][r + 1] * inv, o[x][r + 2] * inv, o[x][r + 3] * inv};
+            if (c < d) store4(a.y, a.ytype, at + c, f);
+        }
+}
+
+template <int T>
+int launch_16(const PromptArgs &a, hipStream_t stream)
+{
+    const int per = a.hq / a.hkv;
+    constexpr int W = 4;
+    const int64_t slots = a.nt * per / (32 * W) + a.nseq;
+    const int64_t groups = slots * a.hkv;
+    if (slots >= (int64_t(1) << 31) || groups > launch_groups(64 * W)) return -1;
+    const dim3 grid((unsigned)groups), block(64 * W);
+    if (a.d <= 64) return launch_kernel(prompt_16<T, 64, W, 64>, grid, block, stream, a, (int)slots, per);
+    if (a.d <= 128) return launch_kernel(prompt_16<T, 128, W, 64>, grid, block, stream, a, (int)slots, per);
+    return launch_kernel(prompt_16<T, 256, W, 32>, grid, block, stream, a, (int)slots, per);
+}
+
 template <int T>
 int launch_f32(const PromptArgs &a, hipStream_t stream)
 {
@@ -237,8 +466,8 @@ int launch_f32(const PromptArgs &a, hipStream_t stream)
 int launch_attend_prompt(const PromptArgs &a, hipStream_t stream)
 {
     if (a.type == T_F32) return launch_f32<T_F32>(a, stream);
-    if (a.type == T_BF16) return launch_f32<T_BF16>(a, stream);
-    return launch_f32<T_F16>(a, stream);
+    if (a.type == T_BF16) return launch_16<T_BF16>(a, stream);
+    return launch_16<T_F16>(a, stream);
 }
 
 }  // namespace qig

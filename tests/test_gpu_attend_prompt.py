@@ -42,6 +42,8 @@ def want(q, k, v, lens, klens, causal, scale, dtype, ytype):
         # 16-bit operands: p is rounded to their type
         step = 0.0 if dtype == F32 else ref.EPS[dtype]
         al.append(ref.allowance(y, mag, amax, d, nk, step, ytype))
+        if dtype == F16 and nk:   # below f16's normal range p keeps 2^-31 of its reference, which is at most its maximum
+            al[-1] = al[-1] + nk * 2.0 ** -31 * v[ka:ka + nk].double().abs().max().item()
         a, ka = a + n, ka + nk
     return torch.cat(ys), torch.cat(al)
 
