@@ -17,7 +17,8 @@
 //    operand as they are.
 //  * A row of 16 lanes loads the 8 tokens' scales that its lanes need, a word or a
 //    few each; each use takes its word from the lane that has it (a row broadcast
-//    within the multiply).
+//    within the multiply).  The keys' m, bf16 as they stand, meet the queries' sums in an
+//    MFMA of their own, the sums in three bf16 parts.
 // Rows: (query, head of the group) pairs of one key head, 16 at a time.
 //
 // Range in f16: a query's row is scaled by a power of two so that its largest
@@ -71,9 +72,47 @@ __device__ __forceinline__ f32x4 mfma_f16(f16x8 a, f16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ uint32_t pack_f16(_Float16 a, _Float16 b)
+__device__ __forceinline__ f32x4 mfma_bf16_16(u32x4 a, u32x4 b, f32x4 c)
 {
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// The compiler would unpack a block's codes all at once, for 100 registers that three
+// waves a SIMD do not have.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// Two values rounded to f16, and what the rounding left.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+}
+__device__ __forceinline__ uint32_t pack_rest(uint32_t hi, float a, float b)
+{
+    const f16x2 v = __builtin_bit_cast(f16x2, hi);
+    return pack_f16(a - (float)v[0], b - (float)v[1]);
+}
+
+// m + sum over x of t[x] * (lane 2 x + PAR's value of each row of 16 lanes).  The compiler
+// makes two instructions of each of these; the wait is that of a row broadcast
+// behind a write of its source (and covers t's last powers).
+template <int PAR>
+__device__ __forceinline__ float row_dot(float m, float v, const float (&t)[8])
+{
+#define QIG_ROW_FMA(T, L) "v_fmac_f32_dpp %0, %1, " T " row_newbcast:" L " row_mask:0xf bank_mask:0xf\n"
+    if constexpr (PAR == 0) {
+        asm("s_nop 1\n" QIG_ROW_FMA("%2", "0") QIG_ROW_FMA("%3", "2") QIG_ROW_FMA("%4", "4") QIG_ROW_FMA("%5", "6")
+                QIG_ROW_FMA("%6", "8") QIG_ROW_FMA("%7", "10") QIG_ROW_FMA("%8", "12") QIG_ROW_FMA("%9", "14")
+            : "+v"(m) : "v"(v), "v"(t[0]), "v"(t[1]), "v"(t[2]), "v"(t[3]), "v"(t[4]), "v"(t[5]), "v"(t[6]), "v"(t[7]));
+    } else {
+        asm("s_nop 1\n" QIG_ROW_FMA("%2", "1") QIG_ROW_FMA("%3", "3") QIG_ROW_FMA("%4", "5") QIG_ROW_FMA("%5", "7")
+                QIG_ROW_FMA("%6", "9") QIG_ROW_FMA("%7", "11") QIG_ROW_FMA("%8", "13") QIG_ROW_FMA("%9", "15")
+            : "+v"(m) : "v"(v), "v"(t[0]), "v"(t[1]), "v"(t[2]), "v"(t[3]), "v"(t[4]), "v"(t[5]), "v"(t[6]), "v"(t[7]));
+    }
+#undef QIG_ROW_FMA
+    return m;
 }
 
 __device__ __forceinline__ float ldexp_f(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
@@ -92,6 +131,7 @@ struct Job {
     Kv4Attend a;
     int per;            // heads of queries on one key head
     int split;          // 0: every row in one piece
+    int room;           // tokens that a row of the table has pages for
     int groups;         // workgroups
     float *slots;       // [groups][2][SLOT]
     Header *headers;    // [groups]
@@ -100,10 +140,10 @@ struct Job {
 // A sequence's place in the list of all blocks.
 struct Seq {
     int q0, n;          // packed queries
-    int64_t length;     // tokens, as given (not negative)
-    int64_t keys;       // of them, those that the table has room for
-    int64_t blocks;     // list entries of one (head, tile): at least one, so that rows without keys get their zeros
-    int tiles;
+    int length;         // tokens, as given (not negative)
+    int keys;           // of them, those that the table has room for
+    uint32_t blocks;    // list entries of one (head, tile): at least one, so that rows without keys get their zeros
+    uint32_t tiles;
 };
 
 __device__ __forceinline__ Seq get_seq(const Job &j, int s)
@@ -119,105 +159,128 @@ __device__ __forceinline__ Seq get_seq(const Job &j, int s)
     }
     const int len = j.c.lengths[s];
     q.length = len < 0 ? 0 : len;
-    const int64_t room = j.c.width * j.c.page;
-    q.keys = q.length < room ? q.length : room;
-    q.blocks = !j.split || q.keys == 0 ? 1 : (q.keys + 31) / 32;
-    q.tiles = (int)(((int64_t)q.n * j.per + ROWS - 1) / ROWS);
+    q.keys = q.length < j.room ? q.length : j.room;
+    q.blocks = !j.split || q.keys == 0 ? 1 : (uint32_t)(q.keys - 1) / 32 + 1;
+    q.tiles = (uint32_t)q.n * (uint32_t)j.per / ROWS + ((uint32_t)q.n * (uint32_t)j.per % ROWS != 0);
     return q;
 }
 
-__device__ __forceinline__ int64_t units(const Job &j, const Seq &q) { return (int64_t)j.c.heads * q.tiles * q.blocks; }
+__device__ __forceinline__ uint32_t units(const Job &j, const Seq &q) { return (uint32_t)j.c.heads * q.tiles * q.blocks; }
 
-// Sum of a 64-bit value over the lanes before this one, and over all 256 threads.
-__device__ __forceinline__ int64_t scan(int64_t v, int64_t *tmp, int64_t &total)
+// Sum of a value over the lanes before this one, and over all 256 threads.
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t *tmp, uint32_t &total)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t s = v;
+    uint32_t s = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int64_t up = __shfl_up(s, o);
+        const uint32_t up = __shfl_up(s, o);
         if (lane >= o) s += up;
     }
     __syncthreads();
     if (lane == 63) tmp[wave] = s;
     __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < wave; ++w) before += tmp[w];
-    total = tmp[0] + tmp[1] + tmp[2] + tmp[3];
-    return before + s - v;
+    const uint32_t t0 = tmp[0], t1 = tmp[1], t2 = tmp[2], t3 = tmp[3];
+    total = t0 + t1 + t2 + t3;
+    return s - v + (wave > 0 ? t0 : 0) + (wave > 1 ? t1 : 0) + (wave > 2 ? t2 : 0);
 }
 
-template <int D> struct Loaded {
-    static constexpr int G = D / 32, Q = G / 2;   // groups of channels, and 16-byte pieces a lane has of the codes
-    u32x4 k[Q], v[Q];
-    uint32_t ks[Q], vs[Q];
+// A lane's operands from a block.  G: groups of channels; Q: the 16-byte pieces that a
+// lane has of the codes, and its words of the scales.
+template <int D> struct Keys {
+    static constexpr int G = D / 32, Q = G / 2;
+    u32x4 c[Q];
+    uint32_t s[Q], m[2][G];                        // m: the scales of keys l and 16 + l
+};
+template <int D> struct Values {
+    static constexpr int Q = D / 64;
+    u32x4 c[Q];
+    uint32_t s[Q];
 };
 
-template <int D>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[D / 64])
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w)
 {
-    if constexpr (D == 64) {
+    if constexpr (N == 1) {
         w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (D == 128) {
+    } else if constexpr (N == 2) {
         const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
         w[0] = v[0], w[1] = v[1];
     } else {
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
-        w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + 4 * i);
+            w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+        }
     }
 }
 
 template <int D>
-__device__ __forceinline__ void load_block(const uint8_t *block, int lane, Loaded<D> &b)
+__device__ __forceinline__ void load_keys(const uint8_t *block, int lane, Keys<D> &k)
 {
-    constexpr int Q = Loaded<D>::Q;
+    constexpr int Q = Keys<D>::Q, G = Keys<D>::G;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) b.k[i] = *reinterpret_cast<const u32x4 *>(block + i * 1024 + lane * 16);
-    load_words<D>(block + 32 * D + lane * (4 * Q), b.ks);
+    for (int i = 0; i < Q; ++i) k.c[i] = *reinterpret_cast<const u32x4 *>(block + i * 1024 + lane * 16);
+    load_words<Q>(block + 32 * D + lane * (4 * Q), k.s);
+    const int l = lane & 15;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) b.v[i] = *reinterpret_cast<const u32x4 *>(block + 16 * D + i * 1024 + lane * 16);
-    load_words<D>(block + 36 * D + lane * (4 * Q), b.vs);
+    for (int u = 0; u < 2; ++u) load_words<G>(block + 32 * D + ((l >> 2) * 8 + u * 4 + (l & 3)) * (4 * G), k.m[u]);
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const uint8_t *block, int lane, Values<D> &v)
+{
+    constexpr int Q = Values<D>::Q;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) v.c[i] = *reinterpret_cast<const u32x4 *>(block + 16 * D + i * 1024 + lane * 16);
+    load_words<Q>(block + 36 * D + lane * (4 * Q), v.s);
 }
 
 template <int T, int D, int QP, int PP>
-__global__ __launch_bounds__(256) void kv4_kernel(Job j)
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 64 ? 4 : QP + PP == 4 ? 2 : 3) void kv4_kernel(Job j)
 {
     typedef elem_t<T> E;
     constexpr int G = D / 32, Q = G / 2, TILES = D / 16;
     __shared__ float joined[WAVES][ROWS * D];
     __shared__ float stats[WAVES][2][ROWS];
-    __shared__ int64_t tmp[4];
-    __shared__ int64_t found[2];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, h = lane >> 4;
+    __shared__ uint32_t tmp[4], found[2];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, h = lane >> 4;
     const int nseq = (int)j.c.nseq;
 
     // the list's length, and where this workgroup's run of it begins
-    int64_t mine = 0, total, size;
+    uint32_t mine = 0, total, before;
     for (int s = threadIdx.x; s < nseq; s += 256) mine += units(j, get_seq(j, s));
-    scan(mine, tmp, total);
-    size = (total + j.groups - 1) / j.groups;
+    before = scan(mine, tmp, total);
+    uint32_t size = (total + j.groups - 1) / j.groups;
     if (j.split && size < WAVES) size = WAVES;
     if (size < 1) size = 1;
-    int64_t at = (int64_t)blockIdx.x * size;
-    const int64_t end = at + size < total ? at + size : total;
+    uint32_t at = blockIdx.x * size;
+    const uint32_t end = at + size < total ? at + size : total;
     if (threadIdx.x == 0 && j.split) j.headers[blockIdx.x].pieces = 0;
     if (at >= end) return;
-    int64_t ahead = 0;
-    for (int s0 = 0; s0 < nseq; s0 += 256) {
-        const int s = s0 + threadIdx.x;
-        const int64_t u = s < nseq ? units(j, get_seq(j, s)) : 0;
-        int64_t sum;
-        const int64_t before = ahead + scan(u, tmp, sum);
-        if (at >= before && at < before + u) {
-            found[0] = s;
+    if (nseq <= 256) {
+        if (at >= before && at < before + mine) {
+            found[0] = threadIdx.x;
             found[1] = before;
         }
-        ahead += sum;
-        if (ahead > at) break;
+    } else {
+        uint32_t ahead = 0;
+        for (int s0 = 0; s0 < nseq; s0 += 256) {
+            const int s = s0 + threadIdx.x;
+            const uint32_t u = s < nseq ? units(j, get_seq(j, s)) : 0;
+            uint32_t sum;
+            before = ahead + scan(u, tmp, sum);
+            if (at >= before && at < before + u) {
+                found[0] = s;
+                found[1] = before;
+            }
+            ahead += sum;
+            if (ahead > at) break;
+        }
     }
     __syncthreads();
-    int s = __builtin_amdgcn_readfirstlane((int)found[0]);
-    int64_t seq_at = found[1];
+    int s = __builtin_amdgcn_readfirstlane(found[0]);
+    uint32_t seq_at = __builtin_amdgcn_readfirstlane(found[1]);
     Seq q = get_seq(j, s);
 
     while (at < end) {
@@ -225,25 +288,51 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
             seq_at += units(j, q);
             q = get_seq(j, ++s);
         }
-        const int64_t part = (at - seq_at) / q.blocks;
-        const int64_t first = (at - seq_at) % q.blocks;             // list entries of this row before the piece
-        const int64_t left = q.blocks - first;
-        const int64_t entries = left < end - at ? left : end - at;
-        const int head = (int)(part / q.tiles), tile = (int)(part % q.tiles);
+        const uint32_t part = (at - seq_at) / q.blocks;
+        const uint32_t first = (at - seq_at) - part * q.blocks;     // list entries of this row before the piece
+        const uint32_t left = q.blocks - first;
+        const uint32_t entries = left < end - at ? left : end - at;
+        const int head = (int)(part / q.tiles), tile = (int)(part - head * q.tiles);
         // the blocks of tokens: all of them where rows are not split
-        const int64_t all = (q.keys + 31) / 32;
-        const int64_t b0 = j.split ? first : 0, b1 = j.split ? (first + entries < all ? first + entries : all) : all;
+        const int all = q.keys == 0 ? 0 : (q.keys - 1) / 32 + 1;
+        const int b0 = j.split ? (int)first : 0;
+        const int b1 = j.split && (int)(first + entries) < all ? (int)(first + entries) : all;
+
+        // the pages of this piece's first 64 columns, one a lane
+        const int32_t *table = j.c.tables + (int64_t)s * j.c.ld;
+        const int page_blocks = j.c.page / 32, width = (int)j.c.width;
+        int col = (b0 + wave) / page_blocks, rem = (b0 + wave) - col * page_blocks;
+        const int step_col = WAVES / page_blocks, step_rem = WAVES - step_col * page_blocks;
+        int col0 = col;
+        const auto ids_from = [&](int c) { return c + lane < width ? table[c + lane] : -1; };
+        int ids = ids_from(col0);
+        const auto next_block = [&]() -> const uint8_t * {
+            if (col - col0 >= 64) {
+                col0 = col;
+                ids = ids_from(col0);
+            }
+            const int page = __builtin_amdgcn_readlane(ids, col - col0);
+            const uint8_t *p = j.c.pages + page * j.c.page_bytes + ((int64_t)head * page_blocks + rem) * (40 * D);
+            col += step_col;
+            rem += step_rem;
+            if (rem >= page_blocks) {
+                rem -= page_blocks;
+                ++col;
+            }
+            return page < 0 || page >= j.c.npages ? nullptr : p;
+        };
 
         // this lane's row: its query, scaled into f16, and the sums of its groups
-        const int64_t R = (int64_t)tile * ROWS + l;
-        const bool real = R < (int64_t)q.n * j.per;
-        const int64_t Rq = real ? R : (int64_t)q.n * j.per - 1;
-        const int qi = (int)(Rq / j.per), qh = head * j.per + (int)(Rq % j.per);
+        const int rows = q.n * j.per;
+        const int R = tile * ROWS + l;
+        const int Rq = R < rows ? R : rows - 1;
+        const int qi = Rq / j.per, qh = head * j.per + (Rq - qi * j.per);
         const E *qp = static_cast<const E *>(j.a.q.p) + (int64_t)(q.q0 + qi) * j.a.q.token + (int64_t)qh * j.a.q.head;
         f16x8 qv[QP][G];
-        float qs[G], F;
+        u32x4 qm = {0, 0, 0, 0};                    // the groups' sums in bf16: the first, second, third part in lanes 0.., 16.., 32..
+        float F;
         {
-            float f[G][8], top = 0.0f;
+            float f[G][8], qs[G], top = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -253,6 +342,9 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
 #pragma unroll
                     for (int i = 0; i < VEC<T>; ++i) f[g][x * VEC<T> + i] = t[i];
                 }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
                 qs[g] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -267,25 +359,27 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
             const int e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 15 : 0;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                _Float16 hi[8], lo[8];
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float v = ldexp_f(f[g][i], ((i >> 1) & 1 ? -4 : 0) - e);
-                    hi[i] = (_Float16)v;
-                    lo[i] = (_Float16)(v - (float)hi[i]);
+                for (int i = 0; i < 4; ++i) {
+                    const float v0 = ldexp_f(f[g][2 * i], (i & 1 ? -4 : 0) - e), v1 = ldexp_f(f[g][2 * i + 1], (i & 1 ? -4 : 0) - e);
+                    hi[i] = pack_f16(v0, v1);
+                    lo[i] = pack_rest(hi[i], v0, v1);
                 }
-                qv[0][g] = f16x8{hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]};
-                if constexpr (QP > 1) qv[1][g] = f16x8{lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]};
-                qs[g] = ldexp_f(qs[g], -24 - e);
+                qv[0][g] = operand(hi[0], hi[1], hi[2], hi[3]);
+                if constexpr (QP > 1) qv[1][g] = operand(lo[0], lo[1], lo[2], lo[3]);
+                const float v = ldexp_f(qs[g], -24 - e);
+                const __bf16 p0 = (__bf16)v, p1 = (__bf16)(v - (float)p0), p2 = (__bf16)(v - (float)p0 - (float)p1);
+                const __bf16 mine = h == 0 ? p0 : h == 1 ? p1 : p2;
+                if (h < 3) qm[g / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, mine) << (16 * (g % 2));
             }
             F = ldexp_f(j.a.c, 24 + e);
         }
-        // the tokens that this row sees: the first `limit` ones
-        int64_t lim = q.length - q.n + qi + 1;
-        const int64_t limit = lim < 0 ? 0 : lim < q.keys ? lim : q.keys;
-        // from this token on some row of the tile sees less than all
-        const int q_first = (int)((int64_t)tile * ROWS / j.per);
-        int64_t full = q.length - q.n + q_first + 1;
+        // the tokens that this row sees: the first `limit` ones; from token `full` on some
+        // row of the tile sees less than all
+        const int lim = q.length - q.n + qi + 1;
+        const int limit = lim < 0 ? 0 : lim < q.keys ? lim : q.keys;
+        int full = q.length - q.n + tile * ROWS / j.per + 1;
         full = full < q.keys ? full : q.keys;
 
         f32x4 o[TILES];
@@ -298,65 +392,50 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
 #pragma unroll
         for (int x = 0; x < Q; ++x) E[x] = -200;
 
-        const int32_t *table = j.c.tables + (int64_t)s * j.c.ld;
-        const int page_blocks = j.c.page / 32;
-        const auto block_at = [&](int64_t b) -> const uint8_t * {
-            const int64_t col = b / page_blocks;
-            const int page = __builtin_amdgcn_readfirstlane(table[col]);
-            if (page < 0 || page >= j.c.npages) return nullptr;
-            return j.c.pages + page * j.c.page_bytes +
-                   ((int64_t)head * page_blocks + (b - col * page_blocks)) * (40 * D);
-        };
-
-        Loaded<D> now, next;
-        int64_t b = b0 + wave;
-        const uint8_t *here = b < b1 ? block_at(b) : nullptr;
-        if (here) load_block<D>(here, lane, now);
+        Keys<D> k;
+        Values<D> v;
+        int b = b0 + wave;
+        const uint8_t *here = b < b1 ? next_block() : nullptr;
+        if (here) {
+            load_keys<D>(here, lane, k);
+            load_values<D>(here, lane, v);
+        }
         for (; b < b1; b += WAVES) {
-            const uint8_t *then = b + WAVES < b1 ? block_at(b + WAVES) : nullptr;
-            if (then) load_block<D>(then, lane, next);
+            const uint8_t *then = b + WAVES < b1 ? next_block() : nullptr;
+            float t[8];
             if (here) {
-                const bool tail = b * 32 + 32 > full;
-                float ks[Q], km[Q], vs[Q], vm[Q];
-#pragma unroll
-                for (int x = 0; x < Q; ++x) {
-                    uint32_t kw = now.ks[x], vw = now.vs[x];
-                    if (tail) {                     // words behind the sequence's end hold anything
-                        const int slot = (l * Q + x) / G;
-                        if (b * 32 + (slot >> 2) * 16 + h * 4 + (slot & 3) >= q.keys) kw = vw = 0;
-                    }
-                    ks[x] = __builtin_bit_cast(float, kw << 16);
-                    km[x] = __builtin_bit_cast(float, kw & 0xffff0000u);
-                    vs[x] = __builtin_bit_cast(float, vw << 16);
-                    vm[x] = __builtin_bit_cast(float, vw & 0xffff0000u);
-                }
-                float t[8];
                 each<2>([&](auto uc) {
                     constexpr int u = uc.value;
-                    f32x4 acc = 0.0f;
+                    u32x4 m4 = {0, 0, 0, 0};
+#pragma unroll
+                    for (int g = 0; g < G; g += 2) m4[g / 2] = __builtin_amdgcn_perm(k.m[u][g + 1], k.m[u][g], 0x07060302);
+                    f32x4 acc = mfma_bf16_16(m4, qm, f32x4(0.0f));
                     each<G>([&](auto gc) {
                         constexpr int g = gc.value, w = u * G + g;
-                        const uint32_t c0 = now.k[w / 4][w % 4], c1 = c0 >> 8;
+                        const uint32_t c0 = k.c[w / 4][w % 4], c1 = c0 >> 8;
                         const f16x8 kv = operand(c0 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x000f000fu, c1 & 0x00f000f0u);
                         f32x4 dot = 0.0f;
                         dot = mfma_f16(kv, qv[0][g], dot);
                         if constexpr (QP > 1) dot = mfma_f16(kv, qv[1][g], dot);
+                        const float ks = __builtin_bit_cast(float, k.s[g % Q] << 16);
                         each<4>([&](auto rc) {
                             constexpr int r = rc.value, from = (u * 4 + r) * 2 + g / Q;
-                            acc[r] = __builtin_fmaf(row_bcast<from>(ks[g % Q]), dot[r], acc[r]);
-                            acc[r] = __builtin_fmaf(row_bcast<from>(km[g % Q]), qs[g], acc[r]);
+                            acc[r] += row_bcast<from>(ks) * dot[r];
                         });
                     });
 #pragma unroll
                     for (int r = 0; r < 4; ++r) t[u * 4 + r] = acc[r] * F;
+                    keep_order();
                 });
-                bool seen[8];
+            }
+            // the keys' registers are free: the next block's come while this one's values are used
+            if (then) load_keys<D>(then, lane, k);
+            if (here) {
+                const bool tail = b * 32 > full - 32;
                 if (tail) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        seen[x] = b * 32 + (x >> 2) * 16 + h * 4 + (x & 3) < limit;
-                        if (!seen[x]) t[x] = -INFINITY;
-                    }
+                    for (int x = 0; x < 8; ++x)
+                        if (b * 32 + (x >> 2) * 16 + h * 4 + (x & 3) >= limit) t[x] = -INFINITY;
                 }
                 float top = t[0];
 #pragma unroll
@@ -379,10 +458,40 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
                     t[x] = __builtin_amdgcn_exp2f(t[x] - base);
                     sum += t[x];
                 }
+                if (tail) {
+                    // Words behind the sequence's end hold anything, and a token may stand for NaN that
+                    // some rows do not see: such words count as 0, and the groups of the rows that do
+                    // see one become NaN.
+                    float bad[Q];
+                    bool any = false;
+#pragma unroll
+                    for (int x = 0; x < Q; ++x) {
+                        const int slot = (l * Q + x) / G;
+                        const uint32_t w = b * 32 + (slot >> 2) * 16 + h * 4 + (slot & 3) < q.keys ? v.s[x] : 0;
+                        const bool nan = (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+                        bad[x] = nan ? 1.0f : 0.0f;
+                        v.s[x] = nan ? 0 : w;
+                        any |= nan;
+                    }
+                    if (__any(any))
+                        each<G>([&](auto gc) {
+                            constexpr int g = gc.value;
+                            each<8>([&](auto xc) {
+                                constexpr int x = xc.value;
+                                const bool hit = row_bcast<x * 2 + g / Q>(bad[g % Q]) != 0.0f;
+                                if (hit && b * 32 + (x >> 2) * 16 + h * 4 + (x & 3) < limit) mm[g] = NAN;
+                            });
+                        });
+                }
+                float vs[Q], vm[Q];
                 // the references of the values' scales
                 bool above = false;
 #pragma unroll
-                for (int x = 0; x < Q; ++x) above |= vs[x] != 0.0f && __builtin_amdgcn_frexp_expf(vs[x]) > E[x];
+                for (int x = 0; x < Q; ++x) {
+                    vs[x] = __builtin_bit_cast(float, v.s[x] << 16);
+                    vm[x] = __builtin_bit_cast(float, v.s[x] & 0xffff0000u);
+                    above |= vs[x] != 0.0f && __builtin_amdgcn_frexp_expf(vs[x]) > E[x];
+                }
                 if (__any(above)) {
 #pragma unroll
                     for (int x = 0; x < Q; ++x) {
@@ -413,37 +522,30 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
                 for (int x = 0; x < Q; ++x) vn[x] = ldexp_f(vs[x], 6 - E[x]);
                 each<G>([&](auto gc) {
                     constexpr int g = gc.value;
-                    _Float16 hi[8], lo[8];
-                    each<8>([&](auto xc) {
-                        constexpr int x = xc.value, from = x * 2 + g / Q;
-                        float w = t[x] * row_bcast<from>(vn[g % Q]);
-                        float m = t[x] * row_bcast<from>(vm[g % Q]);
-                        if (tail && !seen[x]) w = m = 0.0f;   // a token that this row may not see can be anything
-                        mm[g] += m;
-                        hi[x] = (_Float16)w;
-                        if constexpr (PP > 1) lo[x] = (_Float16)(w - (float)hi[x]);
-                    });
-                    const f16x8 p0 = operand(pack_f16(hi[0], hi[1]), pack_f16(hi[2], hi[3]), pack_f16(hi[4], hi[5]),
-                                             pack_f16(hi[6], hi[7]));
-                    f16x8 p1;
+                    mm[g] = row_dot<g / Q>(mm[g], vm[g % Q], t);
+                    float w[8];
+                    each<8>([&](auto xc) { w[xc.value] = t[xc.value] * row_bcast<xc.value * 2 + g / Q>(vn[g % Q]); });
+                    const uint32_t p0 = pack_f16(w[0], w[1]), p1 = pack_f16(w[2], w[3]), p2 = pack_f16(w[4], w[5]), p3 = pack_f16(w[6], w[7]);
+                    const f16x8 hi = operand(p0, p1, p2, p3);
+                    f16x8 lo;
                     if constexpr (PP > 1)
-                        p1 = operand(pack_f16(lo[0], lo[1]), pack_f16(lo[2], lo[3]), pack_f16(lo[4], lo[5]),
-                                     pack_f16(lo[6], lo[7]));
+                        lo = operand(pack_rest(p0, w[0], w[1]), pack_rest(p1, w[2], w[3]), pack_rest(p2, w[4], w[5]), pack_rest(p3, w[6], w[7]));
                     each<2>([&](auto yc) {
                         constexpr int n = 2 * g + yc.value, bit = n % 4;
                         uint32_t c[4];
                         each<4>([&](auto pc) {
-                            constexpr int w = pc.value * (D / 64) + n / 4;
-                            const uint32_t word = now.v[w / 4][w % 4];
+                            constexpr int i = pc.value * (D / 64) + n / 4;
+                            const uint32_t word = v.c[i / 4][i % 4];
                             c[pc.value] = (bit & 2 ? word >> 8 : word) & (bit & 1 ? 0x00f000f0u : 0x000f000fu);
                         });
                         const f16x8 vv = operand(c[0], c[1], c[2], c[3]);
-                        o[n] = mfma_f16(vv, p0, o[n]);
-                        if constexpr (PP > 1) o[n] = mfma_f16(vv, p1, o[n]);
+                        o[n] = mfma_f16(vv, hi, o[n]);
+                        if constexpr (PP > 1) o[n] = mfma_f16(vv, lo, o[n]);
                     });
+                    keep_order();
                 });
             }
-            now = next;
+            if (then) load_values<D>(then, lane, v);
             here = then;
         }
 
@@ -481,9 +583,9 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
         float *slot = j.slots + (int64_t)(blockIdx.x * 2 + (first == 0 ? 1 : 0)) * SLOT<D>;
         for (int x = threadIdx.x * 4; x < ROWS * D; x += 1024) {
             const int row = x / D;
-            f32x4 v = *reinterpret_cast<const f32x4 *>(&joined[0][x]);
+            f32x4 v4 = *reinterpret_cast<const f32x4 *>(&joined[0][x]);
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const f32x4 *>(&joined[w][x]);
+            for (int w = 1; w < WAVES; ++w) v4 += *reinterpret_cast<const f32x4 *>(&joined[w][x]);
             float M = stats[0][0][row], lsum = 0.0f;
 #pragma unroll
             for (int w = 1; w < WAVES; ++w) M = fmaxf(M, stats[w][0][row]);
@@ -491,15 +593,16 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
             for (int w = 0; w < WAVES; ++w)
                 lsum += stats[w][1][row] * __builtin_amdgcn_exp2f(stats[w][0][row] - base_of(M));
             if (whole) {
-                const int64_t Ry = (int64_t)tile * ROWS + row;
-                if (Ry < (int64_t)q.n * j.per) {
+                const int Ry = tile * ROWS + row;
+                if (Ry < rows) {
                     const float inv = lsum != 0.0f ? 1.0f / lsum : 0.0f;
-                    const float f[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-                    store4(j.a.y, j.a.ytype, (int64_t)(q.q0 + (int)(Ry / j.per)) * j.a.y_token +
-                                                 (int64_t)(head * j.per + (int)(Ry % j.per)) * j.a.y_head + x % D, f);
+                    const float f[4] = {v4[0] * inv, v4[1] * inv, v4[2] * inv, v4[3] * inv};
+                    const int i = Ry / j.per;
+                    store4(j.a.y, j.a.ytype, (int64_t)(q.q0 + i) * j.a.y_token +
+                                                 (int64_t)(head * j.per + (Ry - i * j.per)) * j.a.y_head + x % D, f);
                 }
             } else {
-                *reinterpret_cast<f32x4 *>(slot + 2 * ROWS + x) = v;
+                *reinterpret_cast<f32x4 *>(slot + 2 * ROWS + x) = v4;
                 if (x % D == 0) {
                     slot[row] = M;
                     slot[ROWS + row] = lsum;
@@ -507,7 +610,7 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
             }
         }
         if (!whole && first == 0 && threadIdx.x == 0) {
-            const int64_t last = (at + q.blocks - 1) / size;         // the workgroup with the row's last piece
+            const uint32_t last = (at + q.blocks - 1) / size;        // the workgroup with the row's last piece
             j.headers[blockIdx.x] = {s, head, tile, (int)(last - blockIdx.x) + 1};
         }
         at += entries;
@@ -515,33 +618,54 @@ __global__ __launch_bounds__(256) void kv4_kernel(Job j)
 }
 
 // The rows of more than one piece: the first is workgroup g's last one (slot 1), the
-// others are the first ones of the next workgroups (slot 0).
+// others are the first ones of the next workgroups (slot 0).  Four workgroups a
+// header, four rows each: a wave sums a row's pieces, its lanes reading 64 pieces' m
+// and l at once and then D channels of one piece after the other.
 template <int D>
 __global__ __launch_bounds__(256) void kv4_join(Job j)
 {
-    const int g = blockIdx.x;
+    typedef float vec __attribute__((ext_vector_type(D / 64)));
+    const int g = blockIdx.x >> 2, row = (blockIdx.x & 3) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     const Header hd = j.headers[g];
     if (hd.pieces == 0) return;
+    const float *first = j.slots + (int64_t)(g * 2 + 1) * SLOT<D>, *rest = j.slots + (int64_t)(g * 2 + 2) * SLOT<D>;
+    const auto slot_of = [&](int p) { return p == 0 ? first : rest + (int64_t)(p - 1) * (2 * SLOT<D>); };
     const Seq q = get_seq(j, hd.seq);
-    const auto slot_of = [&](int p) { return j.slots + (int64_t)((g + p) * 2 + (p == 0 ? 1 : 0)) * SLOT<D>; };
-    for (int x = threadIdx.x * 4; x < ROWS * D; x += 1024) {
-        const int row = x / D;
-        float M = -INFINITY, lsum = 0.0f;
-        for (int p = 0; p < hd.pieces; ++p) M = fmaxf(M, slot_of(p)[row]);
-        f32x4 v = 0.0f;
-        for (int p = 0; p < hd.pieces; ++p) {
-            const float *slot = slot_of(p);
-            const float fix = __builtin_amdgcn_exp2f(slot[row] - base_of(M));
+    const int R = hd.tile * ROWS + row;
+    if (R >= q.n * j.per) return;
+    float M = -INFINITY, lsum = 0.0f;
+    for (int p = lane; p < hd.pieces; p += 64) M = fmaxf(M, slot_of(p)[row]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+    const float base = base_of(M);
+    vec v = 0.0f;
+    for (int p0 = 0; p0 < hd.pieces; p0 += 64) {
+        float fix = 0.0f;
+        if (p0 + lane < hd.pieces) {
+            const float *slot = slot_of(p0 + lane);
+            fix = __builtin_amdgcn_exp2f(slot[row] - base);
             lsum += slot[ROWS + row] * fix;
-            v += *reinterpret_cast<const f32x4 *>(slot + 2 * ROWS + x) * fix;
         }
-        const int64_t R = (int64_t)hd.tile * ROWS + row;
-        if (R >= (int64_t)q.n * j.per) continue;
-        const float inv = lsum != 0.0f ? 1.0f / lsum : 0.0f;
-        const float f[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-        store4(j.a.y, j.a.ytype, (int64_t)(q.q0 + (int)(R / j.per)) * j.a.y_token +
-                                     (int64_t)(hd.head * j.per + (int)(R % j.per)) * j.a.y_head + x % D, f);
+        const int n = hd.pieces - p0 < 64 ? hd.pieces - p0 : 64;
+        int p = 0;
+        for (; p + 8 <= n; p += 8) {
+            vec w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = *reinterpret_cast<const vec *>(slot_of(p0 + p + i) + 2 * ROWS + row * D + lane * (D / 64));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += w[i] * __shfl(fix, p + i);
+        }
+        for (; p < n; ++p)
+            v += *reinterpret_cast<const vec *>(slot_of(p0 + p) + 2 * ROWS + row * D + lane * (D / 64)) * __shfl(fix, p);
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) lsum += __shfl_xor(lsum, o);
+    const float inv = lsum != 0.0f ? 1.0f / lsum : 0.0f;
+    const int i = R / j.per;
+    const int64_t at = (int64_t)(q.q0 + i) * j.a.y_token + (int64_t)(hd.head * j.per + (R - i * j.per)) * j.a.y_head;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) store1(j.a.y, j.a.ytype, at + lane * (D / 64) + c, v[c] * inv);
 }
 
 template <int T, int D, int QP, int PP>
@@ -549,14 +673,18 @@ int launch_typed(Job j, hipStream_t stream)
 {
     // rows of 16 over all sequences, and their blocks, are at most
     const int64_t rows = j.c.heads * ((j.a.nt * j.per) / ROWS + j.c.nseq);
-    const int64_t blocks = (j.c.width * j.c.page + 31) / 32;
+    const int64_t room = j.c.width * j.c.page, blocks = room / 32 + 1;
     int64_t groups = rows;
     j.split = j.a.ws != nullptr;
+    j.room = room < INT32_MAX ? (int)room : INT32_MAX;
+    // the list is counted in 32 bits
+    const int64_t most_blocks = blocks < (int64_t(1) << 26) ? blocks : int64_t(1) << 26;   // of 2^31 tokens
+    if (j.a.nt * j.per >= (int64_t(1) << 31) || rows > ((int64_t(1) << 31) - 1) / (j.split ? most_blocks : 1)) return -1;
     if (j.split) {
         const int64_t each = 2 * SLOT<D> * 4 + (int64_t)sizeof(Header);
         int64_t most = ATTEND_WS_BYTES / each;
         if (most > 1024) most = 1024;
-        const int64_t want = blocks > (int64_t(1) << 40) / rows ? most : (rows * blocks + WAVES - 1) / WAVES;
+        const int64_t want = (rows * most_blocks + WAVES - 1) / WAVES;
         groups = want < 1 ? 1 : want < most ? want : most;
         j.headers = static_cast<Header *>(j.a.ws);
         j.slots = reinterpret_cast<float *>(j.headers + groups);
@@ -565,7 +693,7 @@ int launch_typed(Job j, hipStream_t stream)
     j.groups = (int)groups;
     const int rc = launch_kernel(kv4_kernel<T, D, QP, PP>, dim3((unsigned)groups), dim3(256), stream, j);
     if (rc != 0 || !j.split) return rc;
-    return launch_kernel(kv4_join<D>, dim3((unsigned)groups), dim3(256), stream, j);
+    return launch_kernel(kv4_join<D>, dim3((unsigned)groups * 4), dim3(256), stream, j);
 }
 
 template <int D>
@@ -583,7 +711,7 @@ int launch_dim(const Job &j, hipStream_t stream)
 
 int launch_attend_kv4(const Kv4 &c, const Kv4Attend &a, hipStream_t stream)
 {
-    Job j = {c, a, a.hq / c.heads, 0, 0, nullptr, nullptr};
+    Job j = {c, a, a.hq / c.heads, 0, 0, 0, nullptr, nullptr};
     if (c.d == 64) return launch_dim<64>(j, stream);
     if (c.d == 128) return launch_dim<128>(j, stream);
     return launch_dim<256>(j, stream);

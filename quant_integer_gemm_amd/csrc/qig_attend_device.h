@@ -38,6 +38,14 @@ __device__ __forceinline__ int held(int at, int64_t n)
     return at < 0 ? 0 : at > n ? (int)n : at;
 }
 
+// One result at element `at` of y, rounded once to y's type.
+__device__ __forceinline__ void store1(void *y, int type, int64_t at, float f)
+{
+    if (type == T_F32) static_cast<float *>(y)[at] = f;
+    else if (type == T_BF16) static_cast<__bf16 *>(y)[at] = (__bf16)f;
+    else static_cast<_Float16 *>(y)[at] = (_Float16)f;
+}
+
 // Four results in a row at element `at` of y, each rounded once to y's type.
 __device__ __forceinline__ void store4(void *y, int type, int64_t at, const float (&f)[4])
 {
