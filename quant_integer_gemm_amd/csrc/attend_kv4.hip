@@ -40,7 +40,7 @@
 namespace qig {
 namespace {
 
-constexpr int WAVES = 4, ROWS = 16;
+constexpr int WAVES = 4, ROWS = 16, CUS = 256;
 constexpr float LAZY = 8.0f;   // the reference follows the maximum when it is this far behind
 
 template <int... I, typename F>
@@ -236,8 +236,12 @@ __device__ __forceinline__ void load_values(const uint8_t *block, int lane, Valu
     load_words<Q>(block + 36 * D + lane * (4 * Q), v.s);
 }
 
+// Workgroups that a CU holds at once (by their registers); with a workspace there are
+// as many in all, each with its share of the list, so that none waits for another's end.
+template <int D, int QP, int PP> constexpr int RESIDENT = D == 256 ? 1 : D == 64 ? 4 : QP + PP == 4 ? 2 : 3;
+
 template <int T, int D, int QP, int PP>
-__global__ __launch_bounds__(256, D == 256 ? 1 : D == 64 ? 4 : QP + PP == 4 ? 2 : 3) void kv4_kernel(Job j)
+__global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
 {
     typedef elem_t<T> E;
     constexpr int G = D / 32, Q = G / 2, TILES = D / 16;
@@ -683,7 +687,7 @@ int launch_typed(Job j, hipStream_t stream)
     if (j.split) {
         const int64_t each = 2 * SLOT<D> * 4 + (int64_t)sizeof(Header);
         int64_t most = ATTEND_WS_BYTES / each;
-        if (most > 1024) most = 1024;
+        if (most > CUS * RESIDENT<D, QP, PP>) most = CUS * RESIDENT<D, QP, PP>;
         const int64_t want = (rows * most_blocks + WAVES - 1) / WAVES;
         groups = want < 1 ? 1 : want < most ? want : most;
         j.headers = static_cast<Header *>(j.a.ws);

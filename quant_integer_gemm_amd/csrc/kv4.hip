@@ -12,40 +12,54 @@
 namespace qig {
 namespace {
 
-// Where a packed token stands.
+// Where a packed token stands.  All lanes of a wave ask for the same one.
 struct Place {
     int64_t block;   // byte offset of head 0's block in the pages, -1: nowhere
     int u, h, i;     // token 16 u + 4 h + i of the block
+    bool inside;     // it is some sequence's
 };
 
 __device__ __forceinline__ Place find_place(const Kv4 &c, int64_t nt, int token)
 {
-    Place p = {-1, 0, 0, 0};
-    int seq = token;
-    int64_t pos;
+    Place p = {-1, 0, 0, 0, false};
+    int seq = token, last = token + 1;
     if (c.starts) {
-        int lo = 0, hi = (int)c.nseq + 1;        // starts at or before the token
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (held(c.starts[mid], nt) <= token) lo = mid + 1; else hi = mid;
-        }
-        seq = lo - 1;
+        const int32_t *starts = c.starts;
+        seq = __builtin_amdgcn_readfirstlane(
+            count_first((int)c.nseq + 1, [&](int s) { return held(starts[s], nt) <= token; }) - 1);
         if (seq < 0 || seq >= c.nseq) return p;
-        pos = (int64_t)c.lengths[seq] - held(c.starts[seq + 1], nt) + token;
-    } else {
-        pos = (int64_t)c.lengths[seq] - 1;
+        last = held(c.starts[seq + 1], nt);
     }
-    const int64_t col = pos / c.page;
-    if (pos < 0 || col >= c.width) return p;
+    p.inside = true;
+    const int64_t pos = (int64_t)c.lengths[seq] - last + token;
+    if (pos < 0 || pos >= c.width * c.page) return p;
+    const int col = (int)(pos / c.page), r = (int)(pos - (int64_t)col * c.page);
     const int page = c.tables[(int64_t)seq * c.ld + col];
     if (page < 0 || page >= c.npages) return p;
-    const int r = (int)(pos - col * c.page);
     p.block = (int64_t)page * c.page_bytes + (int64_t)(r >> 5) * (40 * c.d);
     p.u = (r >> 4) & 1;
     p.h = (r >> 2) & 3;
     p.i = r & 3;
     return p;
 }
+
+// A wave takes one token and 512 channels: 512 / D rows of the token's keys' heads and
+// then its values' heads, eight channels a lane, so that four lanes have a group.
+template <int D>
+struct Lane {
+    int token, head, c;     // c: the lane's first channel
+    bool values, real;
+    __device__ __forceinline__ Lane(const Kv4 &k, int64_t wave, int chunks)
+    {
+        const int lane = threadIdx.x & 63;
+        token = __builtin_amdgcn_readfirstlane((int)(wave / chunks));
+        const int r = (int)(wave % chunks) * (512 / D) + lane / (D / 8);
+        values = r >= k.heads;
+        head = values ? r - k.heads : r;
+        real = r < 2 * k.heads;
+        c = lane % (D / 8) * 8;
+    }
+};
 
 __device__ __forceinline__ uint32_t floor_bf16(float x)
 {
@@ -72,158 +86,170 @@ __device__ __forceinline__ uint32_t scale_word(float lo, float hi, float &s, flo
     return mb | (sb >> 16);
 }
 
-// Which code is nearest is decided in 64 bits.
-__device__ __forceinline__ uint32_t code4(float x, float s, float m)
+// The code of x.  d = x - m is exact in 64 bits, and so is the sign of d - (c -+ 1/2) s
+// (one rounding in an fma): c from the product with 1 / s is at most one off and is put
+// right by these.
+__device__ __forceinline__ uint32_t code4(float x, double m, double s, double inv)
 {
-    if (!(s > 0.0f)) return 0;
-    const double v = __builtin_floor(((double)x - (double)m) / (double)s + 0.5);
-    return v > 15.0 ? 15u : v > 0.0 ? (uint32_t)v : 0u;
+    const double d = (double)x - m;
+    double c = __builtin_floor(__builtin_fma(d, inv, 0.5));
+    c = __builtin_fma(0.5 - c, s, d) < 0.0 ? c - 1.0 : __builtin_fma(-0.5 - c, s, d) >= 0.0 ? c + 1.0 : c;
+    return c > 15.0 ? 15u : c > 0.0 ? (uint32_t)c : 0u;
 }
 
-// A thread: 64 channels of one token and head, of its keys or its values.
-template <int T>
-__global__ __launch_bounds__(256) void write_kernel(Kv4 c, Kv4Rows r, int64_t first, int64_t count)
+// The lowest (or highest) of the four lanes of a group; a NaN stays.
+template <bool LOW>
+__device__ __forceinline__ float of_group(float v)
 {
-    const int64_t id = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= first + count) return;
-    const int part = (int)(id % (c.d / 64));
-    const int64_t row = id / (c.d / 64) / 2;
-    const bool values = (id / (c.d / 64)) & 1;
-    const int head = (int)(row % c.heads), token = (int)(row / c.heads);
-    const Place p = find_place(c, r.nt, token);
-    if (p.block < 0) return;
-    uint8_t *block = c.pages + p.block + (int64_t)head * (c.page / 32) * (40 * c.d);
-    const Heads &from = values ? r.v : r.k;
-    const elem_t<T> *x = static_cast<const elem_t<T> *>(from.p) + (int64_t)token * from.token +
-                         (int64_t)head * from.head + part * 64;
-    const int G = c.d / 32;
-    uint32_t *scales = reinterpret_cast<uint32_t *>(block) + (values ? 9 : 8) * c.d + (p.h * 8 + p.u * 4 + p.i) * G;
-    uint32_t half[16];
+    const auto pick = [](float a, float b) { return (LOW ? b < a : b > a) || b != b ? b : a; };
+    v = pick(v, __shfl_xor(v, 1));
+    return pick(v, __shfl_xor(v, 2));
+}
+
+template <int T, int D>
+__global__ __launch_bounds__(256) void write_kernel(Kv4 c, Kv4Rows r, int64_t first, int64_t count, int chunks)
+{
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (wave >= count) return;
+    const Lane<D> me(c, first + wave, chunks);
+    float f[8];
 #pragma unroll
-    for (int l = 0; l < 16; ++l) half[l] = 0;
+    for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+    if (me.real) {
+        const Heads &from = me.values ? r.v : r.k;
+        const elem_t<T> *x = static_cast<const elem_t<T> *>(from.p) + (int64_t)me.token * from.token +
+                             (int64_t)me.head * from.head + me.c;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        float f[32];
-#pragma unroll
-        for (int k = 0; k < 32 / VEC<T>; ++k) {
+        for (int k = 0; k < 8 / VEC<T>; ++k) {
             float t[VEC<T>];
-            unpack16<T>(load16<T>(x + g * 32 + k * VEC<T>), t);
+            unpack16<T>(load16<T>(x + k * VEC<T>), t);
 #pragma unroll
             for (int i = 0; i < VEC<T>; ++i) f[k * VEC<T> + i] = t[i];
         }
-        float lo = f[0], hi = f[0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i) {
-            // a NaN stays: the group then stands for NaN
-            lo = f[i] < lo || f[i] != f[i] ? f[i] : lo;
-            hi = f[i] > hi || f[i] != f[i] ? f[i] : hi;
-        }
-        float s, m;
-        scales[part * 2 + g] = scale_word(lo, hi, s, m);
-        if (!values) {
-            const int w = p.u * G + part * 2 + g;
-            uint32_t *at = reinterpret_cast<uint32_t *>(block) + ((w >> 2) * 64 + 4 * p.h + p.i) * 4 + (w & 3);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t word = 0;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) word |= code4(f[e * 8 + k], s, m) << (16 * (k & 1) + 4 * (k >> 1));
-                at[e * 64] = word;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) half[k & 15] |= code4(f[k], s, m) << (4 * (2 * g + (k >> 4)));
-        }
     }
-    if (values) {
-        const int w = (2 * p.u + (p.i >> 1)) * (c.d / 64) + part;
-        uint16_t *at = reinterpret_cast<uint16_t *>(block) +
-                       2 * (4 * c.d + ((w >> 2) * 64 + p.h * 16) * 4 + (w & 3)) + (p.i & 1);
+    const Place p = find_place(c, r.nt, me.token);
+    if (p.block < 0) return;
+    float lo = f[0], hi = f[0];
 #pragma unroll
-        for (int l = 0; l < 16; ++l) at[l * 8] = (uint16_t)half[l];
+    for (int i = 1; i < 8; ++i) {
+        // a NaN stays: the group then stands for NaN
+        lo = f[i] < lo || f[i] != f[i] ? f[i] : lo;
+        hi = f[i] > hi || f[i] != f[i] ? f[i] : hi;
+    }
+    float s, m;
+    const uint32_t word = scale_word(of_group<true>(lo), of_group<false>(hi), s, m);
+    const double inv = s > 0.0f ? 1.0 / (double)s : 0.0;
+    uint32_t code[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) code[k] = s > 0.0f ? code4(f[k], m, s, inv) : 0;
+
+    constexpr int G = D / 32;
+    const int g = me.c / 32, e = me.c % 32 / 8;
+    uint8_t *block = c.pages + p.block + (int64_t)me.head * (c.page / 32) * (40 * D);
+    uint32_t *words = reinterpret_cast<uint32_t *>(block);
+    if (me.real && e == 0) words[(me.values ? 9 : 8) * D + (p.h * 8 + p.u * 4 + p.i) * G + g] = word;
+    // keys: the lane's channels are one word
+    if (me.real && !me.values) {
+        uint32_t all = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) all |= code[k] << (16 * (k & 1) + 4 * (k >> 1));
+        const int w = p.u * G + g;
+        words[((w >> 2) * 64 + e * 16 + 4 * p.h + p.i) * 4 + (w & 3)] = all;
+    }
+    // values: channel 64 n + 16 b + l in bits 4 b of the half word l; the four lanes with the
+    // same l have b = 0 .. 3, and each then writes two of their eight
+    if (__any(me.values)) {
+        const int n = me.c / 64, b = me.c / 16 % 4, l0 = me.c % 16;
+        uint32_t two[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            two[k] = (code[2 * k] | code[2 * k + 1] << 16) << (4 * b);
+            two[k] |= __shfl_xor(two[k], 2);
+            two[k] |= __shfl_xor(two[k], 4);
+        }
+        const uint32_t out = b == 0 ? two[0] : b == 1 ? two[1] : b == 2 ? two[2] : two[3];
+        if (me.real && me.values) {
+            const int w = (2 * p.u + (p.i >> 1)) * (D / 64) + n;
+            uint16_t *at = reinterpret_cast<uint16_t *>(block) +
+                           2 * (4 * D + ((w >> 2) * 64 + p.h * 16 + l0 + 2 * b) * 4 + (w & 3)) + (p.i & 1);
+            at[0] = (uint16_t)out;
+            at[8] = (uint16_t)(out >> 16);
+        }
     }
 }
 
 // The same rows back, as the values that they stand for; tokens that stand
 // nowhere are zeros.
-template <int T>
-__global__ __launch_bounds__(256) void read_kernel(Kv4 c, Kv4Rows r, int64_t first, int64_t count)
+template <int T, int D>
+__global__ __launch_bounds__(256) void read_kernel(Kv4 c, Kv4Rows r, int64_t first, int64_t count, int chunks)
 {
-    const int64_t id = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= first + count) return;
-    const int part = (int)(id % (c.d / 64));
-    const int64_t row = id / (c.d / 64) / 2;
-    const bool values = (id / (c.d / 64)) & 1;
-    const int head = (int)(row % c.heads), token = (int)(row / c.heads);
-    if (c.starts && (token < held(c.starts[0], r.nt) || token >= held(c.starts[c.nseq], r.nt))) return;
-    const Place p = find_place(c, r.nt, token);
-    const Heads &to = values ? r.v : r.k;
-    elem_t<T> *y = static_cast<elem_t<T> *>(const_cast<void *>(to.p)) + (int64_t)token * to.token +
-                   (int64_t)head * to.head + part * 64;
-    const uint8_t *block = c.pages + p.block + (int64_t)head * (c.page / 32) * (40 * c.d);
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (wave >= count) return;
+    const Lane<D> me(c, first + wave, chunks);
+    const Place p = find_place(c, r.nt, me.token);
+    if (!p.inside || !me.real) return;
+    constexpr int G = D / 32;
+    const int g = me.c / 32, e = me.c % 32 / 8;
+    const uint8_t *block = c.pages + p.block + (int64_t)me.head * (c.page / 32) * (40 * D);
     const uint32_t *words = reinterpret_cast<const uint32_t *>(block);
-    const uint16_t *halves = reinterpret_cast<const uint16_t *>(block);
-    const int G = c.d / 32;
+    float f[8];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        float f[32];
-        if (p.block < 0) {
+    for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+    if (p.block >= 0) {
+        const uint32_t sm = words[(me.values ? 9 : 8) * D + (p.h * 8 + p.u * 4 + p.i) * G + g];
+        const float s = __builtin_bit_cast(float, sm << 16), m = __builtin_bit_cast(float, sm & 0xffff0000u);
+        uint32_t code[8];
+        if (!me.values) {
+            const int w = p.u * G + g;
+            const uint32_t all = words[((w >> 2) * 64 + e * 16 + 4 * p.h + p.i) * 4 + (w & 3)];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = 0.0f;
+            for (int k = 0; k < 8; ++k) code[k] = all >> (16 * (k & 1) + 4 * (k >> 1));
         } else {
-            const uint32_t sm = words[(values ? 9 : 8) * c.d + (p.h * 8 + p.u * 4 + p.i) * G + part * 2 + g];
-            const float s = __builtin_bit_cast(float, sm << 16), m = __builtin_bit_cast(float, sm & 0xffff0000u);
-            if (!values) {
-                const int w = p.u * G + part * 2 + g;
-                const uint32_t *at = words + ((w >> 2) * 64 + 4 * p.h + p.i) * 4 + (w & 3);
+            const int n = me.c / 64, b = me.c / 16 % 4, l0 = me.c % 16, w = (2 * p.u + (p.i >> 1)) * (D / 64) + n;
+            const uint16_t *at = reinterpret_cast<const uint16_t *>(block) +
+                                 2 * (4 * D + ((w >> 2) * 64 + p.h * 16 + l0) * 4 + (w & 3)) + (p.i & 1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t word = at[e * 64];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        f[e * 8 + k] = __builtin_fmaf((float)((word >> (16 * (k & 1) + 4 * (k >> 1))) & 15u), s, m);
-                }
-            } else {
-                const int w = (2 * p.u + (p.i >> 1)) * (c.d / 64) + part;
-                const uint16_t *at = halves + 2 * (4 * c.d + ((w >> 2) * 64 + p.h * 16) * 4 + (w & 3)) + (p.i & 1);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    f[k] = __builtin_fmaf((float)((at[(k & 15) * 8] >> (4 * (2 * g + (k >> 4)))) & 15u), s, m);
-            }
+            for (int k = 0; k < 8; ++k) code[k] = at[k * 8] >> (4 * b);
         }
 #pragma unroll
-        for (int k = 0; k < 32 / VEC<T>; ++k) {
-            float t[VEC<T>];
+        for (int k = 0; k < 8; ++k) f[k] = __builtin_fmaf((float)(code[k] & 15u), s, m);
+    }
+    const Heads &to = me.values ? r.v : r.k;
+    elem_t<T> *y = static_cast<elem_t<T> *>(const_cast<void *>(to.p)) + (int64_t)me.token * to.token +
+                   (int64_t)me.head * to.head + me.c;
 #pragma unroll
-            for (int i = 0; i < VEC<T>; ++i) t[i] = f[k * VEC<T> + i];
-            store16<T>(y + g * 32 + k * VEC<T>, pack16<T>(t));
-        }
+    for (int k = 0; k < 8 / VEC<T>; ++k) {
+        float t[VEC<T>];
+#pragma unroll
+        for (int i = 0; i < VEC<T>; ++i) t[i] = f[k * VEC<T> + i];
+        store16<T>(y + k * VEC<T>, pack16<T>(t));
     }
 }
 
-template <typename K>
-int launch_rows(K kernel, const Kv4 &c, const Kv4Rows &r, hipStream_t stream)
+template <int D, bool WRITE>
+int launch_rows(const Kv4 &c, const Kv4Rows &r, hipStream_t stream)
 {
-    const int64_t units = r.nt * c.heads * 2 * (c.d / 64);
-    return in_launches(units, launch_groups(256) * 256, [&](int64_t first, int64_t count) {
-        return launch_kernel(kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), stream, c, r, first, count);
+    const int chunks = (2 * c.heads * D + 511) / 512;
+    return in_launches(r.nt * chunks, launch_groups(256) * 4, [&](int64_t first, int64_t count) {
+        const dim3 grid((unsigned)((count + 3) / 4)), block(256);
+        const auto go = [&](auto kernel) { return launch_kernel(kernel, grid, block, stream, c, r, first, count, chunks); };
+        if (r.type == T_F32) return WRITE ? go(write_kernel<T_F32, D>) : go(read_kernel<T_F32, D>);
+        if (r.type == T_BF16) return WRITE ? go(write_kernel<T_BF16, D>) : go(read_kernel<T_BF16, D>);
+        return WRITE ? go(write_kernel<T_F16, D>) : go(read_kernel<T_F16, D>);
     });
+}
+
+template <bool WRITE>
+int launch_dim(const Kv4 &c, const Kv4Rows &r, hipStream_t stream)
+{
+    if (c.d == 64) return launch_rows<64, WRITE>(c, r, stream);
+    if (c.d == 128) return launch_rows<128, WRITE>(c, r, stream);
+    return launch_rows<256, WRITE>(c, r, stream);
 }
 
 }  // namespace
 
-int launch_write_kv4(const Kv4 &c, const Kv4Rows &r, hipStream_t stream)
-{
-    if (r.type == T_F32) return launch_rows(write_kernel<T_F32>, c, r, stream);
-    if (r.type == T_BF16) return launch_rows(write_kernel<T_BF16>, c, r, stream);
-    return launch_rows(write_kernel<T_F16>, c, r, stream);
-}
-
-int launch_read_kv4(const Kv4 &c, const Kv4Rows &r, hipStream_t stream)
-{
-    if (r.type == T_F32) return launch_rows(read_kernel<T_F32>, c, r, stream);
-    if (r.type == T_BF16) return launch_rows(read_kernel<T_BF16>, c, r, stream);
-    return launch_rows(read_kernel<T_F16>, c, r, stream);
-}
+int launch_write_kv4(const Kv4 &c, const Kv4Rows &r, hipStream_t stream) { return launch_dim<true>(c, r, stream); }
+int launch_read_kv4(const Kv4 &c, const Kv4Rows &r, hipStream_t stream) { return launch_dim<false>(c, r, stream); }
 
 }  // namespace qig
