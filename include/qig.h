@@ -692,6 +692,16 @@ int compact_pages(void *pages, int64_t page_bytes, int64_t page_stride, int32_t 
                   hipStream_t stream);
 
 /*
+ * The calls above with their arguments, all but the stream, in the order of their
+ * declarations as 8-byte words (int64_t, a pointer's address, or the scale as a
+ * double), for bindings that convert arguments one by one.  op: 0 attend_prompt, 1
+ * write_kv4, 2 read_kv4, 3 attend_kv4, 4 copy_pages, 5 free_pages, 6 take_pages, 7
+ * fork_pages, 8 compact_pages; QIG_EINVAL for others, and for an int that does not
+ * fit.
+ */
+int qig_attend_packed(int op, const void *words, hipStream_t stream);
+
+/*
  * Test exports: the int32 sub-block partials of the same kernels, for the
  * window of tokens [t0, t1) and rows [j0, j1), written to
  * P[(t - t0)][(j - j0)][sub] (int32, 4-byte aligned), where sub runs over all

@@ -8,28 +8,56 @@ be captured into a graph.
 """
 from __future__ import annotations
 
+import struct
+
 from . import _int8 as _i
-from ._int8 import _call, _is, _matrix, _new, _type
+from ._int8 import _device_of, _is, _matrix, _new, _type
 from ._lib import QigError, load
+
+# The library's calls by number, their arguments packed into one block of 8-byte words
+# (qig_attend_packed): ctypes takes 5 us to convert 25 arguments and 1 us for a block.
+_OPS = {name: (n, struct.Struct(layout)) for n, (name, layout) in enumerate((
+    ("attend_prompt", "=19qd4q"), ("write_kv4", "=20q"), ("read_kv4", "=20q"), ("attend_kv4", "=18qd5q"),
+    ("copy_pages", "=7q"), ("free_pages", "=9q"), ("take_pages", "=10q"), ("fork_pages", "=16q"),
+    ("compact_pages", "=12q")))}
 
 
 def _start():
+    global _i32, _u8, _packed
     if _i.torch is None:
         _i._start()
+    _i32, _u8, _packed = _i.torch.int32, _i.torch.uint8, load().qig_attend_packed
     return _i.torch
+
+
+_packed = None
+
+
+def _call(what, names, tensors, stream, *args):
+    """The library's call `what` with these arguments, on the GPU of the tensors."""
+    op, layout = _OPS[what]
+    dev, here, handle = _device_of(names, tensors, stream)
+    if here:
+        rc = _packed(op, layout.pack(*args), handle)
+    else:
+        with _i.torch.cuda.device(dev):
+            rc = _packed(op, layout.pack(*args), handle)
+    if rc:
+        _i._check(rc, what)
 
 
 def _heads(t, name, heads=None, d=None):
     """(tokens, heads, d, token stride, head stride) of a 3-D tensor with unit
     stride in its last dimension."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1 and t.numel() > 0):
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1 and t.numel() > 0):
         raise QigError(f"{name} must be [tokens][heads][d] with unit stride in the last dimension")
-    if heads is not None and shape[1] != heads:
-        raise QigError(f"{name} has {shape[1]} heads, not {heads}")
-    if d is not None and shape[2] != d:
-        raise QigError(f"{name} has heads of {shape[2]}, not {d}")
-    return shape[0], shape[1], shape[2], stride[0], stride[1]
+    n, h, c = shape
+    if heads is not None and h != heads:
+        raise QigError(f"{name} has {h} heads, not {heads}")
+    if d is not None and c != d:
+        raise QigError(f"{name} has heads of {c}, not {d}")
+    return n, h, c, stride[0], stride[1]
 
 
 def _result(y, name, dtype, nt, heads, d, device, stream):
@@ -51,18 +79,22 @@ def _result(y, name, dtype, nt, heads, d, device, stream):
 
 def _ints(t, n, name):
     """A contiguous int32 vector of n."""
-    _is(t, _i.torch.int32, name)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise QigError(f"{name} must be contiguous with {n} elements, not {list(t.shape)}")
+    if t.dtype is _i32 and t.shape == (n,) and t.is_contiguous():
+        return
+    _is(t, _i32, name)
+    raise QigError(f"{name} must be contiguous with {n} elements, not {list(t.shape)}")
 
 
-def _packed(starts, nseq, name="starts"):
-    _ints(starts, nseq + 1, name)
+def _length(t, name):
+    if len(t.shape) != 1:
+        raise QigError(f"{name} must be a vector")
+    return t.shape[0]
 
 
 def _table(tables):
     """(rows, entries a row, row stride)."""
-    _is(tables, _i.torch.int32, "tables")
+    if tables.dtype is not _i32:
+        _is(tables, _i32, "tables")
     return _matrix(tables, "tables")
 
 
@@ -76,7 +108,8 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, y=Non
     scale: 1 / sqrt(d) where it is None.  y is of q's type, or of ``dtype`` or the
     given y's type; rows outside of every sequence are not written, queries that
     see no key get zeros."""
-    torch = _start()
+    if _packed is None:
+        _start()
     qt = _type(q.dtype, "q")
     _is(k, q.dtype, "k")
     _is(v, q.dtype, "v")
@@ -85,24 +118,23 @@ def attend_prompt(q, k, v, starts, k_starts=None, causal=True, scale=None, y=Non
     nv, _, _, vn, vh = _heads(v, "v", hkv, d)
     if nv != nk:
         raise QigError(f"v has {nv} tokens, k has {nk}")
-    if starts.dim() != 1 or starts.shape[0] < 1:
-        raise QigError("starts must be a vector of one more than the sequences")
-    nseq = starts.shape[0] - 1
-    _packed(starts, nseq)
+    n = _length(starts, "starts")
+    if n < 1:
+        raise QigError("starts must hold one more than the sequences")
+    _ints(starts, n, "starts")
     if k_starts is None:
         k_starts = starts
-    else:
-        _packed(k_starts, nseq, "k_starts")
+    elif k_starts is not starts:
+        _ints(k_starts, n, "k_starts")
     if scale is not None and not scale > 0:
         raise QigError(f"scale must be above 0, not {scale}")
     if dtype is None and y is None:
         dtype = q.dtype
     y, yt, yn, yh = _result(y, "y", dtype, nt, hq, d, q.device, stream)
-    _call(_i._lib.attend_prompt, "attend_prompt", ("q", "k", "v", "starts", "k_starts", "y"),
-          (q, k, v, starts, k_starts, y), stream,
-          (q.data_ptr(), qn, qh, k.data_ptr(), kn, kh, v.data_ptr(), vn, vh, qt, nt, nk, hq, hkv, d,
-           starts.data_ptr(), k_starts.data_ptr(), nseq, 1 if causal else 0, 0.0 if scale is None else scale,
-           y.data_ptr(), yn, yh, yt))
+    _call("attend_prompt", ("q", "k", "v", "starts", "k_starts", "y"), (q, k, v, starts, k_starts, y), stream,
+          q.data_ptr(), qn, qh, k.data_ptr(), kn, kh, v.data_ptr(), vn, vh, qt, nt, nk, hq, hkv, d,
+          starts.data_ptr(), k_starts.data_ptr(), n - 1, 1 if causal else 0, 0.0 if scale is None else scale,
+          y.data_ptr(), yn, yh, yt)
     return y
 
 
@@ -127,11 +159,14 @@ def new_kv4(npages, heads, d, page=64, device="cuda"):
 
 def _cache(pages, tables, lengths, starts, nt, d):
     """The cache's arguments of a call, from heads of d on."""
-    _is(pages, _i.torch.uint8, "pages")
+    if pages.dtype is not _u8:
+        _is(pages, _u8, "pages")
     shape, stride = pages.shape, pages.stride()
-    if len(shape) != 3 or (pages.numel() > 0 and (stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]))):
+    if len(shape) != 3:
         raise QigError("pages must be [pages][heads][bytes], each page contiguous")
     npages, heads, nbytes = shape
+    if (stride[2] != 1 or (heads > 1 and stride[1] != nbytes)) and pages.numel() > 0:
+        raise QigError("pages must be [pages][heads][bytes], each page contiguous")
     page, rest = divmod(nbytes * 4, 5 * d) if d > 0 else (0, 1)
     if rest or page % 32 or page == 0:
         raise QigError(f"pages of {nbytes} bytes a head hold no whole blocks of 32 tokens with heads of {d}")
@@ -140,13 +175,15 @@ def _cache(pages, tables, lengths, starts, nt, d):
     if starts is None:
         if nt != nseq:
             raise QigError(f"{nt} tokens for {nseq} sequences: starts says which are whose")
+        at = 0
     else:
-        _packed(starts, nseq)
+        _ints(starts, nseq + 1, "starts")
+        at = starts.data_ptr()
     return (heads, d, pages.data_ptr(), npages, stride[0] if npages > 1 else heads * nbytes, page, tables.data_ptr(), ld,
-            width, lengths.data_ptr(), None if starts is None else starts.data_ptr(), nseq)
+            width, lengths.data_ptr(), at, nseq)
 
 
-_CACHE = ("pages", "tables", "lengths", "starts")
+_ROWS = ("k", "v", "pages", "tables", "lengths", "starts")
 
 
 def write_kv4(k, v, pages, tables, lengths, starts=None, stream=None):
@@ -155,7 +192,8 @@ def write_kv4(k, v, pages, tables, lengths, starts=None, stream=None):
     sequence's pages, lengths[nseq] (int32) its tokens with the new ones; sequence
     s's are the rows starts[s] .. starts[s + 1], or without starts row s alone.
     Tokens whose place the table does not have are left out."""
-    _start()
+    if _packed is None:
+        _start()
     code = _type(k.dtype, "k")
     _is(v, k.dtype, "v")
     nt, heads, d, kn, kh = _heads(k, "k")
@@ -165,8 +203,8 @@ def write_kv4(k, v, pages, tables, lengths, starts=None, stream=None):
     cache = _cache(pages, tables, lengths, starts, nt, d)
     if cache[0] != heads:
         raise QigError(f"k has {heads} heads, pages have {cache[0]}")
-    _call(_i._lib.write_kv4, "write_kv4", ("k", "v") + _CACHE, (k, v, pages, tables, lengths, starts), stream,
-          (k.data_ptr(), kn, kh, v.data_ptr(), vn, vh, code, nt) + cache)
+    _call("write_kv4", _ROWS, (k, v, pages, tables, lengths, starts), stream,
+          k.data_ptr(), kn, kh, v.data_ptr(), vn, vh, code, nt, *cache)
 
 
 def read_kv4(pages, tables, lengths, d, starts=None, nt=None, k=None, v=None, dtype=None, stream=None):
@@ -175,7 +213,8 @@ def read_kv4(pages, tables, lengths, d, starts=None, nt=None, k=None, v=None, dt
     starts is given and k is not.  fp32, or of ``dtype`` or the given tensors' type.
     Rows that stand nowhere in the cache are zeros, those outside of every
     sequence are not written."""
-    torch = _start()
+    if _packed is None:
+        _start()
     if nt is None:
         if k is not None or v is not None:
             nt = (v if k is None else k).shape[0]
@@ -186,11 +225,11 @@ def read_kv4(pages, tables, lengths, d, starts=None, nt=None, k=None, v=None, dt
     cache = _cache(pages, tables, lengths, starts, nt, d)
     heads = cache[0]
     if dtype is None:
-        dtype = torch.float32 if k is None and v is None else (v if k is None else k).dtype
+        dtype = _i.torch.float32 if k is None and v is None else (v if k is None else k).dtype
     k, code, kn, kh = _result(k, "k", dtype, nt, heads, d, pages.device, stream)
     v, _, vn, vh = _result(v, "v", dtype, nt, heads, d, pages.device, stream)
-    _call(_i._lib.read_kv4, "read_kv4", ("k", "v") + _CACHE, (k, v, pages, tables, lengths, starts), stream,
-          (k.data_ptr(), kn, kh, v.data_ptr(), vn, vh, code, nt) + cache)
+    _call("read_kv4", _ROWS, (k, v, pages, tables, lengths, starts), stream,
+          k.data_ptr(), kn, kh, v.data_ptr(), vn, vh, code, nt, *cache)
     return k, v
 
 
@@ -202,7 +241,8 @@ def attend_kv4(q, pages, tables, lengths, starts=None, scale=None, y=None, dtype
     nothing get zeros.  scale: 1 / sqrt(d) where it is None.  y is of q's type, or of
     ``dtype`` or the given y's.  ws: None, or a workspace (qig.workspace()), which
     lets long sequences be split over the whole GPU."""
-    _start()
+    if _packed is None:
+        _start()
     code = _type(q.dtype, "q")
     nt, hq, d, qn, qh = _heads(q, "q")
     cache = _cache(pages, tables, lengths, starts, nt, d)
@@ -211,11 +251,12 @@ def attend_kv4(q, pages, tables, lengths, starts=None, scale=None, y=None, dtype
     if dtype is None and y is None:
         dtype = q.dtype
     y, yt, yn, yh = _result(y, "y", dtype, nt, hq, d, q.device, stream)
-    if ws is not None and (ws.numel() * ws.element_size() < _i._ws_bytes or not ws.is_contiguous()):
+    if ws is not None and (ws.numel() * (1 if ws.dtype is _u8 else ws.element_size()) < _i._ws_bytes
+                           or not ws.is_contiguous()):
         raise QigError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs {_i._ws_bytes}, contiguous")
-    _call(_i._lib.attend_kv4, "attend_kv4", ("q",) + _CACHE + ("y", "ws"), (q, pages, tables, lengths, starts, y, ws),
-          stream, (q.data_ptr(), qn, qh, code, nt, hq) + cache +
-          (0.0 if scale is None else scale, y.data_ptr(), yn, yh, yt, None if ws is None else ws.data_ptr()))
+    _call("attend_kv4", ("q", "pages", "tables", "lengths", "starts", "y", "ws"),
+          (q, pages, tables, lengths, starts, y, ws), stream, q.data_ptr(), qn, qh, code, nt, hq, *cache,
+          0.0 if scale is None else scale, y.data_ptr(), yn, yh, yt, 0 if ws is None else ws.data_ptr())
     return y
 
 
@@ -228,36 +269,34 @@ def _whole_pages(pages):
     if len(shape) < 2:
         raise QigError("pages must have a dimension of pages and others in each page")
     n = 1
-    for size, step in zip(shape[:0:-1], stride[:0:-1]):
-        if size != 1 and step != n and pages.numel() > 0:
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != n and shape[i] != 1 and pages.numel() > 0:
             raise QigError("each page must be contiguous")
-        n *= size
+        n *= shape[i]
     e = pages.element_size()
     return shape[0], n * e, stride[0] * e if shape[0] > 1 else n * e
 
 
-def _pool(tables, lengths, refs):
-    rows, width, ld = _table(tables)
-    if lengths is not None:
-        _ints(lengths, rows, "lengths")
-    _is(refs, _i.torch.int32, "refs")
-    if refs.dim() != 1 or not refs.is_contiguous():
+def _refs(refs):
+    if refs.dtype is not _i32:
+        _is(refs, _i32, "refs")
+    if len(refs.shape) != 1 or not refs.is_contiguous():
         raise QigError("refs must be a contiguous vector, a count a page")
-    return rows, width, ld, refs.shape[0]
+    return refs.shape[0]
 
 
-def _scratch(npages, rows, device, stream):
-    n = _i._lib.pages_scratch_bytes(npages, rows)
-    if n == 0:
-        raise QigError(f"no pool of {npages} pages and {rows} rows")
-    return _new((n,), _i._u8, device, stream)
-
-
-def _count(t, name, device, stream):
-    if t is None:
-        return _new((1,), _i.torch.int32, device, stream)
-    _ints(t, 1, name)
-    return t
+def _count_and_scratch(given, name, npages, rows, device, stream):
+    """The int32 [1] that a call returns and its scratch memory: one new tensor, of
+    which the count is the first word (the scratch stands 8 bytes on)."""
+    n = (npages + 63) // 64 * 8 + rows * 4 + 8
+    if not 0 < npages <= 1 << 20:
+        raise QigError(f"no pool of {npages} pages")
+    scratch = _new(((n + 3) // 4,), _i32, device, stream)
+    if given is None:
+        given = scratch[:1]
+    else:
+        _ints(given, 1, name)
+    return given, scratch
 
 
 def copy_pages(pages, src, dst, stream=None):
@@ -265,15 +304,14 @@ def copy_pages(pages, src, dst, stream=None):
     with an index outside of the pages is left out.  No page may be named twice in
     dst, or in both src and dst other than in one pair.  pages: any tensor whose first
     dimension counts pages, each contiguous and of a multiple of 16 bytes."""
-    _start()
+    if _packed is None:
+        _start()
     npages, nbytes, step = _whole_pages(pages)
-    if src.dim() != 1:
-        raise QigError("src must be a vector")
-    n = src.shape[0]
+    n = _length(src, "src")
     _ints(src, n, "src")
     _ints(dst, n, "dst")
-    _call(_i._lib.copy_pages, "copy_pages", ("pages", "src", "dst"), (pages, src, dst), stream,
-          (pages.data_ptr(), npages, nbytes, step, src.data_ptr(), dst.data_ptr(), n))
+    _call("copy_pages", ("pages", "src", "dst"), (pages, src, dst), stream,
+          pages.data_ptr(), npages, nbytes, step, src.data_ptr(), dst.data_ptr(), n)
 
 
 def take_pages(tables, lengths, refs, page, missing=None, stream=None):
@@ -281,14 +319,15 @@ def take_pages(tables, lengths, refs, page, missing=None, stream=None):
     ceil(lengths[s] / page) of tables[s] that holds none gets a free one (refs 0,
     then 1), the lowest first, in the order of the table.  Returns int32 [1]: how many
     found none and stay -1."""
-    _start()
-    rows, width, ld, npages = _pool(tables, lengths, refs)
-    missing = _count(missing, "missing", refs.device, stream)
-    scratch = _scratch(npages, rows, refs.device, stream)
-    _call(_i._lib.take_pages, "take_pages", ("tables", "lengths", "refs", "missing", "scratch"),
-          (tables, lengths, refs, missing, scratch), stream,
-          (tables.data_ptr(), rows, ld, width, lengths.data_ptr(), refs.data_ptr(), npages, page, missing.data_ptr(),
-           scratch.data_ptr()))
+    if _packed is None:
+        _start()
+    rows, width, ld = _table(tables)
+    _ints(lengths, rows, "lengths")
+    npages = _refs(refs)
+    missing, scratch = _count_and_scratch(missing, "missing", npages, rows, refs.device, stream)
+    _call("take_pages", ("tables", "lengths", "refs", "missing"), (tables, lengths, refs, missing), stream,
+          tables.data_ptr(), rows, ld, width, lengths.data_ptr(), refs.data_ptr(), npages, page, missing.data_ptr(),
+          scratch.data_ptr() + 8)
     return missing
 
 
@@ -296,14 +335,14 @@ def free_pages(tables, lengths, refs, rows, stream=None):
     """The table's rows named by rows (int32 vector) give up their pages: refs of
     each is one less, their entries are -1 and their lengths 0.  Rows named twice
     do so once; those that the table does not have are left out."""
-    _start()
-    n, width, ld, npages = _pool(tables, lengths, refs)
-    if rows.dim() != 1:
-        raise QigError("rows must be a vector")
-    _ints(rows, rows.shape[0], "rows")
-    _call(_i._lib.free_pages, "free_pages", ("tables", "lengths", "refs", "rows"), (tables, lengths, refs, rows), stream,
-          (tables.data_ptr(), n, ld, width, lengths.data_ptr(), refs.data_ptr(), npages, rows.data_ptr(),
-           rows.shape[0]))
+    if _packed is None:
+        _start()
+    height, width, ld = _table(tables)
+    _ints(lengths, height, "lengths")
+    npages, n = _refs(refs), _length(rows, "rows")
+    _ints(rows, n, "rows")
+    _call("free_pages", ("tables", "lengths", "refs", "rows"), (tables, lengths, refs, rows), stream,
+          tables.data_ptr(), height, ld, width, lengths.data_ptr(), refs.data_ptr(), npages, rows.data_ptr(), n)
 
 
 def fork_pages(pages, tables, lengths, refs, parents, children, page, missing=None, stream=None):
@@ -313,23 +352,21 @@ def fork_pages(pages, tables, lengths, refs, parents, children, page, missing=No
     pairs).  A pair counts where both rows are the table's, no later pair has the
     same child and no pair has its parent as child.  Returns int32 [1]: how many
     copies found no free page (the child's entry is then -1)."""
-    _start()
+    if _packed is None:
+        _start()
     npages, nbytes, step = _whole_pages(pages)
-    rows, width, ld, n_refs = _pool(tables, lengths, refs)
-    if n_refs != npages:
-        raise QigError(f"refs counts {n_refs} pages, pages has {npages}")
-    if parents.dim() != 1:
-        raise QigError("parents must be a vector")
-    n = parents.shape[0]
+    rows, width, ld = _table(tables)
+    _ints(lengths, rows, "lengths")
+    if _refs(refs) != npages:
+        raise QigError(f"refs counts {refs.shape[0]} pages, pages has {npages}")
+    n = _length(parents, "parents")
     _ints(parents, n, "parents")
     _ints(children, n, "children")
-    missing = _count(missing, "missing", refs.device, stream)
-    scratch = _scratch(npages, n, refs.device, stream)
-    _call(_i._lib.fork_pages, "fork_pages",
-          ("pages", "tables", "lengths", "refs", "parents", "children", "missing", "scratch"),
-          (pages, tables, lengths, refs, parents, children, missing, scratch), stream,
-          (pages.data_ptr(), nbytes, step, tables.data_ptr(), rows, ld, width, lengths.data_ptr(), refs.data_ptr(),
-           npages, page, parents.data_ptr(), children.data_ptr(), n, missing.data_ptr(), scratch.data_ptr()))
+    missing, scratch = _count_and_scratch(missing, "missing", npages, n, refs.device, stream)
+    _call("fork_pages", ("pages", "tables", "lengths", "refs", "parents", "children", "missing"),
+          (pages, tables, lengths, refs, parents, children, missing), stream,
+          pages.data_ptr(), nbytes, step, tables.data_ptr(), rows, ld, width, lengths.data_ptr(), refs.data_ptr(),
+          npages, page, parents.data_ptr(), children.data_ptr(), n, missing.data_ptr(), scratch.data_ptr() + 8)
     return missing
 
 
@@ -338,17 +375,16 @@ def compact_pages(pages, tables, refs, used=None, to=None, stream=None):
     the k-th in use from page U on goes to the k-th free page below U, and refs and
     the tables' entries follow.  Returns int32 [1]: U.  to: None, or an int32 vector
     that receives each page's place after it, for pages that are known elsewhere."""
-    _start()
+    if _packed is None:
+        _start()
     npages, nbytes, step = _whole_pages(pages)
-    rows, width, ld, n_refs = _pool(tables, None, refs)
-    if n_refs != npages:
-        raise QigError(f"refs counts {n_refs} pages, pages has {npages}")
+    rows, width, ld = _table(tables)
+    if _refs(refs) != npages:
+        raise QigError(f"refs counts {refs.shape[0]} pages, pages has {npages}")
     if to is not None:
         _ints(to, npages, "to")
-    used = _count(used, "used", refs.device, stream)
-    scratch = _scratch(npages, 0, refs.device, stream)
-    _call(_i._lib.compact_pages, "compact_pages", ("pages", "tables", "refs", "used", "to", "scratch"),
-          (pages, tables, refs, used, to, scratch), stream,
-          (pages.data_ptr(), nbytes, step, tables.data_ptr(), rows, ld, width, refs.data_ptr(), npages, used.data_ptr(),
-           None if to is None else to.data_ptr(), scratch.data_ptr()))
+    used, scratch = _count_and_scratch(used, "used", npages, 0, refs.device, stream)
+    _call("compact_pages", ("pages", "tables", "refs", "used", "to"), (pages, tables, refs, used, to), stream,
+          pages.data_ptr(), nbytes, step, tables.data_ptr(), rows, ld, width, refs.data_ptr(), npages, used.data_ptr(),
+          0 if to is None else to.data_ptr(), scratch.data_ptr() + 8)
     return used

@@ -111,9 +111,9 @@ def _refuse_devices(names, tensors):
         dev = t.device
 
 
-def _call(fn, what, names, tensors, stream, args):
-    """Check that the tensors (the first of them not None) are on one GPU and
-    call fn there."""
+def _device_of(names, tensors, stream):
+    """Check that the tensors (the first of them not None) are on one GPU:
+    (that GPU, whether it is the current one, the handle of the call's stream)."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev or dev < 0:
@@ -125,7 +125,13 @@ def _call(fn, what, names, tensors, stream, args):
         if on is not None and on.index != dev:
             raise QigError(f"stream is on {on}, the tensors on cuda:{dev}")
         handle = stream.cuda_stream
-    if _device() == dev:
+    return dev, _device() == dev, handle
+
+
+def _call(fn, what, names, tensors, stream, args):
+    """Check the tensors' GPU and call fn there."""
+    dev, here, handle = _device_of(names, tensors, stream)
+    if here:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

@@ -65,6 +65,7 @@ SIGNATURES = {
                                      _vp, _int, _i64, _vp]),
     "combine_experts": (ctypes.c_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _vp, _int, _i64, _vp]),
     "mm_i8_form": (ctypes.c_int, [_i64, _i64, _i64, _i64, _int, _int]),
+    "qig_attend_packed": (ctypes.c_int, [_int, ctypes.c_char_p, _vp]),
     "attend_prompt": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _i64, _i64, _i64,
                                      _i64, _vp, _vp, _i64, _int, ctypes.c_float, _vp, _i64, _i64, _int, _vp]),
     "kv4_page_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),

@@ -2,6 +2,7 @@
 // pages: argument checks, then the launches on the caller's stream.  The full
 // contract is in include/qig.h.
 #include <math.h>
+#include <string.h>
 #include <qig.h>
 
 #include "qig_attend.h"
@@ -232,6 +233,47 @@ int compact_pages(void *pages, int64_t page_bytes, int64_t page_stride, int32_t 
     if (!aligned(used, 4) || !aligned(to, 4) || !aligned(scratch, 8)) return QIG_EALIGN;
     const qig::Pool p = {tables, nullptr, refs, rows, width, ld, npages, 0};
     return rc_from_launch(qig::launch_compact_pages(p, pages, page_bytes, page_stride, used, to, scratch, stream));
+}
+
+int qig_attend_packed(int op, const void *words, hipStream_t stream)
+{
+    int64_t w[24];
+    constexpr int COUNT[] = {24, 20, 20, 24, 7, 9, 10, 16, 12};
+    if (op < 0 || op > 8 || !words) return QIG_EINVAL;
+    memcpy(w, words, COUNT[op] * 8);
+    const auto p = [&](int i) { return reinterpret_cast<void *>(w[i]); };
+    const auto n = [&](int i) { return reinterpret_cast<int32_t *>(w[i]); };
+    const auto small = [&](int i) { return w[i] < INT32_MIN || w[i] > INT32_MAX ? -1 : (int)w[i]; };
+    const auto real = [&](int i) {
+        double d;
+        memcpy(&d, &w[i], 8);
+        return (float)d;
+    };
+    switch (op) {
+    case 0:
+        return attend_prompt(p(0), w[1], w[2], p(3), w[4], w[5], p(6), w[7], w[8], small(9), w[10], w[11], w[12], w[13],
+                             w[14], n(15), n(16), w[17], small(18), real(19), p(20), w[21], w[22], small(23), stream);
+    case 1:
+        return write_kv4(p(0), w[1], w[2], p(3), w[4], w[5], small(6), w[7], w[8], w[9], p(10), w[11], w[12], w[13], n(14),
+                         w[15], w[16], n(17), n(18), w[19], stream);
+    case 2:
+        return read_kv4(p(0), w[1], w[2], p(3), w[4], w[5], small(6), w[7], w[8], w[9], p(10), w[11], w[12], w[13], n(14),
+                        w[15], w[16], n(17), n(18), w[19], stream);
+    case 3:
+        return attend_kv4(p(0), w[1], w[2], small(3), w[4], w[5], w[6], w[7], p(8), w[9], w[10], w[11], n(12), w[13],
+                          w[14], n(15), n(16), w[17], real(18), p(19), w[20], w[21], small(22), p(23), stream);
+    case 4:
+        return copy_pages(p(0), w[1], w[2], w[3], n(4), n(5), w[6], stream);
+    case 5:
+        return free_pages(n(0), w[1], w[2], w[3], n(4), n(5), w[6], n(7), w[8], stream);
+    case 6:
+        return take_pages(n(0), w[1], w[2], w[3], n(4), n(5), w[6], w[7], n(8), p(9), stream);
+    case 7:
+        return fork_pages(p(0), w[1], w[2], n(3), w[4], w[5], w[6], n(7), n(8), w[9], w[10], n(11), n(12), w[13], n(14),
+                          p(15), stream);
+    default:
+        return compact_pages(p(0), w[1], w[2], n(3), w[4], w[5], w[6], n(7), w[8], n(9), n(10), p(11), stream);
+    }
 }
 
 }  // extern "C"
