@@ -77,9 +77,6 @@ __device__ __forceinline__ f32x4 mfma_bf16_16(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
 // The compiler would unpack a block's codes all at once, for 100 registers that three
 // waves a SIMD do not have.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }

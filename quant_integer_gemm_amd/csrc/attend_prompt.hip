@@ -241,6 +241,10 @@ template <> struct Mfma16<T_BF16> {
     typedef bf16x8 type;
     static constexpr uint32_t EXP = 0x7f80;
     static constexpr float UP = 0.0f;
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    }
     static __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(type, a), __builtin_bit_cast(type, b), c, 0, 0,
@@ -251,6 +255,10 @@ template <> struct Mfma16<T_F16> {
     typedef f16x8 type;
     static constexpr uint32_t EXP = 0x7c00;
     static constexpr float UP = 6.0f;
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+    }
     static __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(type, a), __builtin_bit_cast(type, b), c, 0, 0, 0);
@@ -268,7 +276,23 @@ __device__ __forceinline__ u32x2 read_turned(const uint16_t *p)
 template <int D> __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
 template <int D> __device__ __forceinline__ int swz_v(int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
 
-template <int T, int D, int W, int KT>
+// One 1 KB copy of 16 bytes a lane, from base + off to LDS byte address lds + 16 lane.
+// The compiler does not see it: what it brings is read behind landed() and a barrier.
+// s_nop 4 covers the waits behind writes of the scalar base and of M0.
+__device__ __forceinline__ void copy16(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_nop 4\n\t"
+                 "global_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "{m0}"(lds)
+                 : "memory");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// DIRECT: keys and values are copied straight into LDS, which takes rows of d = D
+// elements at multiples of 16 bytes; the lane that copies a unit asks for the one that
+// belongs there.  Others go through registers, unaligned or with zeros up to D.
+template <int T, int D, int W, int KT, bool DIRECT>
 __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs a, int slots, int per)
 {
     typedef elem_t<T> E;
@@ -306,10 +330,32 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
     const int wave_end = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32 + 31)));
     const int wave_full = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32)));
 
-    u32x4 ks[N], vs[N];
-    const auto load = [&](int k0) {
+    u32x4 ks[DIRECT ? 1 : N], vs[DIRECT ? 1 : N];
+    uint32_t k_off[DIRECT ? N : 1], v_off[DIRECT ? N : 1];
+    const auto offsets = [&](int rows) {         // of the copies, keys beyond the last one being that again
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            const int u = i * NT + threadIdx.x, r = u / CH, c = u % CH, at = r < rows ? r : rows - 1;
+            k_off[i] = (uint32_t)at * (uint32_t)a.k.token * 2u + (c ^ swz_k<D>(r)) * 16;
+            v_off[i] = (uint32_t)at * (uint32_t)a.v.token * 2u + (c ^ swz_v<D>(r)) * 16;
+        }
+    };
+    if constexpr (DIRECT) offsets(KT);
+    const uint32_t k_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)&lds_k[0][0];
+    const uint32_t v_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)&lds_v[0][0];
+    const int first_wave = __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);
+    const auto load = [&](int k0, int buf) {
+        if constexpr (DIRECT) {
+            if (t.nk - k0 < KT) offsets(t.nk - k0);
+            const E *kb = kp + (int64_t)k0 * a.k.token, *vb = vp + (int64_t)k0 * a.v.token;
+#pragma unroll
+            for (int i = 0; i < N; ++i) copy16(kb, k_off[i], k_lds + (uint32_t)(buf * KT * CH + i * NT + first_wave) * 16);
+#pragma unroll
+            for (int i = 0; i < N; ++i) copy16(vb, v_off[i], v_lds + (uint32_t)(buf * KT * CH + i * NT + first_wave) * 16);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < (DIRECT ? 0 : N); ++i) {
             const int u = i * NT + threadIdx.x, r = u / CH, c = (u % CH) * 8;
             ks[i] = vs[i] = u32x4{0, 0, 0, 0};
             if (k0 + r < t.nk && c < d) {
@@ -318,24 +364,46 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
             }
         }
     };
-    // returns whether a value was not finite (looked for in steps with masks alone)
-    const auto store = [&](int buf, bool masks) {
+    // Not finite values go (and whether there was one is returned).
+    const auto clean = [&](u32x4 &v) {
         uint32_t bad = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = i * NT + threadIdx.x, r = u / CH, c = u % CH;
-            *reinterpret_cast<u32x4 *>(&lds_k[buf][(r * CH + (c ^ swz_k<D>(r))) * 8]) = ks[i];
-            if (masks) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = vs[i][j], lo = (w & M::EXP) == M::EXP, hi = ((w >> 16) & M::EXP) == M::EXP;
-                    bad |= lo | hi;
-                    vs[i][j] = w & ~((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
-                }
-            }
-            *reinterpret_cast<u32x4 *>(&lds_v[buf][(r * CH + (c ^ swz_v<D>(r))) * 8]) = vs[i];
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = v[j], lo = (w & M::EXP) == M::EXP, hi = ((w >> 16) & M::EXP) == M::EXP;
+            bad |= lo | hi;
+            v[j] = w & ~((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
         }
         return (int)bad;
+    };
+    // The step's keys and values are in LDS for all waves; with masks whether there was a
+    // value that is not finite.
+    const auto arrive = [&](int buf, bool masks) {
+        int bad = 0;
+        if constexpr (DIRECT) {
+            landed();
+            __syncthreads();
+            if (!masks) return 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {        // all in place: no step with masks is before another without
+                u32x4 *at = reinterpret_cast<u32x4 *>(&lds_v[buf][(i * NT + threadIdx.x) * 8]);
+                u32x4 v = *at;
+                if (clean(v)) {
+                    *at = v;
+                    bad = 1;
+                }
+            }
+            return __syncthreads_or(bad);
+        }
+#pragma unroll
+        for (int i = 0; i < (DIRECT ? 0 : N); ++i) {
+            const int u = i * NT + threadIdx.x, r = u / CH, c = u % CH;
+            *reinterpret_cast<u32x4 *>(&lds_k[buf][(r * CH + (c ^ swz_k<D>(r))) * 8]) = ks[i];
+            if (masks) bad |= clean(vs[i]);
+            *reinterpret_cast<u32x4 *>(&lds_v[buf][(r * CH + (c ^ swz_v<D>(r))) * 8]) = vs[i];
+        }
+        if (masks) return __syncthreads_or(bad);
+        __syncthreads();
+        return 0;
     };
     const auto masks_at = [&](int k0) { return k0 + KT > all_full; };
 
@@ -349,14 +417,12 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
 
     int bad = 0;
     if (kend > 0) {
-        load(0);
-        bad = store(0, masks_at(0));
+        load(0, 0);
+        bad = arrive(0, masks_at(0));
     }
-    if (masks_at(0)) bad = __syncthreads_or(bad);
-    else __syncthreads();
     for (int k0 = 0, buf = 0; k0 < kend; k0 += KT, buf ^= 1) {
         const bool more = k0 + KT < kend;
-        if (more) load(k0 + KT);
+        if (more) load(k0 + KT, buf ^ 1);
         if (k0 < wave_end) {
             f32x16 s[KT / 32];
 #pragma unroll
@@ -401,7 +467,7 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
                     f[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[y / 2][8 * (y % 2) + r], a.c, -base));
                     l += f[r];
                 }
-                p[y] = pack16<T>(f);
+                p[y] = u32x4{M::pack(f[0], f[1]), M::pack(f[2], f[3]), M::pack(f[4], f[5]), M::pack(f[6], f[7])};
             }
 #pragma unroll
             for (int y = 0; y < KT / 16; ++y)
@@ -416,9 +482,7 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
                 for (int y = 0; y < KT / 32; ++y) poison<D, E>(o, vp, a.v.token, k0 + 32 * y, t.nk, d, end, n, h);
             }
         }
-        bad = more ? store(buf ^ 1, masks_at(k0 + KT)) : 0;
-        if (masks_at(k0 + KT)) bad = __syncthreads_or(bad);
-        else __syncthreads();
+        bad = more ? arrive(buf ^ 1, masks_at(k0 + KT)) : 0;
     }
     l += __shfl_xor(l, 32);
     if (mine >= rows) return;
@@ -434,18 +498,29 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
         }
 }
 
-template <int T>
-int launch_16(const PromptArgs &a, hipStream_t stream)
+template <int T, int D, int W, int KT>
+int launch_16_dim(const PromptArgs &a, hipStream_t stream)
 {
     const int per = a.hq / a.hkv;
-    constexpr int W = 4;
     const int64_t slots = a.nt * per / (32 * W) + a.nseq;
     const int64_t groups = slots * a.hkv;
     if (slots >= (int64_t(1) << 31) || groups > launch_groups(64 * W)) return -1;
     const dim3 grid((unsigned)groups), block(64 * W);
-    if (a.d <= 64) return launch_kernel(prompt_16<T, 64, W, 64>, grid, block, stream, a, (int)slots, per);
-    if (a.d <= 128) return launch_kernel(prompt_16<T, 128, W, 64>, grid, block, stream, a, (int)slots, per);
-    return launch_kernel(prompt_16<T, 256, W, 32>, grid, block, stream, a, (int)slots, per);
+    const auto direct = [](const Heads &x) {
+        return (((uintptr_t)x.p | (uintptr_t)(x.token * 2) | (uintptr_t)(x.head * 2)) & 15) == 0 &&
+               x.token < (int64_t(1) << 30) / KT;   // offsets of a step's rows: 32 bits
+    };
+    if (a.d == D && direct(a.k) && direct(a.v))
+        return launch_kernel(prompt_16<T, D, W, KT, true>, grid, block, stream, a, (int)slots, per);
+    return launch_kernel(prompt_16<T, D, W, KT, false>, grid, block, stream, a, (int)slots, per);
+}
+
+template <int T>
+int launch_16(const PromptArgs &a, hipStream_t stream)
+{
+    if (a.d <= 64) return launch_16_dim<T, 64, 4, 64>(a, stream);
+    if (a.d <= 128) return launch_16_dim<T, 128, 4, 64>(a, stream);
+    return launch_16_dim<T, 256, 4, 32>(a, stream);
 }
 
 template <int T>
