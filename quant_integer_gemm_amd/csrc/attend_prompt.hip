@@ -77,138 +77,194 @@ __device__ __forceinline__ void poison(f32x16 (&o)[D / 32], const E *vp, int64_t
     for (int x = 0; x < D / 32; ++x) poison_tile<D, E>(o[x], vp, step, k0, nk, 32 * x + n, d, end, h);
 }
 
-// fp32 products on v_mfma_f32_32x32x2_f32 for operands of every type (16-bit ones
-// are widened on their way into LDS).  A wave holds 32 queries, a workgroup 4
-// waves; 32 keys a step.
-//   S^T: lane (n = lane % 32, h = lane / 32) gives key n's and query n's channels
+// A workgroup's tile in the list of (tile, key head) pairs, the longest first.  Of the
+// workgroups that the GPU holds at once each CU gets one of every 256; every other
+// 256 are taken in reverse, so that a CU with a long tile has a short one beside it.
+__device__ __forceinline__ uint32_t place(uint32_t block, uint32_t groups)
+{
+    const uint32_t row = block >> 8;
+    return (row & 1) != 0 && (row + 1) * 256 <= groups ? row * 256 + 255 - (block & 255) : block;
+}
+
+// One 1 KB copy of 16 bytes a lane, from base + off to LDS byte address lds + 16 lane.
+// The compiler does not see it: what it brings is read behind landed() and a barrier.
+// s_nop 4 covers the waits behind writes of the scalar base and of M0.
+__device__ __forceinline__ void copy16(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_nop 4\n\t"
+                 "global_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "{m0}"(lds)
+                 : "memory");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// fp32 operands on v_mfma_f32_32x32x2_f32.  Rows are (query, head of the group) pairs of
+// one key head, heads fastest: all heads that share a key head read one copy of it
+// from LDS, and a tile spans few queries, so that little of its last steps is masked.  A
+// wave holds 32 rows, a workgroup 4 waves; 32 keys a step.
+//   S^T: lane (n = lane % 32, h = lane / 32) gives key n's and row n's channels
 //   8 j + 4 h + i: MFMA i of chunk j then sums channels 8 j + i and 8 j + 4 + i, and
 //   four of them need one 16-byte read.
-//   S^T register r of lane (n, h): query n, key 8 (r / 4) + 4 h + r % 4; MFMA r of
+//   S^T register r of lane (n, h): row n, key 8 (r / 4) + 4 h + r % 4; MFMA r of
 //   O^T sums these two keys.
-template <int D>
-struct F32Lds {
-    static constexpr int KS = D + 4;             // row step of K: 16-byte reads of 8 rows meet in no bank
-    float k[32 * KS];
-    float v[32 * D];
-};
-
-template <int T, int D>
+// LDS: 16-byte unit u of row r of K stands at u ^ (r & 15) (rows of 256 bytes), so that 16
+// lanes reading one unit of 16 rows meet in no bank, and of V at u ^ 8 (r / 4 & 1), so
+// that the two keys of a read do not.
+// DIRECT: both are copied straight into LDS, which takes rows of d = D elements at
+// multiples of 16 bytes; others go through registers.
+template <int D, bool DIRECT>
 __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a, int slots, int per)
 {
-    typedef elem_t<T> E;
-    __shared__ F32Lds<D> lds;
-    constexpr int V = VEC<T>, CH = D / V;        // elements and units of 16 bytes in a row
-    const int head = blockIdx.x % a.hq;
+    constexpr int CH = D / 4, N = 32 * CH / 256, BM = 128;   // 16-byte units of a row; of a thread
+    __shared__ __align__(16) float lds_k[2][32 * D], lds_v[2][32 * D];
+    const uint32_t work = place(blockIdx.x, gridDim.x);
+    const int kvh = (int)(work % (uint32_t)a.hkv);
     Tile t;
-    if (!find_rows<128>(a, slots - 1 - (int)(blockIdx.x / a.hq), 1, t)) return;
-    const int first = (int)t.row0;
+    if (!find_rows<BM>(a, slots - 1 - (int)(work / (uint32_t)a.hkv), per, t)) return;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
-    const int kvh = head / per, d = a.d;
-    const E *kp = static_cast<const E *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
-    const E *vp = static_cast<const E *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
+    const int d = a.d;
+    const float *kp = static_cast<const float *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
+    const float *vp = static_cast<const float *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
 
-    const int mine = first + wave * 32 + n;    // this lane's query in its sequence
-    const int row = mine < t.nq ? mine : t.nq - 1;
-    const E *qp = static_cast<const E *>(a.q.p) + (int64_t)(t.q0 + row) * a.q.token + (int64_t)head * a.q.head;
-    float q[D / 2];
+    const int64_t rows = (int64_t)t.nq * per;
+    const int64_t mine = t.row0 + wave * 32 + n;
+    const int64_t row = mine < rows ? mine : rows - 1;
+    const int query = (int)(row / per), head = kvh * per + (int)(row % per);
+    const float *qp = static_cast<const float *>(a.q.p) + (int64_t)(t.q0 + query) * a.q.token + (int64_t)head * a.q.head;
+    f32x4 q[D / 8];
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = 8 * j + 4 * h + i;
-            q[4 * j + i] = c < d ? (float)qp[c] : 0.0f;
-        }
+    for (int j = 0; j < D / 8; ++j) {
+        const int c = 8 * j + 4 * h;
+        q[j] = c < d ? __builtin_bit_cast(f32x4, load16<T_F32>(qp + c)) : f32x4(0.0f);
+    }
 
-    // the keys that this lane's, its wave's and its workgroup's queries see
+    // the keys that this lane's, its wave's and its workgroup's rows see
     const int off = t.nk - t.nq;
-    const auto end_of = [&](int query) {
-        const int e = a.causal ? off + query + 1 : t.nk;
+    const auto end_of = [&](int i) {
+        const int e = a.causal ? off + i + 1 : t.nk;
         return e < 0 ? 0 : e > t.nk ? t.nk : e;
     };
-    const int end = end_of(row);
-    const int last = first + 127 < t.nq ? first + 127 : t.nq - 1;
-    const int kend = end_of(last);
-    const int wave_last = first + wave * 32 + 31 < t.nq ? first + wave * 32 + 31 : t.nq - 1;
-    const int wave_end = end_of(wave_last), wave_full = end_of(first + wave * 32 < t.nq ? first + wave * 32 : t.nq - 1);
+    const auto query_of = [&](int64_t r) { return (int)((r < rows ? r : rows - 1) / per); };
+    const int end = end_of(query);
+    const int kend = end_of(query_of(t.row0 + BM - 1)), all_full = end_of(query_of(t.row0));
+    const int wave_end = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32 + 31)));
+    const int wave_full = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32)));
+    const auto masks_at = [&](int k0) { return k0 + 32 > all_full; };
+    const auto at_k = [](int r, int c) { return r * CH + (c ^ (r & 15)); };
+    const auto at_v = [](int r, int c) { return r * CH + (c ^ (r & 4) << 1); };
+
+    uint32_t k_off[DIRECT ? N : 1], v_off[DIRECT ? N : 1];
+    const auto offsets = [&](int keys) {           // of the copies, keys beyond the last one being that again
+#pragma unroll
+        for (int i = 0; i < (DIRECT ? N : 0); ++i) {
+            const int u = i * 256 + threadIdx.x, r = u / CH, c = u % CH, at = r < keys ? r : keys - 1;
+            k_off[i] = (uint32_t)at * (uint32_t)a.k.token * 4u + (c ^ (r & 15)) * 16;
+            v_off[i] = (uint32_t)at * (uint32_t)a.v.token * 4u + (c ^ (r & 4) << 1) * 16;
+        }
+    };
+    offsets(32);
+    const uint32_t k_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float *)&lds_k[0][0];
+    const uint32_t v_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float *)&lds_v[0][0];
+    const int first_wave = __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);
+    const auto load = [&](int k0, int buf) {
+        if constexpr (DIRECT) {
+            if (t.nk - k0 < 32) offsets(t.nk - k0);
+            const float *kb = kp + (int64_t)k0 * a.k.token, *vb = vp + (int64_t)k0 * a.v.token;
+#pragma unroll
+            for (int i = 0; i < N; ++i) copy16(kb, k_off[i], k_lds + (uint32_t)(buf * 32 * CH + i * 256 + first_wave) * 16);
+#pragma unroll
+            for (int i = 0; i < N; ++i) copy16(vb, v_off[i], v_lds + (uint32_t)(buf * 32 * CH + i * 256 + first_wave) * 16);
+        } else {
+#pragma unroll 2
+            for (int i = 0; i < N; ++i) {
+                const int u = i * 256 + threadIdx.x, r = u / CH, c = u % CH;
+                u32x4 kv = {0, 0, 0, 0}, vv = kv;
+                if (k0 + r < t.nk && 4 * c < d) {
+                    kv = load16<T_F32>(kp + (int64_t)(k0 + r) * a.k.token + 4 * c);
+                    vv = load16<T_F32>(vp + (int64_t)(k0 + r) * a.v.token + 4 * c);
+                }
+                reinterpret_cast<u32x4 *>(lds_k[buf])[at_k(r, c)] = kv;
+                reinterpret_cast<u32x4 *>(lds_v[buf])[at_v(r, c)] = vv;
+            }
+        }
+    };
+    // The step's keys and values are in LDS for all waves; with masks whether there was a
+    // value that is not finite.
+    const auto arrive = [&](int buf, bool masks) {
+        if constexpr (DIRECT) landed();
+        __syncthreads();
+        if (!masks) return 0;
+        int bad = 0;
+        for (int i = threadIdx.x; i < 32 * D; i += 256) {
+            if (!finite(lds_v[buf][i])) {
+                lds_v[buf][i] = 0.0f;
+                bad = 1;
+            }
+        }
+        return __syncthreads_or(bad);
+    };
 
     f32x16 o[D / 32];
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
     float m = -INFINITY, l = 0.0f;
-
-    const int all_full = end_of(first);
-    for (int k0 = 0; k0 < kend; k0 += 32) {
-        const bool masks = k0 + 32 > all_full;   // some query of the workgroup does not see some key
-        int bad = 0;
-        __syncthreads();
-        for (int u = threadIdx.x; u < 32 * CH; u += 256) {
-            const int r = u / CH, c = (u % CH) * V;
-            float kf[V], vf[V];
-            if (k0 + r < t.nk && c < d) {
-                const int64_t key = k0 + r;
-                unpack16<T>(load16<T>(kp + key * a.k.token + c), kf);
-                unpack16<T>(load16<T>(vp + key * a.v.token + c), vf);
-            } else {
+    int bad = 0;
+    if (kend > 0) {
+        load(0, 0);
+        bad = arrive(0, masks_at(0));
+    }
+    for (int k0 = 0, buf = 0; k0 < kend; k0 += 32, buf ^= 1) {
+        const bool more = k0 + 32 < kend;
+        if (more) load(k0 + 32, buf ^ 1);
+        if (k0 < wave_end) {
+            f32x16 s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) kf[i] = vf[i] = 0.0f;
+            for (int j = 0; j < D / 8; ++j) {
+                const f32x4 k4 = reinterpret_cast<const f32x4 *>(lds_k[buf])[at_k(n, 2 * j + h)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_32x32x2f32(k4[i], q[j][i], s, 0, 0, 0);
             }
-            if (masks) {
+            if (k0 + 32 > wave_full) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const bool fine = finite(vf[i]);
-                    bad |= !fine;
-                    vf[i] = fine ? vf[i] : 0.0f;
+                for (int r = 0; r < 16; ++r)
+                    if (k0 + mfma_row(r, h) >= end) s[r] = -INFINITY;
+            }
+            float top = s[0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float mn = fmaxf(m, top * a.c);
+            const float ref = mn == -INFINITY ? 0.0f : mn;
+            const float fix = __builtin_amdgcn_exp2f(m - ref);
+            m = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.c, -ref));
+                sum += s[r];
+            }
+            l = l * fix + sum;
+            if (__any(fix != 1.0f)) {
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) o[x] *= fix;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const int key = mfma_row(r, h);
+                    const float v = lds_v[buf][at_v(key, 8 * x + (n >> 2)) * 4 + (n & 3)];
+                    o[x] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, s[r], o[x], 0, 0, 0);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                lds.k[r * F32Lds<D>::KS + c + i] = kf[i];
-                lds.v[r * D + c + i] = vf[i];
-            }
+            if (bad) poison<D, float>(o, vp, a.v.token, k0, t.nk, d, end, n, h);
         }
-        if (masks) bad = __syncthreads_or(bad);
-        else __syncthreads();
-        if (k0 >= wave_end) continue;
-        f32x16 s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            const f32x4 k4 = *reinterpret_cast<const f32x4 *>(&lds.k[n * F32Lds<D>::KS + 8 * j + 4 * h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_32x32x2f32(k4[i], q[4 * j + i], s, 0, 0, 0);
-        }
-        if (k0 + 32 > wave_full) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (k0 + mfma_row(r, h) >= end) s[r] = -INFINITY;
-        }
-        float top = s[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top * a.c);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float fix = __builtin_amdgcn_exp2f(m - ref);
-        m = mn;
-        float sum = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.c, -ref));
-            sum += s[r];
-        }
-        l = l * fix + sum;
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            o[x] *= fix;
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                o[x] = __builtin_amdgcn_mfma_f32_32x32x2f32(lds.v[mfma_row(r, h) * D + 32 * x + n], s[r], o[x], 0, 0, 0);
-        }
-        if (bad) poison<D, E>(o, vp, a.v.token, k0, t.nk, d, end, n, h);
+        bad = more ? arrive(buf ^ 1, masks_at(k0 + 32)) : 0;
     }
     l += __shfl_xor(l, 32);
-    if (mine >= t.nq) return;
+    if (mine >= rows) return;
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    const int64_t at = (int64_t)(t.q0 + mine) * a.y_token + (int64_t)head * a.y_head;
+    const int64_t at = (int64_t)(t.q0 + query) * a.y_token + (int64_t)head * a.y_head;
 #pragma unroll
     for (int x = 0; x < D / 32; ++x)
 #pragma unroll
@@ -276,19 +332,6 @@ __device__ __forceinline__ u32x2 read_turned(const uint16_t *p)
 template <int D> __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
 template <int D> __device__ __forceinline__ int swz_v(int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
 
-// One 1 KB copy of 16 bytes a lane, from base + off to LDS byte address lds + 16 lane.
-// The compiler does not see it: what it brings is read behind landed() and a barrier.
-// s_nop 4 covers the waits behind writes of the scalar base and of M0.
-__device__ __forceinline__ void copy16(const void *base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_nop 4\n\t"
-                 "global_load_lds_dwordx4 %0, %1"
-                 :
-                 : "v"(off), "s"(base), "{m0}"(lds)
-                 : "memory");
-}
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
 // DIRECT: keys and values are copied straight into LDS, which takes rows of d = D
 // elements at multiples of 16 bytes; the lane that copies a unit asks for the one that
 // belongs there.  Others go through registers, unaligned or with zeros up to D.
@@ -299,9 +342,10 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
     typedef Mfma16<T> M;
     constexpr int NT = 64 * W, BM = 32 * W, CH = D / 8, N = KT * CH / NT;
     __shared__ __align__(16) uint16_t lds_k[2][KT * D], lds_v[2][KT * D];
-    const int kvh = blockIdx.x % a.hkv;
+    const uint32_t work = place(blockIdx.x, gridDim.x);
+    const int kvh = (int)(work % (uint32_t)a.hkv);
     Tile t;
-    if (!find_rows<BM>(a, slots - 1 - (int)(blockIdx.x / a.hkv), per, t)) return;
+    if (!find_rows<BM>(a, slots - 1 - (int)(work / (uint32_t)a.hkv), per, t)) return;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
     const int d = a.d;
     const E *kp = static_cast<const E *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
@@ -426,10 +470,11 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
         if (k0 < wave_end) {
             f32x16 s[KT / 32];
 #pragma unroll
-            for (int y = 0; y < KT / 32; ++y) {
-                s[y] = 0.0f;
+            for (int y = 0; y < KT / 32; ++y) s[y] = 0.0f;
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
+            for (int x = 0; x < D / 16; ++x) {     // two sums in turn: none waits for its own last product
+#pragma unroll
+                for (int y = 0; y < KT / 32; ++y) {
                     const u32x4 kv = *reinterpret_cast<const u32x4 *>(
                         &lds_k[buf][((y * 32 + n) * CH + ((2 * x + h) ^ swz_k<D>(n))) * 8]);
                     s[y] = M::mul(kv, q[x], s[y]);
@@ -498,21 +543,32 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
         }
 }
 
+// Whether the rows of x can be copied straight into LDS, `step` keys at a time: 16-byte
+// units, and offsets of a step's rows in 32 bits.
+bool direct(const Heads &x, int64_t elem, int step)
+{
+    return (((uintptr_t)x.p | (uintptr_t)(x.token * elem) | (uintptr_t)(x.head * elem)) & 15) == 0 &&
+           x.token * elem < (int64_t(1) << 31) / step;
+}
+
+// kernel(grid, slots, rows a query) for tiles of bm rows.
+template <typename F>
+int by_tiles(const PromptArgs &a, int bm, int threads, F launch)
+{
+    const int per = a.hq / a.hkv;
+    const int64_t slots = a.nt * per / bm + a.nseq, groups = slots * a.hkv;
+    if (slots >= (int64_t(1) << 31) || groups > launch_groups(threads)) return -1;
+    return launch(dim3((unsigned)groups), (int)slots, per);
+}
+
 template <int T, int D, int W, int KT>
 int launch_16_dim(const PromptArgs &a, hipStream_t stream)
 {
-    const int per = a.hq / a.hkv;
-    const int64_t slots = a.nt * per / (32 * W) + a.nseq;
-    const int64_t groups = slots * a.hkv;
-    if (slots >= (int64_t(1) << 31) || groups > launch_groups(64 * W)) return -1;
-    const dim3 grid((unsigned)groups), block(64 * W);
-    const auto direct = [](const Heads &x) {
-        return (((uintptr_t)x.p | (uintptr_t)(x.token * 2) | (uintptr_t)(x.head * 2)) & 15) == 0 &&
-               x.token < (int64_t(1) << 30) / KT;   // offsets of a step's rows: 32 bits
-    };
-    if (a.d == D && direct(a.k) && direct(a.v))
-        return launch_kernel(prompt_16<T, D, W, KT, true>, grid, block, stream, a, (int)slots, per);
-    return launch_kernel(prompt_16<T, D, W, KT, false>, grid, block, stream, a, (int)slots, per);
+    return by_tiles(a, 32 * W, 64 * W, [&](dim3 grid, int slots, int per) {
+        if (a.d == D && direct(a.k, 2, KT) && direct(a.v, 2, KT))
+            return launch_kernel(prompt_16<T, D, W, KT, true>, grid, dim3(64 * W), stream, a, slots, per);
+        return launch_kernel(prompt_16<T, D, W, KT, false>, grid, dim3(64 * W), stream, a, slots, per);
+    });
 }
 
 template <int T>
@@ -523,24 +579,26 @@ int launch_16(const PromptArgs &a, hipStream_t stream)
     return launch_16_dim<T, 256, 4, 32>(a, stream);
 }
 
-template <int T>
+template <int D>
+int launch_f32_dim(const PromptArgs &a, hipStream_t stream)
+{
+    return by_tiles(a, 128, 256, [&](dim3 grid, int slots, int per) {
+        if (a.d == D && direct(a.k, 4, 32) && direct(a.v, 4, 32))
+            return launch_kernel(prompt_f32<D, true>, grid, dim3(256), stream, a, slots, per);
+        return launch_kernel(prompt_f32<D, false>, grid, dim3(256), stream, a, slots, per);
+    });
+}
+
 int launch_f32(const PromptArgs &a, hipStream_t stream)
 {
-    const int64_t slots = a.nt / 128 + a.nseq;
-    const int64_t groups = slots * a.hq;
-    if (slots >= (int64_t(1) << 31) || groups > launch_groups(256)) return -1;
-    const dim3 grid((unsigned)groups), block(256);
-    const int per = a.hq / a.hkv;
-    if (a.d <= 64) return launch_kernel(prompt_f32<T, 64>, grid, block, stream, a, (int)slots, per);
-    if (a.d <= 128) return launch_kernel(prompt_f32<T, 128>, grid, block, stream, a, (int)slots, per);
-    return launch_kernel(prompt_f32<T, 256>, grid, block, stream, a, (int)slots, per);
+    return a.d <= 64 ? launch_f32_dim<64>(a, stream) : a.d <= 128 ? launch_f32_dim<128>(a, stream) : launch_f32_dim<256>(a, stream);
 }
 
 }  // namespace
 
 int launch_attend_prompt(const PromptArgs &a, hipStream_t stream)
 {
-    if (a.type == T_F32) return launch_f32<T_F32>(a, stream);
+    if (a.type == T_F32) return launch_f32(a, stream);
     if (a.type == T_BF16) return launch_16<T_BF16>(a, stream);
     return launch_16<T_F16>(a, stream);
 }
