@@ -550,8 +550,8 @@ int combine_experts(const void *h, int htype, int64_t ldh, const float *w,
  *   y      [nt][hq][d] elements of ytype; rows outside of every sequence are left as
  *          they were; rows must not overlap
  * Errors: QIG_EINVAL (unknown type, nt, nk or nseq < 0 or >= 2^31 - 1, heads, d, a
- *         negative stride, causal not 0 or 1, scale, or more tiles than a launch
- *         holds: nt / 128 + nseq tiles of queries by hq, at most 2^23),
+ *         negative stride, causal not 0 or 1, scale, nt * hq / hkv >= 2^31, or more
+ *         tiles than a launch holds: nt * hq / hkv / 128 + nseq by hkv, at most 2^24),
  *         QIG_EALIGN, QIG_ELAUNCH.
  */
 int attend_prompt(const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token, int64_t k_head,

@@ -25,7 +25,7 @@ namespace {
 struct Tile {
     int q0, nq;      // first packed query of the sequence, queries
     int k0, nk;
-    int64_t row0;    // first (query, head) row of the tile in its sequence
+    int rows, row0;  // (query, head) rows of the sequence, the first one of the tile
 };
 
 template <int BM>
@@ -33,7 +33,7 @@ __device__ __forceinline__ bool find_rows(const PromptArgs &a, int slot, int per
 {
     const int32_t *starts = a.starts;
     const int64_t nt = a.nt;
-    const auto first_slot = [&](int s) { return (int64_t)held(starts[s], nt) * per / BM + s; };
+    const auto first_slot = [&](int s) { return held(starts[s], nt) * per / BM + s; };   // nt * per < 2^31
     const int i = __builtin_amdgcn_readfirstlane(
         count_first((int)a.nseq, [&](int s) { return first_slot(s) <= slot; }) - 1);
     if (i < 0) return false;
@@ -42,8 +42,10 @@ __device__ __forceinline__ bool find_rows(const PromptArgs &a, int slot, int per
     t.k0 = held(a.k_starts[i], a.nk);
     t.nk = held(a.k_starts[i + 1], a.nk) - t.k0;
     if (t.nk < 0) t.nk = 0;
-    t.row0 = (slot - first_slot(i)) * BM;
-    return t.row0 >= 0 && t.row0 < (int64_t)t.nq * per;   // below 0: starts that decrease
+    t.rows = t.nq * per;
+    const int64_t row0 = (int64_t)(slot - first_slot(i)) * BM;
+    t.row0 = (int)row0;
+    return row0 >= 0 && row0 < t.rows;   // below 0: starts that decrease
 }
 
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < INFINITY; }
@@ -127,10 +129,9 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
     const float *kp = static_cast<const float *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
     const float *vp = static_cast<const float *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
 
-    const int64_t rows = (int64_t)t.nq * per;
-    const int64_t mine = t.row0 + wave * 32 + n;
-    const int64_t row = mine < rows ? mine : rows - 1;
-    const int query = (int)(row / per), head = kvh * per + (int)(row % per);
+    const uint32_t rows = t.rows, mine = t.row0 + wave * 32 + n;
+    const auto query_of = [&](uint32_t r) { return (int)((r < rows ? r : rows - 1) / (uint32_t)per); };
+    const int query = query_of(mine), head = kvh * per + (int)((mine < rows ? mine : rows - 1) - (uint32_t)query * per);
     const float *qp = static_cast<const float *>(a.q.p) + (int64_t)(t.q0 + query) * a.q.token + (int64_t)head * a.q.head;
     f32x4 q[D / 8];
 #pragma unroll
@@ -145,7 +146,6 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
         const int e = a.causal ? off + i + 1 : t.nk;
         return e < 0 ? 0 : e > t.nk ? t.nk : e;
     };
-    const auto query_of = [&](int64_t r) { return (int)((r < rows ? r : rows - 1) / per); };
     const int end = end_of(query);
     const int kend = end_of(query_of(t.row0 + BM - 1)), all_full = end_of(query_of(t.row0));
     const int wave_end = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32 + 31)));
@@ -351,10 +351,9 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
     const E *kp = static_cast<const E *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
     const E *vp = static_cast<const E *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
 
-    const int64_t rows = (int64_t)t.nq * per;
-    const int64_t mine = t.row0 + wave * 32 + n;
-    const int64_t row = mine < rows ? mine : rows - 1;
-    const int query = (int)(row / per), head = kvh * per + (int)(row % per);
+    const uint32_t rows = t.rows, mine = t.row0 + wave * 32 + n;
+    const auto query_of = [&](uint32_t r) { return (int)((r < rows ? r : rows - 1) / (uint32_t)per); };
+    const int query = query_of(mine), head = kvh * per + (int)((mine < rows ? mine : rows - 1) - (uint32_t)query * per);
     const E *qp = static_cast<const E *>(a.q.p) + (int64_t)(t.q0 + query) * a.q.token + (int64_t)head * a.q.head;
     u32x4 q[D / 16];
 #pragma unroll
@@ -368,7 +367,6 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
         const int e = a.causal ? off + i + 1 : t.nk;
         return e < 0 ? 0 : e > t.nk ? t.nk : e;
     };
-    const auto query_of = [&](int64_t r) { return (int)((r < rows ? r : rows - 1) / per); };
     const int end = end_of(query);
     const int kend = end_of(query_of(t.row0 + BM - 1)), all_full = end_of(query_of(t.row0));
     const int wave_end = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32 + 31)));
@@ -557,7 +555,7 @@ int by_tiles(const PromptArgs &a, int bm, int threads, F launch)
 {
     const int per = a.hq / a.hkv;
     const int64_t slots = a.nt * per / bm + a.nseq, groups = slots * a.hkv;
-    if (slots >= (int64_t(1) << 31) || groups > launch_groups(threads)) return -1;
+    if (a.nt * per >= (int64_t(1) << 31) || slots >= (int64_t(1) << 31) || groups > launch_groups(threads)) return -1;
     return launch(dim3((unsigned)groups), (int)slots, per);
 }
 
