@@ -30,8 +30,8 @@
 //
 // The work, 32 tokens by 16 rows by key head, is split evenly over the workgroups
 // whatever the sequences' lengths: they all sum the lengths and take equal runs of
-// the list of all blocks.  What does not cover a sequence's row goes to the workspace
-// and is joined by a second launch.
+// the list of all blocks.  What does not cover a sequence's row goes to the workspace,
+// and the last workgroup to leave a piece of a row there joins them, in the list's order.
 #include <utility>
 
 #include "qig_attend_device.h"
@@ -41,6 +41,7 @@ namespace qig {
 namespace {
 
 constexpr int WAVES = 4, ROWS = 16, CUS = 256;
+constexpr int LEAST = 8;       // blocks of a run: two a wave, so that a long sequence alone is in fewer pieces
 constexpr float LAZY = 8.0f;   // the reference follows the maximum when it is this far behind
 
 template <int... I, typename F>
@@ -121,8 +122,6 @@ __device__ __forceinline__ float base_of(float ref) { return ref == -INFINITY ? 
 // What a piece of a row leaves in the workspace: m and l of its 16 rows, then O.
 template <int D> constexpr int SLOT = 2 * ROWS + ROWS * D;
 
-struct Header { int seq, head, tile, pieces; };   // the row whose first piece a workgroup has, if it has more
-
 struct Job {
     Kv4 c;
     Kv4Attend a;
@@ -131,7 +130,7 @@ struct Job {
     int room;           // tokens that a row of the table has pages for
     int groups;         // workgroups
     float *slots;       // [groups][2][SLOT]
-    Header *headers;    // [groups]
+    uint32_t *arrived;  // [groups]: pieces of the row that begins in a workgroup's run; 0 before and after a call
 };
 
 // A sequence's place in the list of all blocks.
@@ -233,9 +232,115 @@ __device__ __forceinline__ void load_values(const uint8_t *block, int lane, Valu
     load_words<Q>(block + 36 * D + lane * (4 * Q), v.s);
 }
 
+// Pieces cross XCDs, whose L2s are not coherent: agent-scope accesses, two floats each.
+__device__ __forceinline__ void put2(float *p, float a, float b)
+{
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), __builtin_bit_cast(uint64_t, f32x2{a, b}), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 get2(const float *p)
+{
+    return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED,
+                                                       __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// A tile whose first piece is workgroup g's last one (slot 1), the others being the
+// first ones of the next workgroups (slot 0), by the whole workgroup: 16 threads a row
+// form the maximum and the pieces' factors, 64 pieces at a time, then a wave sums its rows,
+// two at once and 8 pieces of each on their way.  fix: 64 x 16 floats of LDS.
+template <int D>
+__device__ __forceinline__ void join_rows(const Job &j, uint32_t g, int pieces, const Seq &q, int head, int tile, int rows,
+                                          float *fix, float *total)
+{
+    constexpr int C = D < 128 ? 1 : D / 128;       // pairs of channels a lane
+    const auto slot_of = [&](int p) { return j.slots + (int64_t)(p == 0 ? 2 * g + 1 : 2 * (g + p)) * SLOT<D>; };
+    const int here = rows - tile * ROWS < ROWS ? rows - tile * ROWS : ROWS;
+    const int row = threadIdx.x >> 4, sub = threadIdx.x & 15;
+    f32x2 ml[4];
+    float M = -INFINITY, lsum = 0.0f;
+    for (int p0 = 0; p0 < pieces; p0 += 64) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 16 * i + sub;
+            ml[i] = p < pieces && row < here ? get2(slot_of(p) + 2 * row) : f32x2{-INFINITY, 0.0f};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) M = fmaxf(M, ml[i][0]);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+    const float base = base_of(M);
+
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int at = 2 * ROWS + (D < 128 ? (lane & 31) * 2 : lane * 2 * C);
+    f32x2 v[ROWS / WAVES][C];
+#pragma unroll
+    for (int r = 0; r < ROWS / WAVES; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[r][c] = 0.0f;
+    for (int p0 = 0; p0 < pieces; p0 += 64) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 16 * i + sub;
+            if (pieces > 64) ml[i] = p < pieces && row < here ? get2(slot_of(p) + 2 * row) : f32x2{-INFINITY, 0.0f};
+            const float f = __builtin_amdgcn_exp2f(ml[i][0] - base);
+            lsum += ml[i][1] * f;
+            fix[(16 * i + sub) * ROWS + row] = f;
+        }
+        __syncthreads();
+        const int n = pieces - p0 < 64 ? pieces - p0 : 64;
+#pragma unroll
+        for (int r = 0; r < ROWS / WAVES; r += 2) {
+            const int r0 = wave + r * WAVES, r1 = r0 + WAVES;
+            if (r0 >= here) break;
+            constexpr int AHEAD = 8 / C;
+            for (int p = 0; p < n; p += AHEAD) {
+                f32x2 w[2][AHEAD][C];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const float *slot = slot_of(p0 + p + i) + at + 2 * c;
+                        w[0][i][c] = p + i < n ? get2(slot + r0 * D) : f32x2(0.0f);
+                        w[1][i][c] = p + i < n && r1 < here ? get2(slot + r1 * D) : f32x2(0.0f);
+                    }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (p + i >= n) break;
+                    const float f0 = fix[(p + i) * ROWS + r0], f1 = fix[(p + i) * ROWS + r1];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        v[r][c] += w[0][i][c] * f0;
+                        v[r + 1][c] += w[1][i][c] * f1;
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) lsum += __shfl_xor(lsum, o);
+    if (sub == 0) total[row] = lsum;
+    __syncthreads();
+    if (D < 128 && lane >= 32) return;
+#pragma unroll
+    for (int r = 0; r < ROWS / WAVES; ++r) {
+        const int mine = wave + r * WAVES;
+        if (mine >= here) break;
+        const float l = total[mine], inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const int R = tile * ROWS + mine, i = R / j.per;
+        const int64_t y = (int64_t)(q.q0 + i) * j.a.y_token + (int64_t)(head * j.per + (R - i * j.per)) * j.a.y_head;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            store1(j.a.y, j.a.ytype, y + lane * 2 * C + 2 * c, v[r][c][0] * inv);
+            store1(j.a.y, j.a.ytype, y + lane * 2 * C + 2 * c + 1, v[r][c][1] * inv);
+        }
+    }
+}
+
 // Workgroups that a CU holds at once (by their registers); with a workspace there are
 // as many in all, each with its share of the list, so that none waits for another's end.
-template <int D, int QP, int PP> constexpr int RESIDENT = D == 256 ? 1 : D == 64 ? 4 : QP + PP == 4 ? 2 : 3;
+template <int D, int QP, int PP> constexpr int RESIDENT = D == 256 ? 1 : QP == 2 ? 2 : 3;
 
 template <int T, int D, int QP, int PP>
 __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
@@ -244,45 +349,62 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
     constexpr int G = D / 32, Q = G / 2, TILES = D / 16;
     __shared__ float joined[WAVES][ROWS * D];
     __shared__ float stats[WAVES][2][ROWS];
-    __shared__ uint32_t tmp[4], found[2];
+    __shared__ uint32_t tmp[4], found[2], arrivals;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, h = lane >> 4;
     const int nseq = (int)j.c.nseq;
 
     // the list's length, and where this workgroup's run of it begins
-    uint32_t mine = 0, total, before;
-    for (int s = threadIdx.x; s < nseq; s += 256) mine += units(j, get_seq(j, s));
-    before = scan(mine, tmp, total);
-    uint32_t size = (total + j.groups - 1) / j.groups;
-    if (j.split && size < WAVES) size = WAVES;
-    if (size < 1) size = 1;
-    uint32_t at = blockIdx.x * size;
-    const uint32_t end = at + size < total ? at + size : total;
-    if (threadIdx.x == 0 && j.split) j.headers[blockIdx.x].pieces = 0;
-    if (at >= end) return;
-    if (nseq <= 256) {
-        if (at >= before && at < before + mine) {
-            found[0] = threadIdx.x;
-            found[1] = before;
+    uint32_t total, size, at, end, seq_at;
+    int s;
+    Seq q;
+    const auto run_of = [&]() {
+        size = (total + j.groups - 1) / j.groups;
+        if (j.split && size < LEAST) size = LEAST;
+        if (size < 1) size = 1;
+        at = blockIdx.x * size;
+        end = at + size < total ? at + size : total;
+    };
+    if (nseq <= 64) {                               // each wave sums them by itself
+        Seq mine = {};
+        if (lane < nseq) mine = get_seq(j, lane);
+        const uint32_t u = lane < nseq ? units(j, mine) : 0;
+        uint32_t sum = u;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t up = __shfl_up(sum, o);
+            if (lane >= o) sum += up;
         }
+        total = __builtin_amdgcn_readlane(sum, 63);
+        run_of();
+        if (at >= end) return;
+        s = __popcll(__ballot(sum <= at));           // sequences that end before it
+        const auto of = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, s); };
+        seq_at = of(sum - u);
+        q = {(int)of(mine.q0), (int)of(mine.n), (int)of(mine.length), (int)of(mine.keys), of(mine.blocks), of(mine.tiles)};
     } else {
+        uint32_t mine = 0;
+        for (int i = threadIdx.x; i < nseq; i += 256) mine += units(j, get_seq(j, i));
+        scan(mine, tmp, total);
+        run_of();
+        if (at >= end) return;
         uint32_t ahead = 0;
         for (int s0 = 0; s0 < nseq; s0 += 256) {
-            const int s = s0 + threadIdx.x;
-            const uint32_t u = s < nseq ? units(j, get_seq(j, s)) : 0;
+            const int i = s0 + threadIdx.x;
+            const uint32_t u = i < nseq ? units(j, get_seq(j, i)) : 0;
             uint32_t sum;
-            before = ahead + scan(u, tmp, sum);
+            const uint32_t before = ahead + scan(u, tmp, sum);
             if (at >= before && at < before + u) {
-                found[0] = s;
+                found[0] = i;
                 found[1] = before;
             }
             ahead += sum;
             if (ahead > at) break;
         }
+        __syncthreads();
+        s = __builtin_amdgcn_readfirstlane(found[0]);
+        seq_at = __builtin_amdgcn_readfirstlane(found[1]);
+        q = get_seq(j, s);
     }
-    __syncthreads();
-    int s = __builtin_amdgcn_readfirstlane(found[0]);
-    uint32_t seq_at = __builtin_amdgcn_readfirstlane(found[1]);
-    Seq q = get_seq(j, s);
 
     while (at < end) {
         while (at >= seq_at + units(j, q)) {
@@ -581,9 +703,11 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
             *reinterpret_cast<f32x4 *>(&joined[wave][l * D + 16 * n + 4 * h]) = o[n] * fix;
         __syncthreads();
         const bool whole = entries == q.blocks;
+        // this piece is the row's first one in its workgroup's second slot, or in the first slot a later one
         float *slot = j.slots + (int64_t)(blockIdx.x * 2 + (first == 0 ? 1 : 0)) * SLOT<D>;
         for (int x = threadIdx.x * 4; x < ROWS * D; x += 1024) {
-            const int row = x / D;
+            const int row = x / D, Ry = tile * ROWS + row;
+            if (Ry >= rows) break;
             f32x4 v4 = *reinterpret_cast<const f32x4 *>(&joined[0][x]);
 #pragma unroll
             for (int w = 1; w < WAVES; ++w) v4 += *reinterpret_cast<const f32x4 *>(&joined[w][x]);
@@ -594,79 +718,33 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
             for (int w = 0; w < WAVES; ++w)
                 lsum += stats[w][1][row] * __builtin_amdgcn_exp2f(stats[w][0][row] - base_of(M));
             if (whole) {
-                const int Ry = tile * ROWS + row;
-                if (Ry < rows) {
-                    const float inv = lsum != 0.0f ? 1.0f / lsum : 0.0f;
-                    const float f[4] = {v4[0] * inv, v4[1] * inv, v4[2] * inv, v4[3] * inv};
-                    const int i = Ry / j.per;
-                    store4(j.a.y, j.a.ytype, (int64_t)(q.q0 + i) * j.a.y_token +
-                                                 (int64_t)(head * j.per + (Ry - i * j.per)) * j.a.y_head + x % D, f);
-                }
+                const float inv = lsum != 0.0f ? 1.0f / lsum : 0.0f;
+                const float f[4] = {v4[0] * inv, v4[1] * inv, v4[2] * inv, v4[3] * inv};
+                const int i = Ry / j.per;
+                store4(j.a.y, j.a.ytype, (int64_t)(q.q0 + i) * j.a.y_token +
+                                             (int64_t)(head * j.per + (Ry - i * j.per)) * j.a.y_head + x % D, f);
             } else {
-                *reinterpret_cast<f32x4 *>(slot + 2 * ROWS + x) = v4;
-                if (x % D == 0) {
-                    slot[row] = M;
-                    slot[ROWS + row] = lsum;
-                }
+                put2(slot + 2 * ROWS + x, v4[0], v4[1]);
+                put2(slot + 2 * ROWS + x + 2, v4[2], v4[3]);
+                if (x % D == 0) put2(slot + 2 * row, M, lsum);
             }
         }
-        if (!whole && first == 0 && threadIdx.x == 0) {
-            const uint32_t last = (at + q.blocks - 1) / size;        // the workgroup with the row's last piece
-            j.headers[blockIdx.x] = {s, head, tile, (int)(last - blockIdx.x) + 1};
+        if (!whole) {
+            const uint32_t row_at = at - first, owner = row_at / size;
+            const int pieces = (int)((row_at + q.blocks - 1) / size - owner) + 1;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the piece is at the coherence point
+            __syncthreads();
+            if (threadIdx.x == 0)
+                arrivals = __hip_atomic_fetch_add(j.arrived + owner, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (arrivals == (uint32_t)pieces - 1) {
+                join_rows<D>(j, owner, pieces, q, head, tile, rows, &joined[0][0], &stats[0][0][0]);
+                if (threadIdx.x == 0)
+                    __hip_atomic_store(j.arrived + owner, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
         }
         at += entries;
     }
-}
-
-// The rows of more than one piece: the first is workgroup g's last one (slot 1), the
-// others are the first ones of the next workgroups (slot 0).  Four workgroups a
-// header, four rows each: a wave sums a row's pieces, its lanes reading 64 pieces' m
-// and l at once and then D channels of one piece after the other.
-template <int D>
-__global__ __launch_bounds__(256) void kv4_join(Job j)
-{
-    typedef float vec __attribute__((ext_vector_type(D / 64)));
-    const int g = blockIdx.x >> 2, row = (blockIdx.x & 3) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const Header hd = j.headers[g];
-    if (hd.pieces == 0) return;
-    const float *first = j.slots + (int64_t)(g * 2 + 1) * SLOT<D>, *rest = j.slots + (int64_t)(g * 2 + 2) * SLOT<D>;
-    const auto slot_of = [&](int p) { return p == 0 ? first : rest + (int64_t)(p - 1) * (2 * SLOT<D>); };
-    const Seq q = get_seq(j, hd.seq);
-    const int R = hd.tile * ROWS + row;
-    if (R >= q.n * j.per) return;
-    float M = -INFINITY, lsum = 0.0f;
-    for (int p = lane; p < hd.pieces; p += 64) M = fmaxf(M, slot_of(p)[row]);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
-    const float base = base_of(M);
-    vec v = 0.0f;
-    for (int p0 = 0; p0 < hd.pieces; p0 += 64) {
-        float fix = 0.0f;
-        if (p0 + lane < hd.pieces) {
-            const float *slot = slot_of(p0 + lane);
-            fix = __builtin_amdgcn_exp2f(slot[row] - base);
-            lsum += slot[ROWS + row] * fix;
-        }
-        const int n = hd.pieces - p0 < 64 ? hd.pieces - p0 : 64;
-        int p = 0;
-        for (; p + 8 <= n; p += 8) {
-            vec w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = *reinterpret_cast<const vec *>(slot_of(p0 + p + i) + 2 * ROWS + row * D + lane * (D / 64));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v += w[i] * __shfl(fix, p + i);
-        }
-        for (; p < n; ++p)
-            v += *reinterpret_cast<const vec *>(slot_of(p0 + p) + 2 * ROWS + row * D + lane * (D / 64)) * __shfl(fix, p);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) lsum += __shfl_xor(lsum, o);
-    const float inv = lsum != 0.0f ? 1.0f / lsum : 0.0f;
-    const int i = R / j.per;
-    const int64_t at = (int64_t)(q.q0 + i) * j.a.y_token + (int64_t)(hd.head * j.per + (R - i * j.per)) * j.a.y_head;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) store1(j.a.y, j.a.ytype, at + lane * (D / 64) + c, v[c] * inv);
 }
 
 template <int T, int D, int QP, int PP>
@@ -682,19 +760,16 @@ int launch_typed(Job j, hipStream_t stream)
     const int64_t most_blocks = blocks < (int64_t(1) << 26) ? blocks : int64_t(1) << 26;   // of 2^31 tokens
     if (j.a.nt * j.per >= (int64_t(1) << 31) || rows > ((int64_t(1) << 31) - 1) / (j.split ? most_blocks : 1)) return -1;
     if (j.split) {
-        const int64_t each = 2 * SLOT<D> * 4 + (int64_t)sizeof(Header);
-        int64_t most = ATTEND_WS_BYTES / each;
+        int64_t most = ATTEND_WS_BYTES / (2 * SLOT<D> * 4);
         if (most > CUS * RESIDENT<D, QP, PP>) most = CUS * RESIDENT<D, QP, PP>;
         const int64_t want = (rows * most_blocks + WAVES - 1) / WAVES;
         groups = want < 1 ? 1 : want < most ? want : most;
-        j.headers = static_cast<Header *>(j.a.ws);
-        j.slots = reinterpret_cast<float *>(j.headers + groups);
+        j.slots = static_cast<float *>(j.a.ws);
+        j.arrived = reinterpret_cast<uint32_t *>(static_cast<char *>(j.a.ws) + ATTEND_WS_BYTES);
     }
     if (groups > launch_groups(256) || groups >= (int64_t(1) << 31)) return -1;
     j.groups = (int)groups;
-    const int rc = launch_kernel(kv4_kernel<T, D, QP, PP>, dim3((unsigned)groups), dim3(256), stream, j);
-    if (rc != 0 || !j.split) return rc;
-    return launch_kernel(kv4_join<D>, dim3((unsigned)groups * 4), dim3(256), stream, j);
+    return launch_kernel(kv4_kernel<T, D, QP, PP>, dim3((unsigned)groups), dim3(256), stream, j);
 }
 
 template <int D>

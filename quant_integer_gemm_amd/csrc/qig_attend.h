@@ -50,7 +50,8 @@ struct Kv4Attend {
     void *ws;                // or nullptr
 };
 
-// Bytes of the workspace (the stream-K one) that may hold partial results.
+// Bytes of the workspace (the stream-K one) that may hold partial results; 4096 arrival
+// counters of 32 bits, all zero between calls, follow them.
 constexpr int64_t ATTEND_WS_BYTES = int64_t(1024) * 2 * 64 * 64 * 4;
 
 struct Pool {
