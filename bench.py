@@ -47,6 +47,10 @@ METRIC = "MMQ int8 TOPS + µs/GEMM, q4_K & q6_K 3584×3584×nt512; % of int8 MFM
 # of the int8 workloads, which run no k-quant GEMM
 METRICS_I8 = {"ffn_i8": "int8 FFN TOPS, 3584→2×18944 gated→3584, nt2630",
               "experts": "int8 experts' FFN TOPS, 64 of 3584→2×2368 gated→3584, 6 a token, routing included, nt2630"}
+# of the attention workloads
+METRICS_ATTEND = {"attend": "prompt attention TFLOP/s, nt2630, 28 heads on 4 of 128, bf16, its cache write included",
+                  "decode": "decoding attention tokens/s, 64 requests of 4096 cached tokens, 28 heads on 4 of 128, 4-bit "
+                            "cache, its write included"}
 PEAK_INT8_TOPS = 5000.0       # MI355X dense int8 MFMA, published
 PEAK_HBM_GBS = 8000.0         # MI355X HBM3E, published
 NT, OD, ID = 512, 3584, 3584
@@ -61,13 +65,16 @@ def parse():
     # clocks and measured up to ~10% slow, depending on what ran first
     p.add_argument("--warmup", type=int, default=300)
     p.add_argument("--no-cpu-baseline", action="store_true")
-    p.add_argument("--workload", choices=["proj", "ffn", "layer", "layer_q6v", "down", "kv", "ffn_i8", "experts"], default="proj",
+    p.add_argument("--workload", choices=["proj", "ffn", "layer", "layer_q6v", "down", "kv", "ffn_i8", "experts",
+                                          "attend", "decode"], default="proj",
                    help="proj: the q4_K and q6_K 3584x3584 nt=512 GEMMs (the headline); ffn: the 7B-class "
                         "FFN GEMMs at nt=512; layer: all seven GEMMs of a 7B-class layer at nt=2630; down: "
                         "the layer's q6_K down projection alone (3584x18944, nt=2630); kv: the layer's k and v "
                         "projections; layer_q6v: the layer with a q6_K v projection; ffn_i8: the layer's FFN at "
                         "nt=2630 in int8 with scales per token and channel; experts: the same FFN as 64 experts of "
-                        "an eighth of its width, six a token, routing included")
+                        "an eighth of its width, six a token, routing included; attend: the layer's prompt attention "
+                        "at nt=2630 with the write of its keys and values to the 4-bit cache; decode: one token each of "
+                        "64 requests with 4096 cached tokens, written and attended")
     p.add_argument("--activations", choices=["tiled", "pad40"], default="tiled",
                    help="ffn / layer workloads: activation plane of the timed step")
     p.add_argument("--copy-calibration", action="store_true",
@@ -634,6 +641,85 @@ def run_int8(args):
     }), flush=True)
 
 
+def run_attend(args):
+    """The attention workloads, bf16, synthetic inputs of the layer's widths (28 heads
+    of 128 on 4): attend: a prompt of 2630 tokens, its pages taken, keys and values
+    written to the 4-bit cache, and its causal attention; decode: 64 requests of
+    4096 cached tokens, one new token each, written and attended.  Every call of
+    the step is also timed alone."""
+    import torch
+    import quant_integer_gemm_amd as qig
+    dev = torch.device("cuda:0")
+    hq, hkv, d, page = 28, 4, 128, 64
+    prompt = args.workload == "attend"
+    nseq, total = (1, 2630) if prompt else (64, 4096)
+    new = total if prompt else 1
+    g = torch.Generator(device=dev).manual_seed(SEED4)
+
+    def heads(n, h):
+        return torch.randn((n, h, d), generator=g, device=dev).bfloat16()
+
+    nt, width = nseq * new, -(-total // page)
+    q, k, v = heads(nt, hq), heads(nt, hkv), heads(nt, hkv)
+    pages = qig.new_kv4(nseq * width, hkv, d, page, dev)
+    tables = torch.full((nseq, width), -1, dtype=torch.int32, device=dev)
+    lengths = torch.full((nseq,), total, dtype=torch.int32, device=dev)
+    refs = torch.zeros(nseq * width, dtype=torch.int32, device=dev)
+    missing = qig.take_pages(tables, lengths, refs, page)
+    assert int(missing) == 0
+    ws, y = qig.new_workspace(dev), torch.empty_like(q)
+    starts = torch.tensor([0, total], dtype=torch.int32, device=dev) if prompt else None
+    if not prompt:   # the tokens before
+        at = torch.arange(0, nseq * total + 1, total, dtype=torch.int32, device=dev)
+        qig.write_kv4(heads(nseq * total, hkv), heads(nseq * total, hkv), pages, tables, lengths, at)
+    calls = {"take_pages": lambda: qig.take_pages(tables, lengths, refs, page, missing=missing),
+             "write_kv4": lambda: qig.write_kv4(k, v, pages, tables, lengths, starts)}
+    if prompt:
+        calls["attend_prompt"] = lambda: qig.attend_prompt(q, k, v, starts, y=y)
+    else:
+        calls["attend_kv4"] = lambda: qig.attend_kv4(q, pages, tables, lengths, y=y, ws=ws)
+
+    def step():
+        for fn in calls.values():
+            fn()
+
+    spun, clocks = spin_up(step, args.spinup_s)
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        step()
+    torch.cuda.synchronize()
+    ms_per_step = (time.perf_counter() - t0) / args.steps * 1e3
+    per = {n: gpu_avg_us(fn, args.steps) for n, fn in calls.items()}
+    flops = 4.0 * hq * d * (nt * (nt + 1) / 2 if prompt else nseq * total)
+    cache_bytes = 1.25 * d * hkv * nseq * total
+    attention = per["attend_prompt" if prompt else "attend_kv4"] * 1e-6
+    print(json.dumps({
+        "metric": METRICS_ATTEND[args.workload],
+        "value": round(flops / (ms_per_step * 1e-3) / 1e12 if prompt else nt / (ms_per_step * 1e-3), 2),
+        "unit": "TFLOP/s" if prompt else "tokens/s",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms_per_step, 4),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": "bf16",
+        "data": "synthetic",
+        "config": {"workload": args.workload, "requests": nseq, "new_tokens": new, "tokens": total, "heads": hq,
+                   "kv_heads": hkv, "head_size": d, "page": page, "cache": "4 bits, bf16 scale and minimum per 32"},
+        "per_kernel_us": {n: round(t, 3) for n, t in per.items()},
+        "summed_us": round(sum(per.values()), 2),
+        "attention_tflops": round(flops / attention / 1e12, 1),
+        "cache_read_gbs": None if prompt else round(cache_bytes / attention / 1e9, 1),
+        "spinup": {"seconds": args.spinup_s, "steps": spun},
+        "clocks_mhz": clocks,
+    }), flush=True)
+
+
 # rocprofv3 kernel names -> the names bench.py reports
 PROFILE_NAMES = {
     "qig::mmq_kernel<4, 0, 0, 0>": "mmq_q4k", "qig::mmq_kernel<6, 0, 0, 0>": "mmq_q6k_raw",
@@ -840,6 +926,9 @@ def main():
     qig.load()
     if args.workload in METRICS_I8:
         run_int8(args)
+        return
+    if args.workload in METRICS_ATTEND:
+        run_attend(args)
         return
     if args.workload != "proj":
         run_gemm_set(args)

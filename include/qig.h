@@ -618,9 +618,9 @@ int read_kv4(void *k, int64_t k_token, int64_t k_head, void *v, int64_t v_token,
  * attend_kv4 -- attention of the new tokens over all cached ones of their
  * sequences: y[i] = sum over j of p_j v[j] for the values that the cache stands
  * for, the row at position p seeing the positions up to p.  Tokens without a page
- * are left out; a row that sees nothing gets zeros.  fp32 sums; 22 bits or more of
- * every product's operands are kept, for bf16 outputs 11 of p_j s_j; y is rounded
- * once.
+ * are left out; a row that sees nothing gets zeros.  Sums are fp32.  For fp32 q or y the
+ * products' operands keep 22 bits; for 16-bit ones a sum of products keeps 17 bits
+ * below its largest term, and for bf16 y p_j s_j has 11.  y is rounded once.
  *   q      [nt][hq][d] elements of type;  y [nt][hq][d] of ytype
  *   scale  as attend_prompt
  *   ws     NULL, or a workspace as for the stream-K calls (the same rules): lets the

@@ -8,8 +8,12 @@
 //
 // so that both products run on the codes themselves, on v_mfma_f32_16x16x32_f16:
 //  * 4 bits put into the mantissa of a 16-bit zero are the f16 subnormal code *
-//    2^-24 (or code * 2^-20, four bits further up), which the MFMA multiplies exactly.
-//    Eight codes take five instructions and no conversion.
+//    2^-24 (or code * 2^-20, four bits further up): eight codes take five instructions and
+//    no conversion.  The MFMA aligns a sum's products by their operands' exponents, which
+//    for all subnormals is the same one: with the codes in the lowest bits it keeps
+//    about 17 bits below the largest product (measured), far more than 16-bit
+//    results have.  For fp32 queries or results the codes are put in the highest four bits,
+//    code * 2^-18, where it keeps all 24 (eight instructions for eight codes).
 //  * S^T = K Q^T: 16 tokens by 16 rows of queries, one MFMA for each group of 32
 //    channels, whose sum then meets its token's scale.  O^T = V^T P^T: 16 channels by
 //    16 rows over 32 tokens, with P_j s_jg for the channels' group.  The cache's layout
@@ -26,7 +30,8 @@
 // P s is scaled by 2^(6 - E), E the largest exponent of the group's scales so far:
 // with P <= 2^8 it stays below 2^15.  P s is rounded to f16 once where y is bf16 (its
 // 2^-12 is small beside y's own 2^-9); for fp32 and f16 results a second MFMA adds
-// what the rounding left, 22 bits together, and the same for fp32 queries.
+// what the rounding left, 22 bits together, and the same for fp32 queries (QP and PP:
+// parts of the queries and of P s, PP 3 being two parts for fp32 results).
 //
 // The work, 32 tokens by 16 rows by key head, is split evenly over the workgroups
 // whatever the sequences' lengths: they all sum the lengths and take equal runs of
@@ -342,11 +347,23 @@ __device__ __forceinline__ void join_rows(const Job &j, uint32_t g, int pieces, 
 // as many in all, each with its share of the list, so that none waits for another's end.
 template <int D, int QP, int PP> constexpr int RESIDENT = D == 256 ? 1 : QP == 2 ? 2 : 3;
 
+// Two codes of a word, at bits 4 b of its halves, as f16 subnormals: code * 2^-18 where
+// FINE, else code * 2^-24, or 2^-20 for odd b.
+template <int B, bool FINE>
+__device__ __forceinline__ uint32_t codes(uint32_t w)
+{
+    if constexpr (FINE) return (B == 0 ? w << 6 : B == 1 ? w << 2 : B == 2 ? w >> 2 : w >> 6) & 0x03c003c0u;
+    return (B & 2 ? w >> 8 : w) & (B & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+
 template <int T, int D, int QP, int PP>
 __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
 {
     typedef elem_t<T> E;
     constexpr int G = D / 32, Q = G / 2, TILES = D / 16;
+    // fp32 queries (QP 2) or results (PP 3): all bits of the products are kept
+    constexpr bool FINE_K = QP == 2 || PP == 3, FINE_V = PP == 3;
+    constexpr int UP_K = FINE_K ? 18 : 24, UP_V = FINE_V ? 18 : 24;   // codes are 2^-UP
     __shared__ float joined[WAVES][ROWS * D];
     __shared__ float stats[WAVES][2][ROWS];
     __shared__ uint32_t tmp[4], found[2], arrivals;
@@ -485,18 +502,19 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float v0 = ldexp_f(f[g][2 * i], (i & 1 ? -4 : 0) - e), v1 = ldexp_f(f[g][2 * i + 1], (i & 1 ? -4 : 0) - e);
+                    const int sh = (!FINE_K && i & 1 ? -4 : 0) - e;
+                    const float v0 = ldexp_f(f[g][2 * i], sh), v1 = ldexp_f(f[g][2 * i + 1], sh);
                     hi[i] = pack_f16(v0, v1);
                     lo[i] = pack_rest(hi[i], v0, v1);
                 }
                 qv[0][g] = operand(hi[0], hi[1], hi[2], hi[3]);
                 if constexpr (QP > 1) qv[1][g] = operand(lo[0], lo[1], lo[2], lo[3]);
-                const float v = ldexp_f(qs[g], -24 - e);
+                const float v = ldexp_f(qs[g], -UP_K - e);
                 const __bf16 p0 = (__bf16)v, p1 = (__bf16)(v - (float)p0), p2 = (__bf16)(v - (float)p0 - (float)p1);
                 const __bf16 mine = h == 0 ? p0 : h == 1 ? p1 : p2;
                 if (h < 3) qm[g / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, mine) << (16 * (g % 2));
             }
-            F = ldexp_f(j.a.c, 24 + e);
+            F = ldexp_f(j.a.c, UP_K + e);
         }
         // the tokens that this row sees: the first `limit` ones; from token `full` on some
         // row of the tile sees less than all
@@ -535,8 +553,8 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                     f32x4 acc = mfma_bf16_16(m4, qm, f32x4(0.0f));
                     each<G>([&](auto gc) {
                         constexpr int g = gc.value, w = u * G + g;
-                        const uint32_t c0 = k.c[w / 4][w % 4], c1 = c0 >> 8;
-                        const f16x8 kv = operand(c0 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x000f000fu, c1 & 0x00f000f0u);
+                        const uint32_t c = k.c[w / 4][w % 4];
+                        const f16x8 kv = operand(codes<0, FINE_K>(c), codes<1, FINE_K>(c), codes<2, FINE_K>(c), codes<3, FINE_K>(c));
                         f32x4 dot = 0.0f;
                         dot = mfma_f16(kv, qv[0][g], dot);
                         if constexpr (QP > 1) dot = mfma_f16(kv, qv[1][g], dot);
@@ -658,8 +676,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                         uint32_t c[4];
                         each<4>([&](auto pc) {
                             constexpr int i = pc.value * (D / 64) + n / 4;
-                            const uint32_t word = v.c[i / 4][i % 4];
-                            c[pc.value] = (bit & 2 ? word >> 8 : word) & (bit & 1 ? 0x00f000f0u : 0x000f000fu);
+                            c[pc.value] = codes<bit, FINE_V>(v.c[i / 4][i % 4]);
                         });
                         const f16x8 vv = operand(c[0], c[1], c[2], c[3]);
                         o[n] = mfma_f16(vv, hi, o[n]);
@@ -685,7 +702,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                 const int n = 2 * g + y;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    o[n][r] = ldexp_f(o[n][r], e + 24 - 6 - (n & 1 ? 4 : 0)) + mm[g];
+                    o[n][r] = ldexp_f(o[n][r], e + UP_V - 6 - (!FINE_V && n & 1 ? 4 : 0)) + mm[g];
             }
         });
         __syncthreads();                            // the piece before is out of LDS
@@ -775,12 +792,15 @@ int launch_typed(Job j, hipStream_t stream)
 template <int D>
 int launch_dim(const Job &j, hipStream_t stream)
 {
-    const bool fine = j.a.ytype != T_BF16;
-    if (j.a.type == T_F32)
-        return fine ? launch_typed<T_F32, D, 2, 2>(j, stream) : launch_typed<T_F32, D, 2, 1>(j, stream);
-    if (j.a.type == T_BF16)
-        return fine ? launch_typed<T_BF16, D, 1, 2>(j, stream) : launch_typed<T_BF16, D, 1, 1>(j, stream);
-    return fine ? launch_typed<T_F16, D, 1, 2>(j, stream) : launch_typed<T_F16, D, 1, 1>(j, stream);
+    const auto by_result = [&](auto t) {
+        constexpr int T = t.value, QP = T == T_F32 ? 2 : 1;
+        if (j.a.ytype == T_BF16) return launch_typed<T, D, QP, 1>(j, stream);
+        if (j.a.ytype == T_F16) return launch_typed<T, D, QP, 2>(j, stream);
+        return launch_typed<T, D, QP, 3>(j, stream);
+    };
+    if (j.a.type == T_F32) return by_result(std::integral_constant<int, T_F32>());
+    if (j.a.type == T_BF16) return by_result(std::integral_constant<int, T_BF16>());
+    return by_result(std::integral_constant<int, T_F16>());
 }
 
 }  // namespace
