@@ -50,6 +50,21 @@ __device__ __forceinline__ bool find_rows(const PromptArgs &a, int slot, int per
 
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < INFINITY; }
 
+// Values of a 16-byte unit that are not finite go (and whether there was one is returned).
+template <int T>
+__device__ __forceinline__ int clean(u32x4 &v)
+{
+    uint32_t bad = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        constexpr uint32_t EXP = T == T_F32 ? 0x7f800000 : T == T_F16 ? 0x7c00 : 0x7f80;
+        const uint32_t w = v[j], lo = (w & EXP) == EXP, hi = T != T_F32 && ((w >> 16) & EXP) == EXP;
+        bad |= lo | hi;
+        v[j] = w & ~((lo ? T == T_F32 ? ~0u : 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
+    }
+    return (int)bad;
+}
+
 // A value that is not finite must reach the queries that see it and no other one; in the
 // product its 0 * NaN would reach them all.  So in steps where some query does not
 // see some key such values are 0 in LDS, and if there were any the sums that saw one
@@ -295,7 +310,6 @@ constexpr float LAZY = 8.0f;
 template <int T> struct Mfma16;
 template <> struct Mfma16<T_BF16> {
     typedef bf16x8 type;
-    static constexpr uint32_t EXP = 0x7f80;
     static constexpr float UP = 0.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b)
     {
@@ -309,7 +323,6 @@ template <> struct Mfma16<T_BF16> {
 };
 template <> struct Mfma16<T_F16> {
     typedef f16x8 type;
-    static constexpr uint32_t EXP = 0x7c00;
     static constexpr float UP = 6.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b)
     {
@@ -406,17 +419,6 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
             }
         }
     };
-    // Not finite values go (and whether there was one is returned).
-    const auto clean = [&](u32x4 &v) {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t w = v[j], lo = (w & M::EXP) == M::EXP, hi = ((w >> 16) & M::EXP) == M::EXP;
-            bad |= lo | hi;
-            v[j] = w & ~((lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u));
-        }
-        return (int)bad;
-    };
     // The step's keys and values are in LDS for all waves; with masks whether there was a
     // value that is not finite.
     const auto arrive = [&](int buf, bool masks) {
@@ -429,7 +431,7 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
             for (int i = 0; i < N; ++i) {        // all in place: no step with masks is before another without
                 u32x4 *at = reinterpret_cast<u32x4 *>(&lds_v[buf][(i * NT + threadIdx.x) * 8]);
                 u32x4 v = *at;
-                if (clean(v)) {
+                if (clean<T>(v)) {
                     *at = v;
                     bad = 1;
                 }
@@ -440,7 +442,7 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
         for (int i = 0; i < (DIRECT ? 0 : N); ++i) {
             const int u = i * NT + threadIdx.x, r = u / CH, c = u % CH;
             *reinterpret_cast<u32x4 *>(&lds_k[buf][(r * CH + (c ^ swz_k<D>(r))) * 8]) = ks[i];
-            if (masks) bad |= clean(vs[i]);
+            if (masks) bad |= clean<T>(vs[i]);
             *reinterpret_cast<u32x4 *>(&lds_v[buf][(r * CH + (c ^ swz_v<D>(r))) * 8]) = vs[i];
         }
         if (masks) return __syncthreads_or(bad);
@@ -541,6 +543,248 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
         }
 }
 
+// Few rows against many keys: a workgroup has 32 rows, and its four waves each every
+// fourth step of the keys, in LDS of their own and without a barrier; their sums are
+// joined at the end.  A quarter of the serial steps, for four times the reads of keys
+// and values from the caches.
+//   Waits: keys i and values i are N copies each; keys i + 1 are asked for when S^T has
+//   read keys i, values i + 1 when O^T has read values i; so before either product the
+//   N youngest copies may still be on their way.
+// One workgroup has a CU (128 KB of LDS at 128 channels), so it is taken while the tiles of
+// 128 rows would leave CUs or their second places empty.  Tiles of 128 rows against this,
+// 128 channels, us: fp32 with 16 queries on 4096 keys 576 / 166, 1024 causal ones (32 heads
+// on 8) 152 / 116, 1536 267 / 233, 2048 314 / 388; fp16 85 / 40 with 16 queries, 8 x 32 queries
+// on 1024 keys 32 / 19, 512 causal ones 18 / 21.  fp32 at 256 channels, two waves a workgroup:
+// 16 queries on 4096 keys 1090 / 592, 512 causal ones 148 / 109, 768 218 / 229.
+template <int T, int D> struct Split {
+    static constexpr int KT = D == 256 || T == T_F32 ? 32 : 64;
+    static constexpr int W = D == 256 && T == T_F32 ? 2 : 4;     // as many as have room in LDS
+    static constexpr int64_t GROUPS = T != T_F32 ? 128 : D == 256 ? 160 : 400;   // tiles of 128 rows, over all key heads
+};
+
+template <int N>
+__device__ __forceinline__ void all_but(bool more)
+{
+    if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+template <int T, int D, bool DIRECT>
+__global__ __launch_bounds__((64 * Split<T, D>::W), 1) void prompt_split(PromptArgs a, int slots, int per)
+{
+    typedef elem_t<T> E;
+    constexpr int B = sizeof(E), KT = Split<T, D>::KT, W = Split<T, D>::W, CH = D * B / 16, N = KT * CH / 64, V = VEC<T>;
+    constexpr int TILE = KT * D * B;
+    __shared__ __align__(16) uint8_t lds[W][2][TILE];
+    __shared__ float stats[W][2][32];
+    const int kvh = (int)(blockIdx.x % (uint32_t)a.hkv);
+    Tile t;
+    if (!find_rows<32>(a, slots - 1 - (int)(blockIdx.x / (uint32_t)a.hkv), per, t)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+    const int d = a.d;
+    const E *kp = static_cast<const E *>(a.k.p) + (int64_t)t.k0 * a.k.token + (int64_t)kvh * a.k.head;
+    const E *vp = static_cast<const E *>(a.v.p) + (int64_t)t.k0 * a.v.token + (int64_t)kvh * a.v.head;
+    const uint32_t rows = t.rows, mine = t.row0 + n;
+    const auto query_of = [&](uint32_t r) { return (int)((r < rows ? r : rows - 1) / (uint32_t)per); };
+    const int query = query_of(mine), head = kvh * per + (int)((mine < rows ? mine : rows - 1) - (uint32_t)query * per);
+    const E *qp = static_cast<const E *>(a.q.p) + (int64_t)(t.q0 + query) * a.q.token + (int64_t)head * a.q.head;
+    constexpr int QU = CH / 2;                     // 16-byte units of a row in a lane: every other one
+    u32x4 q[QU];
+#pragma unroll
+    for (int x = 0; x < QU; ++x) {
+        const int c = (2 * x + h) * V;
+        q[x] = c < d ? load16<T>(qp + c) : u32x4{0, 0, 0, 0};
+    }
+    const int off = t.nk - t.nq;
+    const auto end_of = [&](int i) {
+        const int e = a.causal ? off + i + 1 : t.nk;
+        return e < 0 ? 0 : e > t.nk ? t.nk : e;
+    };
+    const int end = end_of(query);
+    const int kend = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + 31)));
+    const int full = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0)));
+
+    uint8_t *lk = lds[wave][0], *lv = lds[wave][1];
+    const auto unit_k = [](int r, int c) { return r * CH + (c ^ (T == T_F32 ? r & 15 : swz_k<D>(r))); };
+    const auto unit_v = [](int r, int c) { return r * CH + (c ^ (T == T_F32 ? (r & 4) << 1 : swz_v<D>(r))); };
+    const auto load = [&](bool values, int k0) {
+        const E *p = (values ? vp : kp) + (int64_t)k0 * (values ? a.v.token : a.k.token);
+        const int64_t step = values ? a.v.token : a.k.token;
+        uint8_t *to = values ? lv : lk;
+        const int keys = t.nk - k0;
+        if constexpr (DIRECT) {
+            const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)to;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int u = i * 64 + lane, r = u / CH, pc = u % CH, row = r < keys ? r : keys - 1;
+                const int c = values ? unit_v(r, pc) - r * CH : unit_k(r, pc) - r * CH;
+                copy16(p, (uint32_t)row * (uint32_t)step * (uint32_t)B + c * 16, at + i * 1024);
+            }
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < N; ++i) {
+                const int u = i * 64 + lane, r = u / CH, c = u % CH;
+                const u32x4 w = r < keys && c * V < d ? load16<T>(p + (int64_t)r * step + c * V) : u32x4{0, 0, 0, 0};
+                reinterpret_cast<u32x4 *>(to)[values ? unit_v(r, c) : unit_k(r, c)] = w;
+            }
+        }
+    };
+
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    int k0 = wave * KT;
+    if (k0 < kend) {
+        load(false, k0);
+        load(true, k0);
+    }
+    for (; k0 < kend; k0 += W * KT) {
+        const bool more = k0 + W * KT < kend;
+        if constexpr (DIRECT) all_but<N>(true);
+        else lds_read();
+        f32x16 s[KT / 32];
+#pragma unroll
+        for (int y = 0; y < KT / 32; ++y) s[y] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < QU; ++x)
+#pragma unroll
+            for (int y = 0; y < KT / 32; ++y) {
+                const u32x4 kv = reinterpret_cast<const u32x4 *>(lk)[unit_k(32 * y + n, 2 * x + h)];
+                if constexpr (T == T_F32) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[y] = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(f32x4, kv)[i], __builtin_bit_cast(f32x4, q[x])[i],
+                                                                    s[y], 0, 0, 0);
+                } else {
+                    s[y] = Mfma16<T>::mul(kv, q[x], s[y]);
+                }
+            }
+        lds_read();
+        if (more) load(false, k0 + W * KT);
+        if (k0 + KT > full) {
+#pragma unroll
+            for (int y = 0; y < KT / 32; ++y)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (k0 + 32 * y + mfma_row(r, h) >= end) s[y][r] = -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int y = 0; y < KT / 32; ++y)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[y][r]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top * a.c), ref = mn == -INFINITY ? 0.0f : mn;
+        const float fix = __builtin_amdgcn_exp2f(m - ref);
+        m = mn;
+        float sum = 0.0f;
+        constexpr float UP = T == T_F16 ? 6.0f : 0.0f;
+#pragma unroll
+        for (int y = 0; y < KT / 32; ++y)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[y][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[y][r], a.c, UP - ref));
+                sum += s[y][r];
+            }
+        l = l * fix + sum;
+        if (__any(fix != 1.0f)) {
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) o[x] *= fix;
+        }
+        if constexpr (DIRECT) all_but<N>(more);
+        bool bad = false;
+        if (k0 + KT > full) {                      // values that are not finite go, as in the other kernels
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                u32x4 *at = reinterpret_cast<u32x4 *>(lv) + i * 64 + lane;
+                u32x4 v = *at;
+                if (clean<T>(v)) {
+                    *at = v;
+                    bad = true;
+                }
+            }
+            lds_read();
+            bad = __any(bad);
+        }
+        if constexpr (T == T_F32) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const float v = reinterpret_cast<const float *>(lv)[unit_v(mfma_row(r, h), 8 * x + (n >> 2)) * 4 + (n & 3)];
+                    o[x] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, s[0][r], o[x], 0, 0, 0);
+                }
+        } else {
+            typedef Mfma16<T> M;
+            const int turned = (h * 4 + ((lane & 15) >> 2)) * D, turned_x = swz_v<D>((lane & 15) >> 2);
+            const int turned_c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+#pragma unroll
+            for (int y = 0; y < KT / 16; ++y) {
+                const f32x16 &f = s[y / 2];
+                const int b = 8 * (y % 2);
+                const u32x4 p = {M::pack(f[b], f[b + 1]), M::pack(f[b + 2], f[b + 3]), M::pack(f[b + 4], f[b + 5]),
+                                 M::pack(f[b + 6], f[b + 7])};
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const uint16_t *at = reinterpret_cast<const uint16_t *>(lv) + turned + 16 * y * D +
+                                         (((4 * x + turned_c) ^ turned_x) * 8) + (lane & 1) * 4;
+                    const u32x2 v0 = read_turned(at), v1 = read_turned(at + 8 * D);
+                    o[x] = M::mul(u32x4{v0[0], v0[1], v1[0], v1[1]}, p, o[x]);
+                }
+            }
+        }
+        lds_read();
+        if (more) load(true, k0 + W * KT);
+        if (bad) {
+#pragma unroll
+            for (int y = 0; y < KT / 32; ++y) poison<D, E>(o, vp, a.v.token, k0 + 32 * y, t.nk, d, end, n, h);
+        }
+    }
+
+    l += __shfl_xor(l, 32);
+    if (h == 0) {
+        stats[wave][0][n] = m;
+        stats[wave][1][n] = l;
+    }
+    __syncthreads();                               // all waves are done with their keys and values
+    float top = stats[0][0][n];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, stats[w][0][n]);
+    const float mine_fix = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.0f : top));
+    constexpr int PITCH = D + (D < 256 ? 4 : 0);   // a row's four channels of 16 lanes meet in no bank
+    static_assert(W * 32 * PITCH * 4 <= (int)sizeof(lds), "the waves' sums stand where their keys and values were");
+    float *sums = reinterpret_cast<float *>(&lds[0][0][0]);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const f32x4 f = {o[x][r] * mine_fix, o[x][r + 1] * mine_fix, o[x][r + 2] * mine_fix, o[x][r + 3] * mine_fix};
+            *reinterpret_cast<f32x4 *>(&sums[(wave * 32 + n) * PITCH + 32 * x + mfma_row(r, h)]) = f;
+        }
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < 32 * D; i += 256 * W) {
+        const int row = i / D, c = i % D;
+        const uint32_t R = t.row0 + row;
+        if (R >= rows) break;
+        if (c >= d) continue;
+        float M = stats[0][0][row], sum = 0.0f;
+#pragma unroll
+        for (int w = 1; w < W; ++w) M = fmaxf(M, stats[w][0][row]);
+        f32x4 v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            sum += stats[w][1][row] * __builtin_amdgcn_exp2f(stats[w][0][row] - (M == -INFINITY ? 0.0f : M));
+            v += *reinterpret_cast<const f32x4 *>(&sums[(w * 32 + row) * PITCH + c]);
+        }
+        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+        const float f[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+        const int i_q = (int)(R / (uint32_t)per);
+        store4(a.y, a.ytype, (int64_t)(t.q0 + i_q) * a.y_token + (int64_t)(kvh * per + (int)(R - (uint32_t)i_q * per)) * a.y_head + c, f);
+    }
+}
+
 // Whether the rows of x can be copied straight into LDS, `step` keys at a time: 16-byte
 // units, and offsets of a step's rows in 32 bits.
 bool direct(const Heads &x, int64_t elem, int step)
@@ -559,9 +803,28 @@ int by_tiles(const PromptArgs &a, int bm, int threads, F launch)
     return launch(dim3((unsigned)groups), (int)slots, per);
 }
 
+template <int T, int D>
+bool split(const PromptArgs &a)
+{
+    const int64_t groups = (a.nt * (a.hq / a.hkv) / 128 + a.nseq) * a.hkv;
+    return groups <= Split<T, D>::GROUPS && a.nk > 2 * Split<T, D>::KT;
+}
+
+template <int T, int D>
+int launch_split(const PromptArgs &a, hipStream_t stream)
+{
+    constexpr int e = sizeof(elem_t<T>), KT = Split<T, D>::KT, threads = 64 * Split<T, D>::W;
+    return by_tiles(a, 32, threads, [&](dim3 grid, int slots, int per) {
+        if (a.d == D && direct(a.k, e, KT) && direct(a.v, e, KT))
+            return launch_kernel(prompt_split<T, D, true>, grid, dim3(threads), stream, a, slots, per);
+        return launch_kernel(prompt_split<T, D, false>, grid, dim3(threads), stream, a, slots, per);
+    });
+}
+
 template <int T, int D, int W, int KT>
 int launch_16_dim(const PromptArgs &a, hipStream_t stream)
 {
+    if (split<T, D>(a)) return launch_split<T, D>(a, stream);
     return by_tiles(a, 32 * W, 64 * W, [&](dim3 grid, int slots, int per) {
         if (a.d == D && direct(a.k, 2, KT) && direct(a.v, 2, KT))
             return launch_kernel(prompt_16<T, D, W, KT, true>, grid, dim3(64 * W), stream, a, slots, per);
@@ -580,6 +843,7 @@ int launch_16(const PromptArgs &a, hipStream_t stream)
 template <int D>
 int launch_f32_dim(const PromptArgs &a, hipStream_t stream)
 {
+    if (split<T_F32, D>(a)) return launch_split<T_F32, D>(a, stream);
     return by_tiles(a, 128, 256, [&](dim3 grid, int slots, int per) {
         if (a.d == D && direct(a.k, 4, 32) && direct(a.v, 4, 32))
             return launch_kernel(prompt_f32<D, true>, grid, dim3(256), stream, a, slots, per);
