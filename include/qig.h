@@ -663,8 +663,8 @@ int free_pages(int32_t *tables, int64_t rows, int64_t ld, int64_t width, int32_t
 
 /* take_pages -- every entry below ceil(lengths[row] / page) that is no page gets a
  * free one (refs = 1), the lowest first, in the order of rows and entries; missing
- * [1] = how many got none (they become -1), entries beyond the table's width
- * counted. */
+ * [1] = how many got none (they become -1).  A length beyond width * page has no
+ * entries there: it needs none of them, and none is missing. */
 int take_pages(int32_t *tables, int64_t rows, int64_t ld, int64_t width, const int32_t *lengths, int32_t *refs,
                int64_t npages, int64_t page, int32_t *missing, void *scratch, hipStream_t stream);
 

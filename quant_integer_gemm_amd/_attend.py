@@ -318,7 +318,8 @@ def take_pages(tables, lengths, refs, page, missing=None, stream=None):
     """Give every sequence the pages that its length needs: each entry below
     ceil(lengths[s] / page) of tables[s] that holds none gets a free one (refs 0,
     then 1), the lowest first, in the order of the table.  Returns int32 [1]: how many
-    found none and stay -1."""
+    found none and stay -1.  What a length has beyond the table's width is not
+    counted: the caller keeps lengths within width * page."""
     if _packed is None:
         _start()
     rows, width, ld = _table(tables)

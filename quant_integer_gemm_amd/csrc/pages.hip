@@ -186,14 +186,7 @@ __global__ __launch_bounds__(256) void take_kernel(Pool p, const uint64_t *notes
     if (blockIdx.x != 0 && mine[0] + mine[1] + mine[2] + mine[3] == 0) return;
     const int free = sum_notes<true, W>(notes, p.npages, before, tmp);
     if (blockIdx.x == 0) {
-        int64_t over = 0;                         // pages that the table has no place for
-        for (int64_t r = threadIdx.x; r < p.rows; r += 256) {
-            const int64_t n = pages_for(p.lengths[r], p.page);
-            if (n > p.width) over += n - p.width;
-        }
-        int total;
-        sum_before((int)(over < (1 << 30) ? over : 1 << 30), tmp, total);
-        if (threadIdx.x == 0) *missing = total + (ahead > free ? ahead - free : 0);
+        if (threadIdx.x == 0) *missing = ahead > free ? ahead - free : 0;
         ahead = 0;
     }
     const int64_t row = row0 + wave;

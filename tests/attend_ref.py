@@ -170,7 +170,6 @@ class Pool:
         free, missing = self.free_list(), 0
         for r, n in enumerate(self.len):
             n = max(0, -(-n // page))
-            missing += max(0, n - len(self.t[r]))
             for c in range(min(n, len(self.t[r]))):
                 if not self.ok(self.t[r][c]):
                     self.t[r][c] = -1

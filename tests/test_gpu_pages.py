@@ -242,3 +242,17 @@ def test_captured():
         assert [int(x) for x in out] == [int(x) for x in want]
         assert torch.equal(b.t, c.t) and torch.equal(b.len, c.len) and torch.equal(b.refs, c.refs)
         assert torch.equal(b.pages, c.pages)
+
+
+def test_a_length_beyond_the_table():
+    """Takes the entries that the table has; what is beyond it is not missing."""
+    t = torch.tensor([[3, 5], [-1, -1], [7, -1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([33, 1000, 16], dtype=torch.int32, device="cuda")
+    refs = torch.zeros(9, dtype=torch.int32, device="cuda")
+    refs[[3, 5, 7]] = 1
+    assert int(qig.take_pages(t, lens, refs, 16)) == 0
+    assert t.tolist() == [[3, 5], [0, 1], [7, -1]] and refs.tolist() == [1, 1, 0, 1, 0, 1, 0, 1, 0]
+    refs[:] = 1
+    t[1] = -1
+    assert int(qig.take_pages(t, lens, refs, 16)) == 2
+    assert t.tolist() == [[3, 5], [-1, -1], [7, -1]] and refs.tolist() == [1] * 9
