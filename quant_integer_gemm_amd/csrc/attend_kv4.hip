@@ -177,22 +177,33 @@ __device__ __forceinline__ Seq get_seq(const Job &j, int s)
 
 __device__ __forceinline__ uint32_t units(const Job &j, const Seq &q) { return (uint32_t)j.c.heads * q.tiles * q.blocks; }
 
-// Sum of a value over the lanes before this one, and over all 256 threads.
-__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t *tmp, uint32_t &total)
+// Sums of list entries.  A call's true list is shorter than 2^31; starts that decrease can
+// ask for more, and no sum of theirs may wrap: it stops at 2^31 - 1, beyond which the list
+// is cut off.
+__device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b) { return min(a + b, (uint32_t)INT32_MAX); }
+
+__device__ __forceinline__ uint32_t sum_to_lane(uint32_t s)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t s = v;
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         const uint32_t up = __shfl_up(s, o);
-        if (lane >= o) s += up;
+        if (lane >= o) s = plus(s, up);
     }
+    return s;
+}
+
+// Sum of a value over the threads before this one, and over all 256.
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t *tmp, uint32_t &total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t s = sum_to_lane(v), left = __shfl_up(s, 1);
     __syncthreads();
     if (lane == 63) tmp[wave] = s;
     __syncthreads();
-    const uint32_t t0 = tmp[0], t1 = tmp[1], t2 = tmp[2], t3 = tmp[3];
-    total = t0 + t1 + t2 + t3;
-    return s - v + (wave > 0 ? t0 : 0) + (wave > 1 ? t1 : 0) + (wave > 2 ? t2 : 0);
+    const uint32_t t0 = tmp[0], t1 = plus(t0, tmp[1]), t2 = plus(t1, tmp[2]);
+    total = plus(t2, tmp[3]);
+    return plus(lane > 0 ? left : 0, wave == 0 ? 0 : wave == 1 ? t0 : wave == 2 ? t1 : t2);
 }
 
 // A lane's operands from a block.  G: groups of channels; Q: the 16-byte pieces that a
@@ -393,23 +404,17 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
     if (nseq <= 64) {                               // each wave sums them by itself
         Seq mine = {};
         if (lane < nseq) mine = get_seq(j, lane);
-        const uint32_t u = lane < nseq ? units(j, mine) : 0;
-        uint32_t sum = u;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t up = __shfl_up(sum, o);
-            if (lane >= o) sum += up;
-        }
+        const uint32_t sum = sum_to_lane(lane < nseq ? units(j, mine) : 0);
         total = __builtin_amdgcn_readlane(sum, 63);
         run_of();
         if (at >= end) return;
         s = __popcll(__ballot(sum <= at));           // sequences that end before it
         const auto of = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, s); };
-        seq_at = of(sum - u);
+        seq_at = s > 0 ? (uint32_t)__builtin_amdgcn_readlane((int)sum, s - 1) : 0;
         q = {(int)of(mine.q0), (int)of(mine.n), (int)of(mine.length), (int)of(mine.keys), of(mine.blocks), of(mine.tiles)};
     } else {
         uint32_t mine = 0;
-        for (int i = threadIdx.x; i < nseq; i += 256) mine += units(j, get_seq(j, i));
+        for (int i = threadIdx.x; i < nseq; i += 256) mine = plus(mine, units(j, get_seq(j, i)));
         scan(mine, tmp, total);
         run_of();
         if (at >= end) return;
@@ -418,12 +423,12 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
             const int i = s0 + threadIdx.x;
             const uint32_t u = i < nseq ? units(j, get_seq(j, i)) : 0;
             uint32_t sum;
-            const uint32_t before = ahead + scan(u, tmp, sum);
+            const uint32_t before = plus(ahead, scan(u, tmp, sum));
             if (at >= before && at < before + u) {
                 found[0] = i;
                 found[1] = before;
             }
-            ahead += sum;
+            ahead = plus(ahead, sum);
             if (ahead > at) break;
         }
         __syncthreads();
@@ -757,7 +762,8 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
         }
         if (!whole) {
             const uint32_t row_at = at - first, owner = row_at / size;
-            const int pieces = (int)((row_at + q.blocks - 1) / size - owner) + 1;
+            const uint32_t row_end = min(row_at + q.blocks, total);   // where the list is cut off as well
+            const int pieces = (int)((row_end - 1) / size - owner) + 1;
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the piece is at the coherence point
             __syncthreads();
             if (threadIdx.x == 0)

@@ -394,6 +394,29 @@ def test_wrong_starts_and_lengths_stay_inside():
     assert torch.equal(c.pages, pages)
 
 
+@pytest.mark.parametrize("nseq", [63, 2001])
+def test_starts_that_ask_for_too_much(nseq):
+    """Starts up and down, so that the sequences together ask for more than 2^32 blocks (none
+    of which has a page): nothing outside is touched, and the workspace serves the next call."""
+    c = filled([300, 64], 1, 64, 32)
+    w = qig.new_workspace("cuda")
+    q, two = rows(2000, 16, 64, BF16, 1), rows(2, 16, 64, BF16, 2)
+    want = qig.attend_kv4(two, c.pages, c.tables, c.lengths, ws=w)
+    width = 16384 if nseq > 100 else 1 << 18
+    # the longest list that is counted: nt * 16 / 16 + nseq rows by width + 1 blocks
+    assert (2000 + nseq) * (width + 1) < 2 ** 31 < 2 ** 32 < (nseq // 2) * 2000 * width
+    tables = torch.full((nseq, width), -1, dtype=torch.int32, device="cuda")
+    y = torch.full((2020, 16, 64), 5.0, dtype=BF16, device="cuda")
+    st = ints([0 if i % 2 == 0 else 2000 for i in range(nseq + 1)])
+    qig.attend_kv4(q, c.pages, tables, ints([width * 32] * nseq), st, y=y[10:2010], ws=w)
+    torch.cuda.synchronize()
+    assert (y[:10] == 5).all() and (y[2010:] == 5).all()
+    assert torch.equal(qig.attend_kv4(two, c.pages, c.tables, c.lengths, ws=w), want)
+    many = qig.attend_kv4(rows(64, 16, 64, BF16, 3), c.pages, c.tables[:1].expand(64, -1).contiguous(),
+                          ints([300] * 64), ws=w)
+    assert not many.isnan().any() and (many != 0).any(2).all()
+
+
 def test_the_same_on_every_call():
     lens = [5000, 70, 900]
     c = filled(lens, 2, 128, 64)
