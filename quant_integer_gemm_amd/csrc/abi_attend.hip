@@ -247,7 +247,7 @@ int qig_attend_packed(int op, const void *words, hipStream_t stream)
     const auto real = [&](int i) {
         double d;
         memcpy(&d, &w[i], 8);
-        return (float)d;
+        return d != 0.0 && (float)d == 0.0f ? -1.0f : (float)d;   // too small a scale does not ask for the default
     };
     switch (op) {
     case 0:

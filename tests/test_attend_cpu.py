@@ -281,3 +281,42 @@ def test_pool_by_hand():
     assert p.take(4) == 0 and p.t[2] == [0, 3]
     p.free([1])
     assert p.compact() == (2, [0, 1, 2, 1, 4], [(3, 1)]) and p.t[2] == [0, 1]
+
+
+# The packed calls with their words; nt = 0 (or no pairs), so that valid ones return before a launch.
+PACKED = {
+    0: [P, 256, 64, P, 128, 64, P, 128, 64, 0, 0, 5, 4, 2, 64, P, P, 1, 1, 0.0, P, 256, 64, 0],
+    1: [P, 128, 64, P, 128, 64, 0, 0, 2, 64, P, 9, 5120, 32, P, 4, 4, P, P, 3],
+    2: [P, 128, 64, P, 128, 64, 0, 0, 2, 64, P, 9, 5120, 32, P, 4, 4, P, P, 3],
+    3: [P, 256, 64, 0, 0, 4, 2, 64, P, 9, 5120, 32, P, 4, 4, P, P, 3, 0.0, P, 256, 64, 0, None],
+    4: [P, 20, 64, 64, P, P, 0],
+    5: [P, 4, 8, 8, P, P, 20, P, 0],
+}
+
+
+def _packed(op, words, **at):
+    import struct
+    words = list(words)
+    for i, v in at.items():
+        words[int(i[1:])] = v
+    raw = b"".join(struct.pack("=d" if isinstance(w, float) else "=q",
+                               w.value if isinstance(w, ctypes.c_void_p) else 0 if w is None else w) for w in words)
+    return qig.load().qig_attend_packed(op, raw, None)
+
+
+@pytest.mark.parametrize("op", sorted(PACKED))
+def test_packed_calls_take_their_words(op):
+    assert _packed(op, PACKED[op]) == 0
+    bad = {0: dict(_10=-1), 1: dict(_7=-1), 2: dict(_8=0), 3: dict(_7=96), 4: dict(_6=-1), 5: dict(_8=-1)}[op]
+    assert _packed(op, PACKED[op], **bad) == -1
+
+
+def test_packed_calls_refuse_what_does_not_fit():
+    w = PACKED[0]
+    assert _packed(-1, w) == -1 and _packed(9, w) == -1 and qig.load().qig_attend_packed(0, None, None) == -1
+    for i in ("_9", "_18", "_23"):                       # a type, causal, the result's type
+        assert _packed(0, w, **{i: 1 << 32}) == -1 and _packed(0, w, **{i: -(1 << 40)}) == -1
+    assert _packed(0, w, _19=1e-30) == 0
+    for scale in (1e-50, 1e31, 1e300, -1e-50, float("nan"), float("inf")):
+        assert _packed(0, w, _19=scale) == -1            # 1e-50 is 0 in fp32, which would ask for 1 / sqrt(d)
+        assert _packed(3, PACKED[3], _18=scale) == -1
