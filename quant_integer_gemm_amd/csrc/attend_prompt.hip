@@ -116,6 +116,13 @@ __device__ __forceinline__ void copy16(const void *base, uint32_t off, uint32_t 
 }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// How keys and values reach LDS: through registers, for rows at any address; copied
+// straight into it, for rows of d = D elements at multiples of 16 bytes; and the same with
+// d < D (PADDED), where the lanes of units behind d copy none of the keys, whose places are
+// zeroed once, and any of the values, whose sums are not written.  1024 causal tokens, 32
+// heads on 8 of 96: fp32 175 us through registers, 155 so; fp16 32 and 29.5.
+enum { REGISTERS, STRAIGHT, PADDED };
+
 // fp32 operands on v_mfma_f32_32x32x2_f32.  Rows are (query, head of the group) pairs of
 // one key head, heads fastest: all heads that share a key head read one copy of it
 // from LDS, and a tile spans few queries, so that little of its last steps is masked.  A
@@ -128,16 +135,15 @@ __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" :::
 // LDS: 16-byte unit u of row r of K stands at u ^ (r & 15) (rows of 256 bytes), so that 16
 // lanes reading one unit of 16 rows meet in no bank, and of V at u ^ 8 (r / 4 & 1), so
 // that the two keys of a read do not.
-// DIRECT: both are copied straight into LDS, which takes rows of d = D elements at
-// multiples of 16 bytes; others go through registers.
 // Measured, 2630 causal tokens, 28 heads on 4 of 128: 438 us, 113 TFLOP/s; a large fp32
 // matrix product reaches 154.  The MFMAs are 75% of the time: they have the rate of the
 // vector units here, and the softmax's instructions come on top.  With a head a tile
 // and keys through registers it took 592.
-template <int D, bool DIRECT>
+template <int D, int COPY>
 __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a, int slots, int per)
 {
     constexpr int CH = D / 4, N = 32 * CH / 256, BM = 128;   // 16-byte units of a row; of a thread
+    constexpr bool DIRECT = COPY != REGISTERS, PAD = COPY == PADDED;
     __shared__ __align__(16) float lds_k[2][32 * D], lds_v[2][32 * D];
     const uint32_t work = place(blockIdx.x, gridDim.x);
     const int kvh = (int)(work % (uint32_t)a.hkv);
@@ -173,16 +179,22 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
     const auto at_k = [](int r, int c) { return r * CH + (c ^ (r & 15)); };
     const auto at_v = [](int r, int c) { return r * CH + (c ^ (r & 4) << 1); };
 
-    uint32_t k_off[DIRECT ? N : 1], v_off[DIRECT ? N : 1];
+    uint32_t k_off[DIRECT ? N : 1], v_off[DIRECT ? N : 1], k_in = 0;
     const auto offsets = [&](int keys) {           // of the copies, keys beyond the last one being that again
 #pragma unroll
         for (int i = 0; i < (DIRECT ? N : 0); ++i) {
             const int u = i * 256 + threadIdx.x, r = u / CH, c = u % CH, at = r < keys ? r : keys - 1;
-            k_off[i] = (uint32_t)at * (uint32_t)a.k.token * 4u + (c ^ (r & 15)) * 16;
-            v_off[i] = (uint32_t)at * (uint32_t)a.v.token * 4u + (c ^ (r & 4) << 1) * 16;
+            const int ck = c ^ (r & 15), cv = c ^ (r & 4) << 1;
+            k_off[i] = (uint32_t)at * (uint32_t)a.k.token * 4u + ck * 16;
+            v_off[i] = (uint32_t)at * (uint32_t)a.v.token * 4u + (!PAD || 4 * cv < d ? cv : 0) * 16;
+            k_in |= (uint32_t)(4 * ck < d) << i;
         }
     };
     offsets(32);
+    if constexpr (PAD) {
+        for (int i = threadIdx.x; i < 2 * 32 * D; i += 256) (&lds_k[0][0])[i] = 0.0f;
+        __syncthreads();
+    }
     const uint32_t k_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float *)&lds_k[0][0];
     const uint32_t v_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float *)&lds_v[0][0];
     const int first_wave = __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);
@@ -191,7 +203,8 @@ __global__ __launch_bounds__(256, D > 128 ? 1 : 2) void prompt_f32(PromptArgs a,
             if (t.nk - k0 < 32) offsets(t.nk - k0);
             const float *kb = kp + (int64_t)k0 * a.k.token, *vb = vp + (int64_t)k0 * a.v.token;
 #pragma unroll
-            for (int i = 0; i < N; ++i) copy16(kb, k_off[i], k_lds + (uint32_t)(buf * 32 * CH + i * 256 + first_wave) * 16);
+            for (int i = 0; i < N; ++i)
+                if (!PAD || k_in >> i & 1) copy16(kb, k_off[i], k_lds + (uint32_t)(buf * 32 * CH + i * 256 + first_wave) * 16);
 #pragma unroll
             for (int i = 0; i < N; ++i) copy16(vb, v_off[i], v_lds + (uint32_t)(buf * 32 * CH + i * 256 + first_wave) * 16);
         } else {
@@ -357,15 +370,14 @@ __device__ __forceinline__ u32x2 read_turned(const uint16_t *p)
 template <int D> __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
 template <int D> __device__ __forceinline__ int swz_v(int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
 
-// DIRECT: keys and values are copied straight into LDS, which takes rows of d = D
-// elements at multiples of 16 bytes; the lane that copies a unit asks for the one that
-// belongs there.  Others go through registers, unaligned or with zeros up to D.
-template <int T, int D, int W, int KT, bool DIRECT>
+// The lane that copies a unit asks for the one that belongs there.
+template <int T, int D, int W, int KT, int COPY>
 __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs a, int slots, int per)
 {
     typedef elem_t<T> E;
     typedef Mfma16<T> M;
     constexpr int NT = 64 * W, BM = 32 * W, CH = D / 8, N = KT * CH / NT;
+    constexpr bool DIRECT = COPY != REGISTERS, PAD = COPY == PADDED;
     __shared__ __align__(16) uint16_t lds_k[2][KT * D], lds_v[2][KT * D];
     const uint32_t work = place(blockIdx.x, gridDim.x);
     const int kvh = (int)(work % (uint32_t)a.hkv);
@@ -398,16 +410,22 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
     const int wave_full = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0 + wave * 32)));
 
     u32x4 ks[DIRECT ? 1 : N], vs[DIRECT ? 1 : N];
-    uint32_t k_off[DIRECT ? N : 1], v_off[DIRECT ? N : 1];
+    uint32_t k_off[DIRECT ? N : 1], v_off[DIRECT ? N : 1], k_in = 0;
     const auto offsets = [&](int rows) {         // of the copies, keys beyond the last one being that again
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int u = i * NT + threadIdx.x, r = u / CH, c = u % CH, at = r < rows ? r : rows - 1;
-            k_off[i] = (uint32_t)at * (uint32_t)a.k.token * 2u + (c ^ swz_k<D>(r)) * 16;
-            v_off[i] = (uint32_t)at * (uint32_t)a.v.token * 2u + (c ^ swz_v<D>(r)) * 16;
+            const int ck = c ^ swz_k<D>(r), cv = c ^ swz_v<D>(r);
+            k_off[i] = (uint32_t)at * (uint32_t)a.k.token * 2u + ck * 16;
+            v_off[i] = (uint32_t)at * (uint32_t)a.v.token * 2u + (!PAD || 8 * cv < d ? cv : 0) * 16;
+            k_in |= (uint32_t)(8 * ck < d) << i;
         }
     };
     if constexpr (DIRECT) offsets(KT);
+    if constexpr (PAD) {
+        for (int i = threadIdx.x; i < 2 * KT * D / 2; i += NT) reinterpret_cast<uint32_t *>(&lds_k[0][0])[i] = 0;
+        __syncthreads();
+    }
     const uint32_t k_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)&lds_k[0][0];
     const uint32_t v_lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)&lds_v[0][0];
     const int first_wave = __builtin_amdgcn_readfirstlane(threadIdx.x & ~63);
@@ -416,7 +434,8 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
             if (t.nk - k0 < KT) offsets(t.nk - k0);
             const E *kb = kp + (int64_t)k0 * a.k.token, *vb = vp + (int64_t)k0 * a.v.token;
 #pragma unroll
-            for (int i = 0; i < N; ++i) copy16(kb, k_off[i], k_lds + (uint32_t)(buf * KT * CH + i * NT + first_wave) * 16);
+            for (int i = 0; i < N; ++i)
+                if (!PAD || k_in >> i & 1) copy16(kb, k_off[i], k_lds + (uint32_t)(buf * KT * CH + i * NT + first_wave) * 16);
 #pragma unroll
             for (int i = 0; i < N; ++i) copy16(vb, v_off[i], v_lds + (uint32_t)(buf * KT * CH + i * NT + first_wave) * 16);
             return;
@@ -559,7 +578,8 @@ __global__ __launch_bounds__(64 * W, D > 128 ? 1 : 2) void prompt_16(PromptArgs 
 // fourth step of the keys, in LDS of their own and without a barrier; their sums are
 // joined at the end.  A quarter of the serial steps, for four times the reads of keys
 // and values from the caches.
-//   Waits: keys i and values i are N copies each; keys i + 1 are asked for when S^T has
+//   Waits: keys i and values i are N copies each (where all lanes take part in all of
+// them, else each product waits for all); keys i + 1 are asked for when S^T has
 //   read keys i, values i + 1 when O^T has read values i; so before either product the
 //   N youngest copies may still be on their way.
 // One workgroup has a CU (128 KB of LDS at 128 channels), so it is taken while the tiles of
@@ -582,12 +602,13 @@ __device__ __forceinline__ void all_but(bool more)
 }
 __device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <int T, int D, bool DIRECT>
+template <int T, int D, int COPY>
 __global__ __launch_bounds__((64 * Split<T, D>::W), 1) void prompt_split(PromptArgs a, int slots, int per)
 {
     typedef elem_t<T> E;
     constexpr int B = sizeof(E), KT = Split<T, D>::KT, W = Split<T, D>::W, CH = D * B / 16, N = KT * CH / 64, V = VEC<T>;
     constexpr int TILE = KT * D * B;
+    constexpr bool PAD = COPY == PADDED;
     __shared__ __align__(16) uint8_t lds[W][2][TILE];
     __shared__ float stats[W][2][32];
     const int kvh = (int)(blockIdx.x % (uint32_t)a.hkv);
@@ -618,6 +639,7 @@ __global__ __launch_bounds__((64 * Split<T, D>::W), 1) void prompt_split(PromptA
     const int full = __builtin_amdgcn_readfirstlane(end_of(query_of(t.row0)));
 
     uint8_t *lk = lds[wave][0], *lv = lds[wave][1];
+    // Layouts decide how keys come, not which kernel: results are the same bits at any address.
     const auto unit_k = [](int r, int c) { return r * CH + (c ^ (T == T_F32 ? r & 15 : swz_k<D>(r))); };
     const auto unit_v = [](int r, int c) { return r * CH + (c ^ (T == T_F32 ? (r & 4) << 1 : swz_v<D>(r))); };
     const auto load = [&](bool values, int k0) {
@@ -625,21 +647,22 @@ __global__ __launch_bounds__((64 * Split<T, D>::W), 1) void prompt_split(PromptA
         const int64_t step = values ? a.v.token : a.k.token;
         uint8_t *to = values ? lv : lk;
         const int keys = t.nk - k0;
-        if constexpr (DIRECT) {
-            const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)to;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int u = i * 64 + lane, r = u / CH, pc = u % CH, row = r < keys ? r : keys - 1;
-                const int c = values ? unit_v(r, pc) - r * CH : unit_k(r, pc) - r * CH;
-                copy16(p, (uint32_t)row * (uint32_t)step * (uint32_t)B + c * 16, at + i * 1024);
-            }
-        } else {
-#pragma unroll 4
+        if constexpr (COPY == REGISTERS) {
+#pragma unroll 8
             for (int i = 0; i < N; ++i) {
                 const int u = i * 64 + lane, r = u / CH, c = u % CH;
                 const u32x4 w = r < keys && c * V < d ? load16<T>(p + (int64_t)r * step + c * V) : u32x4{0, 0, 0, 0};
                 reinterpret_cast<u32x4 *>(to)[values ? unit_v(r, c) : unit_k(r, c)] = w;
             }
+            return;
+        }
+        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)to;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = i * 64 + lane, r = u / CH, pc = u % CH, row = r < keys ? r : keys - 1;
+            int c = (values ? unit_v(r, pc) : unit_k(r, pc)) - r * CH;
+            if (PAD && values && c * V >= d) c = 0;
+            if (!PAD || c * V < d) copy16(p, (uint32_t)row * (uint32_t)step * (uint32_t)B + c * 16, at + i * 1024);
         }
     };
 
@@ -648,14 +671,19 @@ __global__ __launch_bounds__((64 * Split<T, D>::W), 1) void prompt_split(PromptA
     for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
     float m = -INFINITY, l = 0.0f;
     int k0 = wave * KT;
+    if constexpr (PAD) {
+#pragma unroll 4
+        for (int i = lane; i < TILE / 16; i += 64) reinterpret_cast<u32x4 *>(lk)[i] = u32x4{0, 0, 0, 0};
+        lds_read();
+    }
     if (k0 < kend) {
         load(false, k0);
         load(true, k0);
     }
     for (; k0 < kend; k0 += W * KT) {
         const bool more = k0 + W * KT < kend;
-        if constexpr (DIRECT) all_but<N>(true);
-        else lds_read();
+        if constexpr (COPY == REGISTERS) lds_read();
+        else all_but<N>(!PAD);
         f32x16 s[KT / 32];
 #pragma unroll
         for (int y = 0; y < KT / 32; ++y) s[y] = 0.0f;
@@ -705,7 +733,7 @@ __global__ __launch_bounds__((64 * Split<T, D>::W), 1) void prompt_split(PromptA
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) o[x] *= fix;
         }
-        if constexpr (DIRECT) all_but<N>(more);
+        if constexpr (COPY != REGISTERS) all_but<N>(more && !PAD);
         bool bad = false;
         if (k0 + KT > full) {                      // values that are not finite go, as in the other kernels
 #pragma unroll
@@ -805,6 +833,12 @@ bool direct(const Heads &x, int64_t elem, int step)
            x.token * elem < (int64_t(1) << 31) / step;
 }
 
+int copy_of(const PromptArgs &a, int64_t elem, int step, int D)
+{
+    if (!direct(a.k, elem, step) || !direct(a.v, elem, step)) return REGISTERS;
+    return a.d == D ? STRAIGHT : PADDED;
+}
+
 // kernel(grid, slots, rows a query) for tiles of bm rows.
 template <typename F>
 int by_tiles(const PromptArgs &a, int bm, int threads, F launch)
@@ -825,11 +859,12 @@ bool split(const PromptArgs &a)
 template <int T, int D>
 int launch_split(const PromptArgs &a, hipStream_t stream)
 {
-    constexpr int e = sizeof(elem_t<T>), KT = Split<T, D>::KT, threads = 64 * Split<T, D>::W;
+    constexpr int KT = Split<T, D>::KT, threads = 64 * Split<T, D>::W;
     return by_tiles(a, 32, threads, [&](dim3 grid, int slots, int per) {
-        if (a.d == D && direct(a.k, e, KT) && direct(a.v, e, KT))
-            return launch_kernel(prompt_split<T, D, true>, grid, dim3(threads), stream, a, slots, per);
-        return launch_kernel(prompt_split<T, D, false>, grid, dim3(threads), stream, a, slots, per);
+        const int copy = copy_of(a, sizeof(elem_t<T>), KT, D);
+        if (copy == STRAIGHT) return launch_kernel(prompt_split<T, D, STRAIGHT>, grid, dim3(threads), stream, a, slots, per);
+        if (copy == PADDED) return launch_kernel(prompt_split<T, D, PADDED>, grid, dim3(threads), stream, a, slots, per);
+        return launch_kernel(prompt_split<T, D, REGISTERS>, grid, dim3(threads), stream, a, slots, per);
     });
 }
 
@@ -838,9 +873,10 @@ int launch_16_dim(const PromptArgs &a, hipStream_t stream)
 {
     if (split<T, D>(a)) return launch_split<T, D>(a, stream);
     return by_tiles(a, 32 * W, 64 * W, [&](dim3 grid, int slots, int per) {
-        if (a.d == D && direct(a.k, 2, KT) && direct(a.v, 2, KT))
-            return launch_kernel(prompt_16<T, D, W, KT, true>, grid, dim3(64 * W), stream, a, slots, per);
-        return launch_kernel(prompt_16<T, D, W, KT, false>, grid, dim3(64 * W), stream, a, slots, per);
+        const int copy = copy_of(a, 2, KT, D);
+        if (copy == STRAIGHT) return launch_kernel(prompt_16<T, D, W, KT, STRAIGHT>, grid, dim3(64 * W), stream, a, slots, per);
+        if (copy == PADDED) return launch_kernel(prompt_16<T, D, W, KT, PADDED>, grid, dim3(64 * W), stream, a, slots, per);
+        return launch_kernel(prompt_16<T, D, W, KT, REGISTERS>, grid, dim3(64 * W), stream, a, slots, per);
     });
 }
 
@@ -857,9 +893,10 @@ int launch_f32_dim(const PromptArgs &a, hipStream_t stream)
 {
     if (split<T_F32, D>(a)) return launch_split<T_F32, D>(a, stream);
     return by_tiles(a, 128, 256, [&](dim3 grid, int slots, int per) {
-        if (a.d == D && direct(a.k, 4, 32) && direct(a.v, 4, 32))
-            return launch_kernel(prompt_f32<D, true>, grid, dim3(256), stream, a, slots, per);
-        return launch_kernel(prompt_f32<D, false>, grid, dim3(256), stream, a, slots, per);
+        const int copy = copy_of(a, 4, 32, D);
+        if (copy == STRAIGHT) return launch_kernel(prompt_f32<D, STRAIGHT>, grid, dim3(256), stream, a, slots, per);
+        if (copy == PADDED) return launch_kernel(prompt_f32<D, PADDED>, grid, dim3(256), stream, a, slots, per);
+        return launch_kernel(prompt_f32<D, REGISTERS>, grid, dim3(256), stream, a, slots, per);
     });
 }
 

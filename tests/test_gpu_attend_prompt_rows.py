@@ -110,3 +110,37 @@ def test_few_queries_in_a_graph(dtype, d):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want_)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [8, 40, 64, 72, 96, 128, 136])
+@pytest.mark.parametrize("many", [False, True])
+def test_a_key_at_minus_infinity(dtype, d, many):
+    """A channel of a key at -infinity, positive in all queries: the key counts for nothing."""
+    lens = [150] + ([3] * 60 if many else [])
+    hq, hkv = (16, 8) if many else (2, 1)
+    q, k, v = make(lens, lens, hq, hkv, d, dtype, d)
+    q[:, :, 0] = q[:, :, 0].abs() + 1
+    k[70:73, 0, 0] = -math.inf
+    y = qig.attend_prompt(q, k, v, ints(starts_of(lens)))
+    k[70:73, 0] = 0
+    k[70:73, 0, 0] = -60000                     # far below all others: 0 in 64 bits too
+    w, al = want(q, k, v, lens, lens, True, 1 / math.sqrt(d), dtype, dtype)
+    ref.check(y, w, al)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [40, 80, 96, 128, 136])
+@pytest.mark.parametrize("many", [False, True])
+def test_odd_addresses(dtype, d, many):
+    """Rows that no 16-byte copy can take give the results of those that one can."""
+    lens = [200, 70] + ([3] * 60 if many else [])
+    hq, hkv = (16, 8) if many else (2, 1)
+    q, k, v = make(lens, lens, hq, hkv, d, dtype, d)
+    wide = torch.full((sum(lens), hkv * d * 2 + 3), math.nan, dtype=dtype, device="cuda")
+    ko, vo = (wide[:, i:i + hkv * d].unflatten(1, (hkv, d)) for i in (1, hkv * d + 3))
+    ko.copy_(k)
+    vo.copy_(v)
+    y = qig.attend_prompt(q, ko, vo, ints(starts_of(lens)))
+    w, al = want(q, k, v, lens, lens, True, 1 / math.sqrt(d), dtype, dtype)
+    ref.check(y, w, al)
