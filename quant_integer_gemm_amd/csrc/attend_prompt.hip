@@ -95,12 +95,14 @@ __device__ __forceinline__ void poison(f32x16 (&o)[D / 32], const E *vp, int64_t
 }
 
 // A workgroup's tile in the list of (tile, key head) pairs, the longest first.  Of the
-// workgroups that the GPU holds at once each CU gets one of every 256; every other
-// 256 are taken in reverse, so that a CU with a long tile has a short one beside it.
+// first 512 workgroups a CU gets one of the first and one of the second 256: the second
+// are taken in reverse, so that a CU with a long tile has a short one beside it; later ones
+// go where there is room.  2630 fp32 tokens, 28 heads on 4 of 128 (576 tiles): 507 us in the
+// list's order, 436 so.  Every other 256 in reverse: the same there, but 388 for 367 with
+// 4 x 1000 tokens of 32 heads on 8, and 63 for 58 in fp16.
 __device__ __forceinline__ uint32_t place(uint32_t block, uint32_t groups)
 {
-    const uint32_t row = block >> 8;
-    return (row & 1) != 0 && (row + 1) * 256 <= groups ? row * 256 + 255 - (block & 255) : block;
+    return block >> 8 == 1 && groups >= 512 ? 256 + 255 - (block & 255) : block;
 }
 
 // One 1 KB copy of 16 bytes a lane, from base + off to LDS byte address lds + 16 lane.
