@@ -123,6 +123,26 @@ def test_borders(dtype):
     assert (off <= s[..., None] * 0.5 + np.abs(want.reshape(off.shape)) * 2.0 ** -24).all()
 
 
+@pytest.mark.parametrize("ratio", [0, 4, 12])
+def test_values_next_to_borders(ratio):
+    """fp32 values a few steps to either side of where a code begins, next to minima up to
+    2^ratio times the scale."""
+    n, d = 600, 128
+    g = torch.Generator().manual_seed(ratio)
+    s = (torch.rand((n, 1, d // 32, 1), generator=g) + 0.5).bfloat16().float()
+    m = ((torch.rand((n, 1, d // 32, 1), generator=g) - 0.5) * 2.0 ** ratio).bfloat16().float()
+    code = torch.randint(0, 15, (n, 1, d // 32, 32), generator=g)
+    x = (m.double() + (code.double() + 0.5) * s.double()).float()
+    x = (x.view(torch.int32) + torch.randint(-3, 4, x.shape, generator=g, dtype=torch.int32)).view(torch.float32)
+    x[..., :1], x[..., 1:2] = m, (m.double() + 15 * s.double()).float()
+    x = x.reshape(n, 1, d)
+    c = Cache([n], 1, d, 32)
+    c.write(x.cuda(), -x.cuda(), ints([0, n]))
+    k, v = c.read(n, ints([0, n]))
+    assert np.array_equal(k.cpu().numpy(), ref.stands_for(x.numpy()))
+    assert np.array_equal(v.cpu().numpy(), ref.stands_for(-x.numpy()))
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_not_finite(bad):
     """A group that holds one stands for NaN, the others for what they are."""
