@@ -85,6 +85,10 @@ __device__ __forceinline__ uint32_t ceil_bf16(double x)
 // The scale's word of 32 values: s in its low half, m in its high one.
 __device__ __forceinline__ uint32_t scale_word(float lo, float hi, float &s, float &m)
 {
+    if (lo != lo) {                              // by its bits some NaN would round to 0
+        s = m = NAN;
+        return 0x7fc07fc0;
+    }
     const uint32_t mb = floor_bf16(lo);
     m = __builtin_bit_cast(float, mb);
     const uint32_t sb = ceil_bf16(((double)hi - (double)m) / 15.0);

@@ -139,8 +139,13 @@ def test_values_next_to_borders(ratio):
     c = Cache([n], 1, d, 32)
     c.write(x.cuda(), -x.cuda(), ints([0, n]))
     k, v = c.read(n, ints([0, n]))
-    assert np.array_equal(k.cpu().numpy(), ref.stands_for(x.numpy()))
-    assert np.array_equal(v.cpu().numpy(), ref.stands_for(-x.numpy()))
+    # a few steps below 0 in bits is NaN: those groups stand for NaN, the others for numbers
+    for got, of in ((k, x), (v, -x)):
+        of = of.numpy().reshape(n, -1, 32)
+        nan = np.isnan(of).any(2)
+        want = ref.stands_for(np.where(nan[..., None], 0, of).reshape(n, 1, d)).reshape(of.shape)
+        want[nan] = math.nan
+        assert np.array_equal(got.cpu().numpy().reshape(of.shape), want, equal_nan=True) and nan.mean() < 0.01
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
