@@ -27,9 +27,16 @@
 //
 // Range in f16: a query's row is scaled by a power of two so that its largest
 // value lies in [2^14, 2^15); what falls below 2^-24 there is 2^-39 of the largest.
-// P s is scaled by 2^(6 - E), E the largest exponent of the group's scales so far:
-// with P <= 2^8 it stays below 2^15.  P s is rounded to f16 once where y is bf16 (its
-// 2^-12 is small beside y's own 2^-9); for fp32 and f16 results a second MFMA adds
+// P s is scaled by 2^(7 - E), E the largest exponent of the group's scales that the wave has
+// met: with P <= 2^8 it stays below 2^15.  While all of those scales lie within 2^NEAR of each
+// other a row's largest P s is at least 1/4 there (its largest P is at least 1), and f16's
+// smallest step no more than 2^-22 of it.  From the first block on that has a scale
+// further below E, or none (a zero), a wave scales each block's P s, and O for their product,
+// by each row's largest one: what a row does not see, or gives no weight, takes no bits from
+// the rest however large it is.  (The checks cost 2%, 59.7 -> 60.7 us for the batch below.  64
+// requests of 4096 tokens 45 us, with a first token of values 2^20 times the others' 57.)
+// P s is rounded to f16 once where y is bf16 (its
+// 2^-11 is small beside y's own 2^-8); for fp32 and f16 results a second MFMA adds
 // what the rounding left, 22 bits together, and the same for fp32 queries (QP and PP:
 // parts of the queries and of P s, PP 3 being two parts for fp32 results).
 //
@@ -56,6 +63,7 @@ namespace {
 
 constexpr int WAVES = 4, ROWS = 16, CUS = 256;
 constexpr int LEAST = 8;       // blocks of a run: two a wave, so that a long sequence alone is in fewer pieces
+constexpr int NEAR = 8;        // scales of a group within 2^NEAR of each other share E
 constexpr float LAZY = 8.0f;   // the reference follows the maximum when it is this far behind
 
 template <int... I, typename F>
@@ -128,6 +136,18 @@ __device__ __forceinline__ float row_dot(float m, float v, const float (&t)[8])
 }
 
 __device__ __forceinline__ float ldexp_f(float x, int e) { return __builtin_amdgcn_ldexpf(x, e); }
+
+// A row's sums in group G of its channels.
+template <int G, int N, typename F>
+__device__ __forceinline__ void for_o(f32x4 (&o)[N], F f)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float v = o[2 * G + i / 4][i % 4];
+        f(v);
+        o[2 * G + i / 4][i % 4] = v;
+    }
+}
 
 // What exponents are taken against: 0 where nothing has been seen, so that the power is
 // 0 there and a NaN stays one.
@@ -539,13 +559,14 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
 
         f32x4 o[TILES];
         float mm[G], ref = -INFINITY, sum = 0.0f;
-        int E[Q];                                   // exponents of the scales' references, in the scales' lanes
+        int E[Q];                                   // largest exponents of the scales (biased), in the scales' lanes
+        bool apart = false;                         // some scale was far below E
 #pragma unroll
         for (int x = 0; x < TILES; ++x) o[x] = 0.0f;
 #pragma unroll
         for (int g = 0; g < G; ++g) mm[g] = 0.0f;
 #pragma unroll
-        for (int x = 0; x < Q; ++x) E[x] = -200;
+        for (int x = 0; x < Q; ++x) E[x] = 0;
 
         Keys<D> k;
         Values<D> v;
@@ -613,6 +634,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                     t[x] = __builtin_amdgcn_exp2f(t[x] - base);
                     sum += t[x];
                 }
+                int skip = 0;                       // words that no row has to do with
                 if (tail) {
                     // Words behind the sequence's end hold anything, and a token may stand for NaN that
                     // some rows do not see: such words count as 0, and the groups of the rows that do
@@ -627,6 +649,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                         bad[x] = nan ? 1.0f : 0.0f;
                         v.s[x] = nan ? 0 : w;
                         any |= nan;
+                        skip |= (nan || b * 32 + (slot >> 2) * 16 + h * 4 + (slot & 3) >= q.keys) << x;
                     }
                     if (__any(any))
                         each<G>([&](auto gc) {
@@ -640,18 +663,21 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                 }
                 float vs[Q], vm[Q];
                 // the references of the values' scales
-                bool above = false;
+                bool out = false;
 #pragma unroll
                 for (int x = 0; x < Q; ++x) {
                     vs[x] = __builtin_bit_cast(float, v.s[x] << 16);
                     vm[x] = __builtin_bit_cast(float, v.s[x] & 0xffff0000u);
-                    above |= vs[x] != 0.0f && __builtin_amdgcn_frexp_expf(vs[x]) > E[x];
+                    const int e = v.s[x] >> 7 & 0xff;
+                    out |= (uint32_t)(E[x] - e) > NEAR && !(skip >> x & 1);
                 }
-                if (__any(above)) {
+                if (__builtin_expect(__any(out), false)) {
+                    bool below = false;
 #pragma unroll
                     for (int x = 0; x < Q; ++x) {
                         // lanes of the same parity hold the same groups
-                        int e = vs[x] != 0.0f ? __builtin_amdgcn_frexp_expf(vs[x]) : -200;
+                        const int mine = v.s[x] >> 7 & 0xff;
+                        int e = mine;
 #pragma unroll
                         for (int dist = 2; dist < 64; dist <<= 1) {
                             const int other = __shfl_xor(e, dist);
@@ -660,6 +686,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                         e = e > E[x] ? e : E[x];
                         const int shift = E[x] - e;
                         E[x] = e;
+                        below |= e - mine > NEAR && !(skip >> x & 1);
 #pragma unroll
                         for (int par = 0; par < 2; ++par) {
                             const int sh = __builtin_amdgcn_readlane(shift, par);
@@ -671,15 +698,36 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                             }
                         }
                     }
+                    apart |= __any(below);
                 }
                 float vn[Q];
 #pragma unroll
-                for (int x = 0; x < Q; ++x) vn[x] = ldexp_f(vs[x], 6 - E[x]);
+                for (int x = 0; x < Q; ++x) vn[x] = ldexp_f(vs[x], apart ? -8 : 133 - E[x]);   // apart: P s < 2^126
                 each<G>([&](auto gc) {
                     constexpr int g = gc.value;
                     mm[g] = row_dot<g / Q>(mm[g], vm[g % Q], t);
                     float w[8];
                     each<8>([&](auto xc) { w[xc.value] = t[xc.value] * row_bcast<xc.value * 2 + g / Q>(vn[g % Q]); });
+                    int back = 0;                   // 2^-back: O's unit to that of these P s, never a larger one
+                    if (__builtin_expect(apart, false)) {
+                        float most = w[0], held_most = 0.0f;
+#pragma unroll
+                        for (int x = 1; x < 8; ++x) most = fmaxf(most, w[x]);
+                        for_o<g>(o, [&](float &v) { held_most = fmaxf(held_most, fabsf(v)); });
+#pragma unroll
+                        for (int dist = 16; dist < 64; dist <<= 1) {
+                            most = fmaxf(most, __shfl_xor(most, dist));
+                            held_most = fmaxf(held_most, __shfl_xor(held_most, dist));
+                        }
+                        const int unit = 141 - __builtin_amdgcn_readlane(E[g % Q], g / Q);
+                        back = most > 0.0f ? unit - 15 + __builtin_amdgcn_frexp_expf(most) : 0;
+                        // O stays below 2^100: what is that far below it adds nothing
+                        const int least = held_most > 0.0f ? __builtin_amdgcn_frexp_expf(held_most) - 100 : back;
+                        back = back > least ? back : least;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) w[x] = ldexp_f(w[x], unit - back);
+                        for_o<g>(o, [&](float &v) { v = ldexp_f(v, -back); });
+                    }
                     const uint32_t p0 = pack_f16(w[0], w[1]), p1 = pack_f16(w[2], w[3]), p2 = pack_f16(w[4], w[5]), p3 = pack_f16(w[6], w[7]);
                     const f16x8 hi = operand(p0, p1, p2, p3);
                     f16x8 lo;
@@ -696,6 +744,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                         o[n] = mfma_f16(vv, hi, o[n]);
                         if constexpr (PP > 1) o[n] = mfma_f16(vv, lo, o[n]);
                     });
+                    if (__builtin_expect(apart, false)) for_o<g>(o, [&](float &v) { v = ldexp_f(v, back); });
                     keep_order();
                 });
             }
@@ -710,13 +759,13 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
             constexpr int g = gc.value;
             mm[g] += __shfl_xor(mm[g], 16);
             mm[g] += __shfl_xor(mm[g], 32);
-            const int e = __builtin_amdgcn_readlane(E[g % Q], g / Q);
+            const int e = __builtin_amdgcn_readlane(E[g % Q], g / Q) - 133;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int n = 2 * g + y;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    o[n][r] = ldexp_f(o[n][r], e + UP_V - 6 - (!FINE_V && n & 1 ? 4 : 0)) + mm[g];
+                    o[n][r] = ldexp_f(o[n][r], e + UP_V - (!FINE_V && n & 1 ? 4 : 0)) + mm[g];
             }
         });
         __syncthreads();                            // the piece before is out of LDS
