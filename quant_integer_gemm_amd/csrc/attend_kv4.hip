@@ -406,6 +406,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
     constexpr int UP_K = FINE_K ? 18 : 24, UP_V = FINE_V ? 18 : 24;   // codes are 2^-UP
     __shared__ float joined[WAVES][ROWS * D];
     __shared__ float stats[WAVES][2][ROWS];
+    __shared__ int beyond[WAVES][64];               // each lane's own (a register more spills: 61 -> 63 us)
     __shared__ uint32_t tmp[4], found[2], arrivals;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, h = lane >> 4;
     const int nseq = (int)j.c.nseq;
@@ -504,7 +505,8 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
         const E *qp = static_cast<const E *>(j.a.q.p) + (int64_t)(q.q0 + qi) * j.a.q.token + (int64_t)qh * j.a.q.head;
         f16x8 qv[QP][G];
         u32x4 qm = {0, 0, 0, 0};                    // the groups' sums in bf16: the first, second, third part in lanes 0.., 16.., 32..
-        float F;
+        float F;                                    // t = F times the codes' sums
+        bool steep;                                 // and times 2^beyond for some row
         {
             float f[G][8], qs[G], top = 0.0f;
 #pragma unroll
@@ -548,7 +550,12 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                 const __bf16 mine = h == 0 ? p0 : h == 1 ? p1 : p2;
                 if (h < 3) qm[g / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, mine) << (16 * (g % 2));
             }
-            F = ldexp_f(j.a.c, UP_K + e);
+            // F alone may lie beyond fp32 where t does not
+            int over = __builtin_amdgcn_frexp_expf(j.a.c) + UP_K + e - 126;
+            over = over > 0 ? over : 0;
+            F = ldexp_f(j.a.c, UP_K + e - over);
+            steep = __any(over > 0);
+            if (steep) beyond[wave][lane] = over;
         }
         // the tokens that this row sees: the first `limit` ones; from token `full` on some
         // row of the tile sees less than all
@@ -603,6 +610,9 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
                     for (int r = 0; r < 4; ++r) t[u * 4 + r] = acc[r] * F;
                     keep_order();
                 });
+                if (__builtin_expect(steep, false))
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) t[x] = ldexp_f(t[x], beyond[wave][lane]);
             }
             // the keys' registers are free: the next block's come while this one's values are used
             if (then) load_keys<D>(then, lane, k);

@@ -160,6 +160,28 @@ def test_scales_up_and_down(ytype, ws):
     ref.check(y, want, allow)
 
 
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("ytype", [F32, F16, BF16])
+@pytest.mark.parametrize("qtype,scale", [(F32, None), (BF16, None), (F32, 1.0), (BF16, 1.0), (F32, 1e30), (F16, 1e30)])
+def test_steep_scores(qtype, scale, ytype, ws):
+    """Queries and scales at the types' upper ends: scores are finite and far apart, one key has all
+    of the weight.  Its score is an eighth above the others' at least, which no rounding of a score
+    (2^-17 of its terms) makes up, so that the values' part of the allowance is all of it."""
+    n, d, at = 300, 64, 77
+    k, v = rows(n, 1, d, F32, 1).cpu().clamp(-2, 0.5), rows(n, 1, d, F32, 2).cpu()
+    k[at] = 2.0
+    q = 1 + rows(1, 4, d, F32, 3).cpu() * 0.001
+    # sum of q k scale at most 64 * 2 * 1.03 * this: below 2^127
+    q *= 2.0 ** (119 if scale == 1.0 else 122 if scale is None else 14) / (1 if scale is None else 1.03)
+    c, ks, vs = written(k, v)
+    q = q.to(qtype)
+    assert ks[at].sum() * 0.9 > ks.sum(2)[torch.arange(n) != at].max() and q.isfinite().all()
+    y = qig.attend_kv4(q.cuda(), c.pages, c.tables, c.lengths, scale=scale, dtype=ytype,
+                       ws=qig.new_workspace("cuda") if ws else None)
+    want, _, values = formula(q.double() / q.double().abs().max() * 1e4, ks, vs, [n - 1], ytype)   # as steep, for exp
+    ref.check(y, want, values)
+
+
 def test_numbers_of_the_oracle():
     """The oracle's softmax against a sum by hand."""
     k, v = torch.zeros((2, 1, 64)), torch.zeros((2, 1, 64))
