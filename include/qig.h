@@ -620,10 +620,11 @@ int read_kv4(void *k, int64_t k_token, int64_t k_head, void *v, int64_t v_token,
  * for, the row at position p seeing the positions up to p.  Tokens without a page
  * are left out; a row that sees nothing gets zeros.  Sums are fp32.  For fp32 q or y the
  * products' operands keep 22 bits; for 16-bit ones a sum of products keeps 17 bits
- * below its largest term, and for bf16 y p_j s_j has 11.  Otherwise a p_j s_j is off by
- * 2^-23 of the row's largest in those 32 channels at most: tokens that a row does not see, or
+ * below its largest term, and for bf16 y p_j s_j has 11.  Besides, a p_j s_j is off by
+ * 2^-23 of the row's largest in those 32 channels at most (tokens that a row does not see, or
  * gives no weight, take nothing from the others, their values up to 2^100 times as
- * large.  y is rounded once.
+ * large), and a q by 2^-23 of the row's largest in those 32 channels, 2^-19 where q
+ * and y have 16 bits.  y is rounded once.
  *   q      [nt][hq][d] elements of type;  y [nt][hq][d] of ytype
  *   scale  as attend_prompt
  *   ws     NULL, or a workspace as for the stream-K calls (the same rules): lets the

@@ -26,7 +26,10 @@
 // Rows: (query, head of the group) pairs of one key head, 16 at a time.
 //
 // Range in f16: a query's row is scaled by a power of two so that its largest
-// value lies in [2^14, 2^15); what falls below 2^-24 there is 2^-39 of the largest.
+// value lies in [2^14, 2^15); what falls below 2^-24 there is 2^-39 of the largest.  Where the
+// largest of some 32 channels is less than 2^-QNEAR of that, each 32 have a power of their own,
+// applied to their sums in a copy of the scores' part (the search for it costs 1.3%, 61.0 ->
+// 61.8 us for the batch below).
 // P s is scaled by 2^(7 - E), E the largest exponent of the group's scales that the wave has
 // met: with P <= 2^8 it stays below 2^15.  While all of those scales lie within 2^NEAR of each
 // other a row's largest P s is at least 1/4 there (its largest P is at least 1), and f16's
@@ -64,6 +67,7 @@ namespace {
 constexpr int WAVES = 4, ROWS = 16, CUS = 256;
 constexpr int LEAST = 8;       // blocks of a run: two a wave, so that a long sequence alone is in fewer pieces
 constexpr int NEAR = 8;        // scales of a group within 2^NEAR of each other share E
+constexpr int QNEAR = 16;      // a query's groups of channels within 2^QNEAR of its largest share a power
 constexpr float LAZY = 8.0f;   // the reference follows the maximum when it is this far behind
 
 template <int... I, typename F>
@@ -407,6 +411,7 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
     __shared__ float joined[WAVES][ROWS * D];
     __shared__ float stats[WAVES][2][ROWS];
     __shared__ int beyond[WAVES][64];               // each lane's own (a register more spills: 61 -> 63 us)
+    __shared__ int16_t apart_q[G][WAVES][64];
     __shared__ uint32_t tmp[4], found[2], arrivals;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 15, h = lane >> 4;
     const int nseq = (int)j.c.nseq;
@@ -507,8 +512,9 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
         u32x4 qm = {0, 0, 0, 0};                    // the groups' sums in bf16: the first, second, third part in lanes 0.., 16.., 32..
         float F;                                    // t = F times the codes' sums
         bool steep;                                 // and times 2^beyond for some row
+        bool uneven;                                // groups of channels have powers of their own, 2^apart_q to the row's
         {
-            float f[G][8], qs[G], top = 0.0f;
+            float f[G][8], qs[G], tops[G], top = 0.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -521,24 +527,39 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                qs[g] = 0.0f;
+                qs[g] = tops[g] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    top = fmaxf(top, fabsf(f[g][i]));
+                    tops[g] = fmaxf(tops[g], fabsf(f[g][i]));
                     qs[g] += f[g][i];
                 }
                 qs[g] += __shfl_xor(qs[g], 16);
                 qs[g] += __shfl_xor(qs[g], 32);
+                tops[g] = fmaxf(tops[g], __shfl_xor(tops[g], 16));
+                tops[g] = fmaxf(tops[g], __shfl_xor(tops[g], 32));
+                top = fmaxf(top, tops[g]);
             }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const int e = top > 0.0f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 15 : 0;
+            const bool plain = top > 0.0f && top < INFINITY;
+            const int e = plain ? __builtin_amdgcn_frexp_expf(top) - 15 : 0;
+            int down[G];
+            bool far = false;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                down[g] = plain && tops[g] > 0.0f ? e + 15 - __builtin_amdgcn_frexp_expf(tops[g]) : 0;
+                far |= down[g] > QNEAR;
+            }
+            uneven = __any(far);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (!uneven) down[g] = 0;
+                else apart_q[g][wave][lane] = (int16_t)-down[g];
+            }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int sh = (!FINE_K && i & 1 ? -4 : 0) - e;
+                    const int sh = (!FINE_K && i & 1 ? -4 : 0) - e + down[g];
                     const float v0 = ldexp_f(f[g][2 * i], sh), v1 = ldexp_f(f[g][2 * i + 1], sh);
                     hi[i] = pack_f16(v0, v1);
                     lo[i] = pack_rest(hi[i], v0, v1);
@@ -587,29 +608,40 @@ __global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
             const uint8_t *then = b + WAVES < b1 ? next_block() : nullptr;
             float t[8];
             if (here) {
-                each<2>([&](auto uc) {
-                    constexpr int u = uc.value;
-                    u32x4 m4 = {0, 0, 0, 0};
+                const auto scores = [&](auto uneven_c) {
+                    constexpr bool UNEVEN = uneven_c.value;
+                    each<2>([&](auto uc) {
+                        constexpr int u = uc.value;
+                        u32x4 m4 = {0, 0, 0, 0};
 #pragma unroll
-                    for (int g = 0; g < G; g += 2) m4[g / 2] = __builtin_amdgcn_perm(k.m[u][g + 1], k.m[u][g], 0x07060302);
-                    f32x4 acc = mfma_bf16_16(m4, qm, f32x4(0.0f));
-                    each<G>([&](auto gc) {
-                        constexpr int g = gc.value, w = u * G + g;
-                        const uint32_t c = k.c[w / 4][w % 4];
-                        const f16x8 kv = operand(codes<0, FINE_K>(c), codes<1, FINE_K>(c), codes<2, FINE_K>(c), codes<3, FINE_K>(c));
-                        f32x4 dot = 0.0f;
-                        dot = mfma_f16(kv, qv[0][g], dot);
-                        if constexpr (QP > 1) dot = mfma_f16(kv, qv[1][g], dot);
-                        const float ks = __builtin_bit_cast(float, k.s[g % Q] << 16);
-                        each<4>([&](auto rc) {
-                            constexpr int r = rc.value, from = (u * 4 + r) * 2 + g / Q;
-                            acc[r] += row_bcast<from>(ks) * dot[r];
+                        for (int g = 0; g < G; g += 2) m4[g / 2] = __builtin_amdgcn_perm(k.m[u][g + 1], k.m[u][g], 0x07060302);
+                        f32x4 acc = mfma_bf16_16(m4, qm, f32x4(0.0f));
+                        each<G>([&](auto gc) {
+                            constexpr int g = gc.value, w = u * G + g;
+                            uint32_t c = k.c[w / 4][w % 4];
+                            if constexpr (UNEVEN) asm("" : "+v"(c));   // else both ways' codes would be formed ahead of the branch
+                            const f16x8 kv = operand(codes<0, FINE_K>(c), codes<1, FINE_K>(c), codes<2, FINE_K>(c), codes<3, FINE_K>(c));
+                            f32x4 dot = 0.0f;
+                            dot = mfma_f16(kv, qv[0][g], dot);
+                            if constexpr (QP > 1) dot = mfma_f16(kv, qv[1][g], dot);
+                            if constexpr (UNEVEN) {
+                                const int up = apart_q[g][wave][lane];
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) dot[r] = ldexp_f(dot[r], up);
+                            }
+                            const float ks = __builtin_bit_cast(float, k.s[g % Q] << 16);
+                            each<4>([&](auto rc) {
+                                constexpr int r = rc.value, from = (u * 4 + r) * 2 + g / Q;
+                                acc[r] += row_bcast<from>(ks) * dot[r];
+                            });
                         });
-                    });
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) t[u * 4 + r] = acc[r] * F;
-                    keep_order();
-                });
+                        for (int r = 0; r < 4; ++r) t[u * 4 + r] = acc[r] * F;
+                        keep_order();
+                    });
+                };
+                if (__builtin_expect(uneven, false)) scores(std::true_type());
+                else scores(std::false_type());
                 if (__builtin_expect(steep, false))
 #pragma unroll
                     for (int x = 0; x < 8; ++x) t[x] = ldexp_f(t[x], beyond[wave][lane]);

@@ -30,7 +30,7 @@ def formula(q, k, v, pos, ytype):
 
     A score is off by what kv4_allowance counts: (d + 3 + d / 16) half steps of fp32 of its
     terms' sizes, 2^-22 of them for queries in two parts (also allowed to the others, which are
-    exact) and 2^-39 of the row's largest |q| a channel; p by that factor, twice (its sum).
+    exact) and 2^-39 of the row's largest |q| of 32 channels in each of them; p by that factor, twice (its sum).
     p s is rounded to f16 once for bf16 results (2^-11), else in two parts (2^-22), and is off
     by no less than 2^-23 of the row's largest p s in the group: half of f16's smallest step,
     2^-25, where the largest is at least 1/4.  Codes are at most 15.  For 16-bit results an
@@ -52,7 +52,8 @@ def formula(q, k, v, pos, ytype):
     top = top.repeat_interleave(32, 2)
     seen_k = torch.where(see[None, :, :, None], k.abs().transpose(0, 1)[:, None], torch.zeros(()).double())
     amax = torch.einsum("ihd,hijd->hij", q.abs(), seen_k).amax(2).T[..., None] * scale
-    amp = (q.abs().amax(2).T[..., None] * seen_k.sum(3).amax(2)[..., None]).transpose(0, 1) * scale
+    most = q.abs().unflatten(2, (G, 32)).amax(3).transpose(0, 1)                         # [hq][n][G]
+    amp = (most[:, :, None] * seen_k.unflatten(3, (G, 32)).sum(4)).sum(3).amax(2).T[..., None] * scale
     score = (d + 3 + d // 16 + 4) * E32 * amax + 2.0 ** -39 * amp
     step = 2.0 ** -11 if ytype == BF16 else 2.0 ** -22
     err = mag * ((3 * nk + 32) * E32 + step) + nk * 15 * 2.0 ** -23 * top
@@ -180,6 +181,30 @@ def test_steep_scores(qtype, scale, ytype, ws):
                        ws=qig.new_workspace("cuda") if ws else None)
     want, _, values = formula(q.double() / q.double().abs().max() * 1e4, ks, vs, [n - 1], ytype)   # as steep, for exp
     ref.check(y, want, values)
+
+
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("ytype", [F32, F16, BF16])
+@pytest.mark.parametrize("qtype,d,ratio", [(F32, 64, 12), (F32, 128, 24), (F32, 256, 60), (BF16, 128, 24), (BF16, 64, 40),
+                                           (BF16, 256, 100), (F16, 128, 20), (F16, 64, 26)])
+def test_queries_of_different_sizes(qtype, d, ratio, ytype, ws):
+    """One group of a query's channels is 2^ratio times the others' and its keys are that much
+    smaller (or zeros): the others' part of the scores keeps its bits."""
+    for n, zeros in ((200, False), (333, True)):
+        k, v = rows(n, 2, d, F32, 1).cpu(), rows(n, 2, d, F32, 2).cpu()
+        q = rows(3, 8, d, F32, 3).cpu()
+        half = ratio // 2 if qtype == F16 else 0       # both ends of fp16
+        q *= 2.0 ** -half
+        k *= 2.0 ** half
+        q[:, :4, 32:64] *= 2.0 ** ratio
+        q[:, 6:, :32] *= 2.0 ** ratio                  # other rows of a tile, another group; two even ones
+        k[:, 0, 32:64] *= 0 if zeros else 2.0 ** -ratio
+        k[:, 1, :32] *= 0 if zeros else 2.0 ** -ratio
+        q = q.to(qtype)
+        c, ks, vs = written(k, v)
+        y = attend(c, q, ints([0, 3]), ytype, ws)
+        want, allow, _ = formula(q, ks, vs, [n - 3, n - 2, n - 1], ytype)
+        ref.check(y, want, allow, f"{n} tokens")
 
 
 def test_numbers_of_the_oracle():
