@@ -549,8 +549,8 @@ int combine_experts(const void *h, int htype, int64_t ldh, const float *w,
  *   scale  0 for 1 / sqrt(d), else above 0 and at most 1e30
  *   y      [nt][hq][d] elements of ytype; rows outside of every sequence are left as
  *          they were; rows must not overlap
- * Errors: QIG_EINVAL (unknown type, nt, nk or nseq < 0 or >= 2^31 - 1, heads, d, a
- *         negative stride, causal not 0 or 1, scale, nt * hq / hkv >= 2^31, or more
+ * Errors: QIG_EINVAL (unknown type, nt, nk or nseq < 0, nt >= 2^31, nseq >= 2^31 - 1, nk > 2^31 -
+ *         1024, heads, d, a negative stride, causal not 0 or 1, scale, nt * hq / hkv >= 2^31, or more
  *         tiles than a launch holds: nt * hq / hkv / 128 + nseq by hkv, at most 2^24),
  *         QIG_EALIGN, QIG_ELAUNCH.
  */

@@ -88,7 +88,8 @@ int attend_prompt(const void *q, int64_t q_token, int64_t q_head, const void *k,
 {
     float c;
     if (bad_type(type) || bad_type(ytype) || bad_heads(hq, hkv) || d < 8 || d > 256 || d % 8 != 0) return QIG_EINVAL;
-    if (nt < 0 || nt >= INT_LIM || nk < 0 || nk >= INT_LIM || nseq < 0 || nseq >= INT_LIM - 1) return QIG_EINVAL;
+    // the kernels count keys in ints, up to 256 at a step and one step ahead
+    if (nt < 0 || nt >= INT_LIM || nk < 0 || nk > INT_LIM - 1024 || nseq < 0 || nseq >= INT_LIM - 1) return QIG_EINVAL;
     if ((causal != 0 && causal != 1) || !exponent(scale, d, c)) return QIG_EINVAL;
     if (bad_strides(q_token, q_head) || bad_strides(k_token, k_head) || bad_strides(v_token, v_head) ||
         bad_strides(y_token, y_head))
