@@ -565,8 +565,9 @@ int attend_prompt(const void *q, int64_t q_token, int64_t q_head, const void *k,
  * group,
  *   m = the largest bf16 <= lo,  s = the smallest bf16 >= (hi - m) / 15,
  *   c = floor((x - m) / s + 1/2) held to 0 .. 15   (0 where s = 0),
- * decided exactly in 64 bits, and the group stands for m + s * c (formed in fp32):
- * no value is off by more than s / 2.  A group with a NaN or an infinity in it, or a
+ * in fp64 arithmetic (hi - m, its 15th part and x - m are each rounded to nearest before s
+ * is rounded up and c decided), and the group stands for m + s * c (formed in fp32): no
+ * value is off by more than s / 2 and the roundings, 2^-51 of it in fp64.  A group with a NaN or an infinity in it, or a
  * value beyond the bf16 range, stands for NaN.
  *
  * A page holds `page` tokens of hkv heads: [hkv][page / 32] blocks of 32 tokens,

@@ -3,9 +3,12 @@
 // 32 values of a row, lo the lowest and hi the highest of them, are kept as
 //   m = the largest bf16 <= lo,  s = the smallest bf16 >= (hi - m) / 15,
 //   c = floor((x - m) / s + 1/2), held to 0 .. 15   (0 where s = 0)
-// and stand for m + s c.  With m rounded down and s up no value lies outside of
-// m .. m + 15 s, so that none is off by more than s / 2.  Both as bf16 are one word
-// for 32 values: 5 bits a value, the codes 4 of them.
+// in fp64 arithmetic: hi - m, its 15th part and x - m are each rounded to nearest (exact
+// while x and m lie within 2^29 of each other) before s is rounded up and the nearest
+// code decided.  They stand for m + s c.  With m rounded down and s up no value lies outside
+// of m .. m + 15 s by more than fp64's roundings, 2^-51 of it, so that none is off by more than
+// s / 2 and that.  Both as bf16 are one word for 32 values: 5 bits a value, the codes 4 of
+// them.
 //
 // A wave has a token and 512 channels, so that a few tokens are many waves; a group's
 // ends are two exchanges among four lanes.  Measured, 4 heads of 128: 2630 tokens from
@@ -96,9 +99,9 @@ __device__ __forceinline__ uint32_t scale_word(float lo, float hi, float &s, flo
     return mb | (sb >> 16);
 }
 
-// The code of x.  d = x - m is exact in 64 bits, and so is the sign of d - (c -+ 1/2) s
-// (one rounding in an fma): c from the product with 1 / s is at most one off and is put
-// right by these.
+// The code of x: of d = x - m as fp64 has it, exactly.  The sign of d - (c -+ 1/2) s is (one
+// rounding in an fma): c from the product with 1 / s is at most one off and is put right by
+// these.
 __device__ __forceinline__ uint32_t code4(float x, double m, double s, double inv)
 {
     const double d = (double)x - m;

@@ -207,6 +207,21 @@ def test_queries_of_different_sizes(qtype, d, ratio, ytype, ws):
         ref.check(y, want, allow, f"{n} tokens")
 
 
+def test_minima_far_below_the_rest():
+    """What fp64 rounds away of hi - m is not there: hi = 15 and lo = -2^-70 have s = 1, a code's
+    border that lies 2^-70 above a value is met by it."""
+    x = torch.zeros((2, 1, 64))
+    x[:, 0, ::32], x[:, 0, 1::32] = torch.tensor([[15.0], [-15.0]]), torch.tensor([[-2.0 ** -70], [2.0 ** -70]])
+    x[:, 0, 2::32], x[:, 0, 3::32] = 2.5, -2.5
+    x[0, 0, 3::32] = 7.0
+    x[1, 0, 2::32] = -12.5
+    codes, s, m = ref.quantize4(x.numpy())
+    assert (s == 1).all() and (m[0] == -2.0 ** -70).all() and (codes[0, 0, :, :4] == [15, 0, 3, 7]).all()
+    c, ks, (vc, vs, vm) = written(x, x)
+    k, v = qig.read_kv4(c.pages, c.tables, c.lengths, 64, ints([0, 2]), 2)
+    assert torch.equal(k.cpu().double(), ks) and torch.equal(v, k)
+
+
 def test_numbers_of_the_oracle():
     """The oracle's softmax against a sum by hand."""
     k, v = torch.zeros((2, 1, 64)), torch.zeros((2, 1, 64))
