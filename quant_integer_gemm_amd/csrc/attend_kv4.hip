@@ -387,9 +387,14 @@ __device__ __forceinline__ void join_rows(const Job &j, uint32_t g, int pieces, 
     }
 }
 
-// Workgroups that a CU holds at once (by their registers); with a workspace there are
-// as many in all, each with its share of the list, so that none waits for another's end.
+// Workgroups a CU with a workspace, each with its share of the list: no more than its
+// registers hold at once, so that none waits for another's end.  (They hold one more for 64
+// channels with fp32 queries and for 256 with 16-bit ones.)
 template <int D, int QP, int PP> constexpr int RESIDENT = D == 256 ? 1 : QP == 2 ? 2 : 3;
+
+// What the registers are to hold: without a workspace 256 requests of 700 tokens, 16 heads on 2
+// of 256, take 31 us with two workgroups a CU and 50 with one.
+template <int D, int QP, int PP> constexpr int HELD = D == 256 && QP == 1 ? 2 : RESIDENT<D, QP, PP>;
 
 // Two codes of a word, at bits 4 b of its halves, as f16 subnormals: code * 2^-18 where
 // FINE, else code * 2^-24, or 2^-20 for odd b.
@@ -401,7 +406,7 @@ __device__ __forceinline__ uint32_t codes(uint32_t w)
 }
 
 template <int T, int D, int QP, int PP>
-__global__ __launch_bounds__(256, (RESIDENT<D, QP, PP>)) void kv4_kernel(Job j)
+__global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
 {
     typedef elem_t<T> E;
     constexpr int G = D / 32, Q = G / 2, TILES = D / 16;
