@@ -541,7 +541,11 @@ int combine_experts(const void *h, int htype, int64_t ldh, const float *w,
  * it sees makes its results NaN or infinite (a value's, those of its channel).
  * fp32 operands are multiplied in fp32.  16-bit operands are multiplied exactly and
  * summed in fp32; p is rounded to their type for the second product.  y is rounded
- * once.
+ * once.  Sums of p v are formed before their division by that of p: values whose sum over
+ * the keys, times 2^8, is beyond fp32 make a result infinite.  A call's results are the same
+ * bits every time; in which order a sequence's sums are formed depends on the call's totals
+ * (rows, heads, keys), so its last bits may differ between two batches.  y must not overlap q,
+ * k or v.
  *
  *   q      [nt][hq][d], k and v [nk][hkv][d], elements of type
  *   d      a multiple of 8 from 8 to 256
@@ -629,10 +633,14 @@ int read_kv4(void *k, int64_t k_token, int64_t k_head, void *v, int64_t v_token,
  *   q      [nt][hq][d] elements of type;  y [nt][hq][d] of ytype
  *   scale  as attend_prompt
  *   ws     NULL, or a workspace as for the stream-K calls (the same rules): lets the
- *          sequences be split over the GPU in equal parts whatever their lengths.
- *          Without it each (sequence, head, 16 rows) is one workgroup's.  y differs in
- *          the order of fp32 sums alone.
- * Also QIG_EINVAL without ws for 2^24 or more of those.
+ *          sequences be split over the GPU in equal parts whatever their lengths, of
+ *          256 tokens at least.  Without it each (sequence, head, 16 rows) is one workgroup's,
+ *          which is faster where all sequences are shorter than a thousand tokens or so.  y
+ *          differs in the order of fp32 sums alone.
+ * What attend_prompt says of sums before their division, last bits and overlap holds here
+ * too.  Also QIG_EINVAL for nt * hq / hkv >= 2^31, without ws for 2^24 or more of those
+ * ((nt * hq / hkv / 16 + nseq) * hkv), and with ws where they, times the width * page / 32 + 1
+ * blocks that the table has room for, reach 2^31.
  */
 int attend_kv4(const void *q, int64_t q_token, int64_t q_head, int type, int64_t nt, int64_t hq, int64_t hkv, int64_t d,
                const void *pages, int64_t npages, int64_t page_stride, int64_t page, const int32_t *tables, int64_t ld,

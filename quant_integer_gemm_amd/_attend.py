@@ -240,7 +240,8 @@ def attend_kv4(q, pages, tables, lengths, starts=None, scale=None, y=None, dtype
     less.  Pages that the table does not have are left out; queries that see
     nothing get zeros.  scale: 1 / sqrt(d) where it is None.  y is of q's type, or of
     ``dtype`` or the given y's.  ws: None, or a workspace (qig.workspace()), which
-    lets long sequences be split over the whole GPU."""
+    lets long sequences be split over the whole GPU; where all are shorter than a
+    thousand tokens or so the call is faster without."""
     if _packed is None:
         _start()
     code = _type(q.dtype, "q")

@@ -49,13 +49,16 @@
 // and the last workgroup to leave a piece of a row there joins them, in the list's order.
 //
 // Measured, 28 query heads on 4 of 128, bf16: 64 requests of up to 16384 tokens (209 MB of
-// cache) 50 us, 4.2 TB/s, where a large copy moves 5.3 and a large sum reads 4.0: the
-// cache's bytes.  (One register copy of a block less, the keys' m on an MFMA and a 32-bit
-// list took it from 111 to 75 us, as many workgroups as the GPU holds to 64, the lengths
-// summed by each wave and one launch to 50.)  One request of 4099 tokens 18 us, 2.6 MB:
-// latency, a chain of the lengths' sum 1.5 us, the sequence 1.1, the blocks 2.2, the waves'
-// join 1.8, the piece's write 1.2, the count 0.8, and the last one's reads and sums.  A
-// launch of its own for the join: 17.7, but 22.7 for 21.4 with 16 x 5 drafted tokens.
+// cache) 52-62 us as cards go, 3.4-4.0 TB/s, where a large copy moves 5.3.  Waves wait half of
+// their cycles for their blocks, and the vector units are busy half of the time: three waves a
+// SIMD with one block each on its way reach neither limit.  (One register copy of a
+// block less, the keys' m on an MFMA and a 32-bit list took it from 111 to 75 us, as many
+// workgroups as the GPU holds to 64, the lengths summed by each wave and one launch to 50, on
+// one card; the checks for scales and queries far apart from 59.7 to 61.8, on another.)  One
+// request of 4099 tokens 19 us, 2.6 MB: latency, a chain of the lengths' sum 1.5 us, the
+// sequence 1.1, the blocks 2.2, the waves' join 1.8, the piece's write 1.2, the count 0.8, and
+// the last one's reads and sums.  A launch of its own for the join: 17.7 for 18.2, but 22.7
+// for 21.4 with 16 x 5 drafted tokens.
 #include <utility>
 
 #include "qig_attend_device.h"
@@ -65,7 +68,11 @@ namespace qig {
 namespace {
 
 constexpr int WAVES = 4, ROWS = 16, CUS = 256;
-constexpr int LEAST = 8;       // blocks of a run: two a wave, so that a long sequence alone is in fewer pieces
+// Blocks of a run: two a wave, so that a long sequence alone is in fewer pieces.  Runs of short
+// sequences' rows are as long, one row behind the other: 64 requests on 4 key heads take 44 us
+// with 30 tokens each, 13 with 100, 27 with 1000 and 26 with 2000, and without a workspace 8,
+// 8, 20 and 33.
+constexpr int LEAST = 8;
 constexpr int NEAR = 8;        // scales of a group within 2^NEAR of each other share E
 constexpr int QNEAR = 16;      // a query's groups of channels within 2^QNEAR of its largest share a power
 constexpr float LAZY = 8.0f;   // the reference follows the maximum when it is this far behind

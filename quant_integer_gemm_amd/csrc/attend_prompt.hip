@@ -94,8 +94,9 @@ __device__ __forceinline__ void poison(f32x16 (&o)[D / 32], const E *vp, int64_t
     for (int x = 0; x < D / 32; ++x) poison_tile<D, E>(o[x], vp, step, k0, nk, 32 * x + n, d, end, h);
 }
 
-// A workgroup's tile in the list of (tile, key head) pairs, the longest first.  Of the
-// first 512 workgroups a CU gets one of the first and one of the second 256: the second
+// A workgroup's tile in the list of (tile, key head) pairs, from the last sequence's last tile
+// on: within a causal sequence the longest come first; across sequences nothing orders
+// them, so that a batch may end on its longest one.  Of the first 512 workgroups a CU gets one of the first and one of the second 256: the second
 // are taken in reverse, so that a CU with a long tile has a short one beside it; later ones
 // go where there is room.  2630 fp32 tokens, 28 heads on 4 of 128 (576 tiles): 507 us in the
 // list's order, 436 so.  Every other 256 in reverse: the same there, but 388 for 367 with
