@@ -30,14 +30,14 @@
 // largest of some 32 channels is less than 2^-QNEAR of that, each 32 have a power of their own,
 // applied to their sums in a copy of the scores' part (the search for it costs 1.3%, 61.0 ->
 // 61.8 us for the batch below).
-// P s is scaled by 2^(7 - E), E the largest exponent of the group's scales that the wave has
-// met: with P <= 2^8 it stays below 2^15.  While all of those scales lie within 2^NEAR of each
-// other a row's largest P s is at least 1/4 there (its largest P is at least 1), and f16's
-// smallest step no more than 2^-22 of it.  From the first block on that has a scale
-// further below E, or none (a zero), a wave scales each block's P s, and O for their product,
+// P s is scaled by 2^(10 - E), scales below 2^E: with P <= 2^LAZY it stays below 2^15.  E is HEAD
+// above the largest exponent in the wave's first block.  While all scales of the group that
+// the wave has met lie in [2^(E - NEAR - 1), 2^E) a row's largest P s is at least 1/4 there (its
+// largest P is at least 1), and f16's smallest step no more than 2^-22 of it.  From the first
+// block on that has a scale outside of that, or none (a zero), a wave scales each block's P s, and O for their product,
 // by each row's largest one: what a row does not see, or gives no weight, takes no bits from
 // the rest however large it is.  (The checks cost 2%, 59.7 -> 60.7 us for the batch below.  64
-// requests of 4096 tokens 45 us, with a first token of values 2^20 times the others' 57.)
+// requests of 4096 tokens 45 us, with a first token of values 2^20 times the others' 59.)
 // P s is rounded to f16 once where y is bf16 (its
 // 2^-11 is small beside y's own 2^-8); for fp32 and f16 results a second MFMA adds
 // what the rounding left, 22 bits together, and the same for fp32 queries (QP and PP:
@@ -73,9 +73,11 @@ constexpr int WAVES = 4, ROWS = 16, CUS = 256;
 // with 30 tokens each, 13 with 100, 27 with 1000 and 26 with 2000, and without a workspace 8,
 // 8, 20 and 33.
 constexpr int LEAST = 8;
-constexpr int NEAR = 8;        // scales of a group within 2^NEAR of each other share E
+constexpr float LAZY = 5.0f;   // the reference follows the maximum when it is this far behind
+constexpr int NEAR = 16 - (int)LAZY;   // scales of a group from 2^(E - NEAR) on share E
+constexpr int HEAD = 3;        // what E is above the first block's largest scale
+constexpr int NONE = -1;       // no block yet
 constexpr int QNEAR = 16;      // a query's groups of channels within 2^QNEAR of its largest share a power
-constexpr float LAZY = 8.0f;   // the reference follows the maximum when it is this far behind
 
 template <int... I, typename F>
 __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f)
@@ -419,6 +421,7 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
     constexpr int G = D / 32, Q = G / 2, TILES = D / 16;
     // fp32 queries (QP 2) or results (PP 3): all bits of the products are kept
     constexpr bool FINE_K = QP == 2 || PP == 3, FINE_V = PP == 3;
+    constexpr int UP_P = 141 - (int)LAZY;   // P <= 2^LAZY, s < 2^(E - 126) and their product scaled by 2^(UP_P - E) < 2^15
     constexpr int UP_K = FINE_K ? 18 : 24, UP_V = FINE_V ? 18 : 24;   // codes are 2^-UP
     __shared__ float joined[WAVES][ROWS * D];
     __shared__ float stats[WAVES][2][ROWS];
@@ -599,14 +602,14 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
 
         f32x4 o[TILES];
         float mm[G], ref = -INFINITY, sum = 0.0f;
-        int E[Q];                                   // largest exponents of the scales (biased), in the scales' lanes
-        bool apart = false;                         // some scale was far below E
+        int E[Q];                                   // what the scales' exponents stay below (biased), in the scales' lanes
+        bool apart = false;                         // some scale was outside of E's window
 #pragma unroll
         for (int x = 0; x < TILES; ++x) o[x] = 0.0f;
 #pragma unroll
         for (int g = 0; g < G; ++g) mm[g] = 0.0f;
 #pragma unroll
-        for (int x = 0; x < Q; ++x) E[x] = 0;
+        for (int x = 0; x < Q; ++x) E[x] = NONE;
 
         Keys<D> k;
         Values<D> v;
@@ -716,7 +719,7 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
                         });
                 }
                 float vs[Q], vm[Q];
-                // the references of the values' scales
+                // scales outside of their window
                 bool out = false;
 #pragma unroll
                 for (int x = 0; x < Q; ++x) {
@@ -731,16 +734,17 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
                     for (int x = 0; x < Q; ++x) {
                         // lanes of the same parity hold the same groups
                         const int mine = v.s[x] >> 7 & 0xff;
-                        int e = mine;
+                        int top = mine;
 #pragma unroll
                         for (int dist = 2; dist < 64; dist <<= 1) {
-                            const int other = __shfl_xor(e, dist);
-                            e = other > e ? other : e;
+                            const int other = __shfl_xor(top, dist);
+                            top = other > top ? other : top;
                         }
-                        e = e > E[x] ? e : E[x];
-                        const int shift = E[x] - e;
-                        E[x] = e;
-                        below |= e - mine > NEAR && !(skip >> x & 1);
+                        const int was = E[x];
+                        if (was < top) E[x] = top + HEAD > NEAR + 1 ? top + HEAD : NEAR + 1;
+                        // words before this block may lie anywhere in a window that has moved
+                        below |= (was != NONE && E[x] != was) || (E[x] - mine > NEAR && !(skip >> x & 1));
+                        const int shift = was - E[x];
 #pragma unroll
                         for (int par = 0; par < 2; ++par) {
                             const int sh = __builtin_amdgcn_readlane(shift, par);
@@ -756,7 +760,7 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
                 }
                 float vn[Q];
 #pragma unroll
-                for (int x = 0; x < Q; ++x) vn[x] = ldexp_f(vs[x], apart ? -8 : 133 - E[x]);   // apart: P s < 2^126
+                for (int x = 0; x < Q; ++x) vn[x] = ldexp_f(vs[x], apart ? -8 : UP_P - E[x]);   // apart: P s < 2^126
                 each<G>([&](auto gc) {
                     constexpr int g = gc.value;
                     mm[g] = row_dot<g / Q>(mm[g], vm[g % Q], t);
@@ -773,7 +777,7 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
                             most = fmaxf(most, __shfl_xor(most, dist));
                             held_most = fmaxf(held_most, __shfl_xor(held_most, dist));
                         }
-                        const int unit = 141 - __builtin_amdgcn_readlane(E[g % Q], g / Q);
+                        const int unit = UP_P + 8 - __builtin_amdgcn_readlane(E[g % Q], g / Q);
                         back = most > 0.0f ? unit - 15 + __builtin_amdgcn_frexp_expf(most) : 0;
                         // O stays below 2^100: what is that far below it adds nothing
                         const int least = held_most > 0.0f ? __builtin_amdgcn_frexp_expf(held_most) - 100 : back;
@@ -813,7 +817,7 @@ __global__ __launch_bounds__(256, (HELD<D, QP, PP>)) void kv4_kernel(Job j)
             constexpr int g = gc.value;
             mm[g] += __shfl_xor(mm[g], 16);
             mm[g] += __shfl_xor(mm[g], 32);
-            const int e = __builtin_amdgcn_readlane(E[g % Q], g / Q) - 133;
+            const int e = __builtin_amdgcn_readlane(E[g % Q], g / Q) - UP_P;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int n = 2 * g + y;

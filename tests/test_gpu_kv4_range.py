@@ -144,6 +144,41 @@ def test_a_small_value_with_the_weight(size, qtype, d, ytype, ws):
 
 
 @pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("ytype", [F32, F16, BF16])
+@pytest.mark.parametrize("qtype,d", [(F32, 64), (BF16, 128), (F16, 128), (BF16, 256)])
+def test_many_small_values_with_the_weight(qtype, d, ytype, ws):
+    """As above, with whole blocks of zeros ahead of the first values."""
+    for n, zeros in ((300, 32), (500, 160), (3000, 129)):
+        k, v = rows(n, 1, d, F32, 1).cpu() * 0.1, rows(n, 1, d, F32, 2).cpu()
+        q = (1 + rows(1, 4, d, F32, 3).cpu() * 0.01).to(qtype)
+        k[:zeros] = 22 * math.log(2) / math.sqrt(d)
+        v[:zeros] = 0.0
+        c, ks, vs = written(k, v)
+        y = attend(c, q, None, ytype, ws)
+        want, allow, _ = formula(q, ks, vs, [n - 1], ytype)
+        ref.check(y, want, allow, f"{zeros} of {n}")
+
+
+@pytest.mark.parametrize("ws", [False, True])
+@pytest.mark.parametrize("ytype", [F32, F16, BF16])
+@pytest.mark.parametrize("qtype,d", [(F32, 64), (BF16, 128), (F16, 128), (BF16, 256)])
+@pytest.mark.parametrize("step", [3, 5, 7, -7])
+def test_scales_in_steps(step, qtype, d, ytype, ws):
+    """Scales that rise by 2^step every 128 tokens (four waves' blocks), or every 32, while the
+    weights fall as much: every token counts alike."""
+    for each in (128, 32):
+        n = 6 * each + 7
+        e = (torch.arange(n) // each) * step
+        k = (-e * math.log(2) / math.sqrt(d))[:, None, None].expand(n, 1, d).contiguous().float()
+        v = rows(n, 1, d, F32, 2).cpu() * torch.exp2(e.double()).float()[:, None, None]
+        c, ks, vs = written(k, v)
+        q = (1 + rows(1, 4, d, F32, 3).cpu() * 0.001).to(qtype)
+        y = attend(c, q, None, ytype, ws)
+        want, allow, _ = formula(q, ks, vs, [n - 1], ytype)
+        check_seen(y, want, allow, ytype, f"{each} tokens a step")
+
+
+@pytest.mark.parametrize("ws", [False, True])
 @pytest.mark.parametrize("ytype", [F32, BF16])
 def test_scales_up_and_down(ytype, ws):
     """Scales that rise and fall by 2^80 along a sequence while the weights do the opposite, so
